@@ -457,6 +457,157 @@ PA_API int pa_paged_attention_prefill_run(const void* q, const void* k_cache, co
                                           size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * pa_paged_attention_decode_window -- pa_paged_attention_decode with a
+ * sliding window and a few first tokens that stay visible.  (No counterpart
+ * on the pages.)
+ *
+ * With n = context_lens[b], the query of sequence b sees token t when t < n
+ * and (window == 0 or t >= n - window or t < num_sinks): the newest `window`
+ * tokens, itself among them, and the first `num_sinks`.  window == 0 is no
+ * window (num_sinks then says nothing); a window of n or more changes
+ * nothing.  Otherwise the result, the layouts, dtypes and limits are those of
+ * pa_paged_attention_decode.  A block with no visible token is not read, nor
+ * is its table entry, which may hold anything (the program may have freed
+ * the block); of a block that is read, masked slots never reach the result,
+ * whatever they hold.  window < 0 or num_sinks < 0: PA_ERR_INVALID_ARG.
+ *
+ * _plan reads context_lens (device) and writes the work list into the
+ * workspace; any number of _run calls may follow it in stream order with the
+ * same sizes, window and num_sinks, over any caches (16-bit and, with
+ * pa_paged_attention_decode_q8_run, 8-bit).  A run uses the lengths the plan
+ * read and ignores context_lens' later contents.  A run whose workspace holds no plan
+ * for its sizes does nothing and sets the status word (pa_check_status
+ * returns PA_ERR_INVALID_ARG).  The workspace
+ * (pa_paged_attention_decode_window_workspace_size bytes, 256-byte aligned)
+ * belongs to one call at a time and needs no initialisation.
+ * num_seqs * num_kv_heads * max_blocks_per_seq must stay below 2^31.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_paged_attention_decode_window_workspace_size(int num_seqs, int num_q_heads,
+                                                           int num_kv_heads, int head_dim,
+                                                           int max_blocks_per_seq, size_t* bytes);
+PA_API int pa_paged_attention_decode_window(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int window, int num_sinks, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, float scale, int dtype,
+    void* out, void* workspace, size_t workspace_bytes, void* stream);
+PA_API int pa_paged_attention_decode_window_plan(const int32_t* context_lens, int window,
+                                                 int num_sinks, int num_seqs, int num_q_heads,
+                                                 int num_kv_heads, int head_dim,
+                                                 int max_blocks_per_seq, void* workspace,
+                                                 size_t workspace_bytes, void* stream);
+PA_API int pa_paged_attention_decode_window_run(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int window, int num_sinks, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, float scale, int dtype,
+    void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_paged_attention_decode_q8 -- pa_paged_attention_decode_window over a
+ * cache held in 8 bits (see pa_kv_append_q8 for its format).  (No counterpart
+ * on the pages.)
+ *
+ *   k_cache, v_cache : e4m3 codes [num_blocks][num_kv_heads][16][head_dim]
+ *   k_scale, v_scale : fp32 [num_blocks][num_kv_heads], positive and finite
+ *   K_t = k_scale[phys][g] * code, likewise V_t
+ *
+ * q and out are PA_F16 or PA_BF16 (PA_F32: PA_ERR_UNSUPPORTED).  Everything
+ * else, the plan and the workspace included, as for
+ * pa_paged_attention_decode_window; window 0 reads the whole context.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_paged_attention_decode_q8(
+    const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+    const float* v_scale, const int32_t* block_tables, const int32_t* context_lens, int window,
+    int num_sinks, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream);
+PA_API int pa_paged_attention_decode_q8_run(
+    const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+    const float* v_scale, const int32_t* block_tables, const int32_t* context_lens, int window,
+    int num_sinks, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_paged_attention_prefill_window -- pa_paged_attention_prefill with a
+ * sliding window and a few first tokens that stay visible.  (No counterpart
+ * on the pages.)
+ *
+ * The query row at position p sees token t when t <= p and (window == 0 or
+ * t > p - window or t < num_sinks).  Arguments, layouts, checks, plan / run
+ * split and workspace (pa_paged_attention_prefill_workspace_size) otherwise
+ * as for pa_paged_attention_prefill; the plan also depends on window and
+ * num_sinks, which the run must repeat.  Blocks that no row of a chunk sees
+ * are not read, nor are their table entries.  window == 0 is
+ * pa_paged_attention_prefill itself.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_paged_attention_prefill_window(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* query_start, int window, int num_sinks,
+    int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream);
+PA_API int pa_paged_attention_prefill_window_plan(
+    const int32_t* context_lens, const int32_t* query_start, int window, int num_sinks,
+    int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, float scale, int dtype, void* workspace, size_t workspace_bytes,
+    void* stream);
+PA_API int pa_paged_attention_prefill_window_run(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* query_start, int window, int num_sinks,
+    int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_kv_append_q8 -- quantise the new tokens' K/V rows into an 8-bit paged
+ * cache.  (No counterpart on the pages.)
+ *
+ * Sequence b's newest T_b = query_start[b + 1] - query_start[b] tokens are
+ * rows query_start[b] .. of k and v ([num_tokens][num_kv_heads][head_dim],
+ * `dtype` f32, f16 or bf16); context_lens[b] counts them.  Token i of them is
+ * at position context_lens[b] - T_b + i, in block position / 16 of the
+ * sequence's table.  Per block, KV head and K / V the cache holds e4m3 codes
+ * and one scale, and a value is code * scale:
+ *   - want = 2^e, e the smallest integer with |x| <= 448 * 2^e for every
+ *     finite new x of the block (clamped to -100 .. 120);
+ *   - a block that begins within the new tokens takes scale = want; one that
+ *     holds older tokens of the sequence takes max(its scale, want), and when
+ *     that is larger than its scale the older tokens' codes are rounded anew
+ *     (to nearest even) from their values;
+ *   - the new codes are x / scale rounded to nearest even; infinities become
+ *     +-448, NaN stays NaN.
+ * Slots behind the last token keep their bits.  Only blocks with a new token
+ * are touched; a block must not be written to by two sequences of one call
+ * (copy-on-write guarantees this).  T_b = 1 everywhere is a decode step.
+ * A sequence with T_b < 0, T_b > context_lens[b], context_lens[b] >
+ * max_blocks_per_seq * 16 or rows outside [0, num_tokens) is skipped and sets
+ * PA_ERR_DEVICE_BOUNDS, as does a block whose table entry is outside
+ * [0, num_blocks).  k, v and the caches must be 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_kv_append_q8(const void* k, const void* v, void* k_cache, void* v_cache,
+                           float* k_scale, float* v_scale, const int32_t* block_tables,
+                           const int32_t* context_lens, const int32_t* query_start, int num_seqs,
+                           int num_tokens, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                           int num_blocks, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_block_dequantize -- whole blocks of an 8-bit cache as values in a cache
+ * of `dtype`.  (No counterpart on the pages.)
+ *
+ * For every pair (src, dst) of src_dst_pairs (int64, device): all 16 rows of
+ * every KV head of k_out[dst] = k_scale[src] * code, rounded to nearest even
+ * into `dtype` (f32, f16 or bf16), likewise v.  k_out / v_out have
+ * num_out_blocks blocks laid out as every cache here, so chunked prefill and
+ * the other 16-bit paths run on them.  Two pairs with one dst race.  A pair
+ * with an id out of range is skipped and sets PA_ERR_DEVICE_BOUNDS.  Tensors
+ * must be 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_block_dequantize(const void* k_cache, const void* v_cache, const float* k_scale,
+                               const float* v_scale, const int64_t* src_dst_pairs, int num_pairs,
+                               int num_kv_heads, int head_dim, int num_blocks, int num_out_blocks,
+                               int dtype, void* k_out, void* v_out, void* stream);
+
+/* ------------------------------------------------------------------------
  * pa_paged_attention_decode_noalloc -- pa_paged_attention_decode without a
  * caller-provided workspace.  (No counterpart on the pages: this entry point
  * exists for callers, not for the method.)

@@ -15,6 +15,12 @@ Device entry points (hand-written sm_103a kernels behind the C ABI in
   sequence's newest tokens attend causally over the paged cache
   (:func:`prefill_plan` + :func:`paged_attention_prefill_run` split it so one
   plan serves every layer);
+* :func:`paged_attention_decode_window`, :func:`paged_attention_prefill_window`
+  -- the two with a sliding window and a few first tokens that stay visible;
+* :func:`kv_append_q8`, :func:`paged_attention_decode_q8`,
+  :func:`block_dequantize` -- a cache held in 8 bits (e4m3 codes, a
+  power-of-two scale per block and head): quantising append, decode (windowed
+  or not), whole blocks read back as 16- or 32-bit values;
 * :func:`block_copy` -- copy-on-write block copies across all layers;
 * :func:`block_swap` -- whole blocks between the device caches and
   page-locked host caches (preemption / offload), all layers in one launch;
@@ -40,7 +46,14 @@ from .ops import (LayerCaches, Prepared, alloc_prefill_workspace, alloc_workspac
                   shared_prefix_workspace_size, prefill_workspace_size,
                   paged_attention_decode_plan, paged_attention_decode_run,
                   prepare_decode_append_run, prepare_decode_plan, prepare_decode_run,
-                  paged_attention_decode_noalloc, prepare_kv_append, workspace_size)
+                  paged_attention_decode_noalloc, prepare_kv_append, workspace_size,
+                  alloc_window_workspace, paged_attention_decode_window,
+                  paged_attention_decode_window_plan, paged_attention_decode_window_run,
+                  paged_attention_decode_window_workspace_size, prepare_decode_window_run,
+                  paged_attention_decode_q8, paged_attention_decode_q8_run, prepare_decode_q8_run,
+                  paged_attention_prefill_window, paged_attention_prefill_window_plan,
+                  paged_attention_prefill_window_run, kv_append_q8, prepare_kv_append_q8,
+                  block_dequantize, prepare_block_dequantize)
 from .pool import BlockPool  # noqa: F401
 
 # the C entry points' own names for the calls above whose Python name is shorter

@@ -101,6 +101,24 @@ SIGNATURES = {
                                             _i, C.c_float, _i, _vp, _vp, _sz, _vp]),
     "pa_paged_attention_decode_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
                                                C.c_float, _i, _vp, _vp]),
+    "pa_paged_attention_decode_window_workspace_size": (_i, [_i, _i, _i, _i, _i, C.POINTER(_sz)]),
+    "pa_paged_attention_decode_window": (_i, [_vp] * 5 + [_i] * 8 + [C.c_float, _i, _vp, _vp, _sz,
+                                                                     _vp]),
+    "pa_paged_attention_decode_window_plan": (_i, [_vp] + [_i] * 7 + [_vp, _sz, _vp]),
+    "pa_paged_attention_decode_window_run": (_i, [_vp] * 5 + [_i] * 8 + [C.c_float, _i, _vp, _vp,
+                                                                         _sz, _vp]),
+    "pa_paged_attention_decode_q8": (_i, [_vp] * 7 + [_i] * 8 + [C.c_float, _i, _vp, _vp, _sz,
+                                                                 _vp]),
+    "pa_paged_attention_decode_q8_run": (_i, [_vp] * 7 + [_i] * 8 + [C.c_float, _i, _vp, _vp, _sz,
+                                                                     _vp]),
+    "pa_paged_attention_prefill_window": (_i, [_vp] * 6 + [_i] * 9 + [C.c_float, _i, _vp, _vp,
+                                                                      _sz, _vp]),
+    "pa_paged_attention_prefill_window_plan": (_i, [_vp] * 2 + [_i] * 8 + [C.c_float, _i, _vp,
+                                                                           _sz, _vp]),
+    "pa_paged_attention_prefill_window_run": (_i, [_vp] * 6 + [_i] * 9 + [C.c_float, _i, _vp,
+                                                                          _vp, _sz, _vp]),
+    "pa_kv_append_q8": (_i, [_vp] * 9 + [_i] * 7 + [_vp]),
+    "pa_block_dequantize": (_i, [_vp] * 5 + [_i] * 6 + [_vp, _vp, _vp]),
     "pa_block_copy": (_i, [C.POINTER(_vp), C.POINTER(_vp), _i, _vp, _i, _i, _i, _i, _i, _vp]),
     "pa_block_swap": (_i, [C.POINTER(_vp), C.POINTER(_vp), C.POINTER(_vp), C.POINTER(_vp), _i,
                            _vp, _i, _i, _i, _i, _i, _i, _i, _vp]),

@@ -113,6 +113,9 @@ struct Params {
   // tcgen05 kernel: whole warps of output rows go out through the tensor
   // map of out (tensor-copy stores from shared memory), else thread by thread
   int out_tma;
+  // Sliding window (window > 0): the row at position p sees token t <= p when
+  // t > p - window or t < num_sinks.
+  int window, num_sinks;
   float scale, scale_log2;
   int* header;
   int4* units;       // 2 x int4 per unit (see plan)
@@ -1607,9 +1610,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // --------------------------------------------------------------- fp32 path
-// One warp per (query row, query head): a decode over the row's causal prefix.
-template <int D>
-__global__ void __launch_bounds__(128) prefill_f32_kernel(const Params p) {
+// One warp per (query row, query head): a decode over the tokens the row sees.
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void narrow(float& y, float x) { y = x; }
+__device__ __forceinline__ void narrow(__half& y, float x) { y = __float2half_rn(x); }
+__device__ __forceinline__ void narrow(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(128) prefill_simple_kernel(const Params p) {
   constexpr int E = D / 32;
   const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -1633,18 +1643,21 @@ __global__ void __launch_bounds__(128) prefill_f32_kernel(const Params p) {
   }
   const int pos = ctx - qlen + (row - p.query_start[b]);
   const int g = h / p.group;
-  const float* qv = static_cast<const float*>(p.q) + (size_t(row) * p.num_q_heads + h) * D + lane * E;
-  const float* k_cache = static_cast<const float*>(p.k_cache);
-  const float* v_cache = static_cast<const float*>(p.v_cache);
+  const T* qv = static_cast<const T*>(p.q) + (size_t(row) * p.num_q_heads + h) * D + lane * E;
+  const T* k_cache = static_cast<const T*>(p.k_cache);
+  const T* v_cache = static_cast<const T*>(p.v_cache);
   const int32_t* table = p.block_tables + size_t(b) * p.max_blocks;
   float qr[E], acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    qr[e] = qv[e];
+    qr[e] = widen(qv[e]);
     acc[e] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
-  for (int t = 0; t <= pos; ++t) {
+  const int low = p.window ? max(0, pos - p.window + 1) : 0;  // the window's first token
+  const int sinks = min(p.num_sinks, low);                    // visible before it
+  for (int i = 0; i < sinks + pos - low + 1; ++i) {
+    const int t = i < sinks ? i : low + i - sinks;
     int phys = table[t / kBlockSize];
     if (phys < 0 || phys >= p.num_blocks) {
       if (lane == 0) dev::flag_status(p.status, kStatusBounds);
@@ -1653,7 +1666,7 @@ __global__ void __launch_bounds__(128) prefill_f32_kernel(const Params p) {
     const size_t r = ((size_t(phys) * p.num_kv_heads + g) * kBlockSize + t % kBlockSize) * D + lane * E;
     float dot = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) dot = fmaf(qr[e], k_cache[r + e], dot);
+    for (int e = 0; e < E; ++e) dot = fmaf(qr[e], widen(k_cache[r + e]), dot);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     const float sc = dot * p.scale;
@@ -1661,12 +1674,12 @@ __global__ void __launch_bounds__(128) prefill_f32_kernel(const Params p) {
     const float a = expf(m - mn), pw = expf(sc - mn);
     l = l * a + pw;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + pw * v_cache[r + e];
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + pw * widen(v_cache[r + e]);
     m = mn;
   }
-  float* out = static_cast<float*>(p.out) + (size_t(row) * p.num_q_heads + h) * D + lane * E;
+  T* out = static_cast<T*>(p.out) + (size_t(row) * p.num_q_heads + h) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = acc[e] / l;
+  for (int e = 0; e < E; ++e) narrow(out[e], acc[e] / l);
 }
 
 }  // namespace prefill
@@ -1809,7 +1822,7 @@ enum class Mode { kPlanAndRun, kPlanOnly, kRunOnly };
 // Validation, then the plan and / or the attention kernel.  The plan reads
 // only context_lens and query_start (and the sizes); q, the caches, the
 // tables and out may be NULL for Mode::kPlanOnly.
-int prefill_entry(Mode mode, const void* q, const void* k_cache, const void* v_cache,
+int prefill_entry(Mode mode, int window, int num_sinks, const void* q, const void* k_cache, const void* v_cache,
                   const int32_t* block_tables, const int32_t* context_lens,
                   const int32_t* query_start, int num_seqs, int total_q, int num_q_heads,
                   int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks,
@@ -1818,6 +1831,8 @@ int prefill_entry(Mode mode, const void* q, const void* k_cache, const void* v_c
   int rc = check_shapes(num_seqs, total_q, num_q_heads, num_kv_heads, head_dim,
                         max_blocks_per_seq, dtype, who);
   if (rc != PA_OK) return rc;
+  if (window < 0 || num_sinks < 0)
+    return fail(PA_ERR_INVALID_ARG, "%s: window and num_sinks must not be negative", who);
   if (num_seqs == 0 || total_q == 0) return PA_OK;
   const bool runs = mode != Mode::kPlanOnly;
   if (!context_lens || !query_start)
@@ -1860,20 +1875,26 @@ int prefill_entry(Mode mode, const void* q, const void* k_cache, const void* v_c
   prm.head_dim = head_dim;
   prm.max_blocks = max_blocks_per_seq;
   prm.num_blocks = num_blocks;
+  prm.window = window;
+  prm.num_sinks = num_sinks;
   prm.scale = scale;
   prm.scale_log2 = scale * 1.4426950408889634f;
   prm.status = status;
   prm.timeout_ns = 1000000000ull;
 
-  if (dtype == PA_F32) {
+  if (dtype == PA_F32 || window > 0) {
     // one warp per (row, head) needs no plan
     if (!runs) return PA_OK;
     const long long units = (long long)total_q * num_q_heads;
     const int blocks = int((units + 3) / 4);
-    if (head_dim == 64)
-      prefill_f32_kernel<64><<<blocks, 128, 0, s>>>(prm);
+    auto launch = [&](auto* kernel) { kernel<<<blocks, 128, 0, s>>>(prm); };
+    if (dtype == PA_F32)
+      launch(head_dim == 64 ? prefill_simple_kernel<float, 64> : prefill_simple_kernel<float, 128>);
+    else if (dtype == PA_F16)
+      launch(head_dim == 64 ? prefill_simple_kernel<__half, 64> : prefill_simple_kernel<__half, 128>);
     else
-      prefill_f32_kernel<128><<<blocks, 128, 0, s>>>(prm);
+      launch(head_dim == 64 ? prefill_simple_kernel<__nv_bfloat16, 64>
+                            : prefill_simple_kernel<__nv_bfloat16, 128>);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s (fp32): launch failed: %s", who, cudaGetErrorString(e));
     return PA_OK;
@@ -1900,7 +1921,7 @@ PA_API int pa_paged_attention_prefill(const void* q, const void* k_cache, const 
                                       int dtype, void* out, void* workspace,
                                       size_t workspace_bytes, void* stream) {
   PA_TRACE("pa_paged_attention_prefill");
-  return pa::prefill::prefill_entry(pa::prefill::Mode::kPlanAndRun, q, k_cache, v_cache,
+  return pa::prefill::prefill_entry(pa::prefill::Mode::kPlanAndRun, 0, 0, q, k_cache, v_cache,
                                     block_tables, context_lens, query_start, num_seqs, total_q,
                                     num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
                                     num_blocks, scale, dtype, out, workspace, workspace_bytes,
@@ -1914,7 +1935,7 @@ PA_API int pa_paged_attention_prefill_plan(const int32_t* context_lens,
                                            int dtype, void* workspace, size_t workspace_bytes,
                                            void* stream) {
   PA_TRACE("pa_paged_attention_prefill_plan");
-  return pa::prefill::prefill_entry(pa::prefill::Mode::kPlanOnly, nullptr, nullptr, nullptr,
+  return pa::prefill::prefill_entry(pa::prefill::Mode::kPlanOnly, 0, 0, nullptr, nullptr, nullptr,
                                     nullptr, context_lens, query_start, num_seqs, total_q,
                                     num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, 0,
                                     scale, dtype, nullptr, workspace, workspace_bytes, stream,
@@ -1929,11 +1950,52 @@ PA_API int pa_paged_attention_prefill_run(const void* q, const void* k_cache, co
                                           int dtype, void* out, void* workspace,
                                           size_t workspace_bytes, void* stream) {
   PA_TRACE("pa_paged_attention_prefill_run");
-  return pa::prefill::prefill_entry(pa::prefill::Mode::kRunOnly, q, k_cache, v_cache,
+  return pa::prefill::prefill_entry(pa::prefill::Mode::kRunOnly, 0, 0, q, k_cache, v_cache,
                                     block_tables, context_lens, query_start, num_seqs, total_q,
                                     num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
                                     num_blocks, scale, dtype, out, workspace, workspace_bytes,
                                     stream, "paged_attention_prefill_run");
+}
+
+PA_API int pa_paged_attention_prefill_window(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* query_start, int window, int num_sinks,
+    int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  PA_TRACE("pa_paged_attention_prefill_window");
+  return pa::prefill::prefill_entry(pa::prefill::Mode::kPlanAndRun, window, num_sinks, q, k_cache,
+                                    v_cache, block_tables, context_lens, query_start, num_seqs,
+                                    total_q, num_q_heads, num_kv_heads, head_dim,
+                                    max_blocks_per_seq, num_blocks, scale, dtype, out, workspace,
+                                    workspace_bytes, stream, "paged_attention_prefill_window");
+}
+
+PA_API int pa_paged_attention_prefill_window_plan(
+    const int32_t* context_lens, const int32_t* query_start, int window, int num_sinks,
+    int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, float scale, int dtype, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  PA_TRACE("pa_paged_attention_prefill_window_plan");
+  return pa::prefill::prefill_entry(pa::prefill::Mode::kPlanOnly, window, num_sinks, nullptr,
+                                    nullptr, nullptr, nullptr, context_lens, query_start, num_seqs,
+                                    total_q, num_q_heads, num_kv_heads, head_dim,
+                                    max_blocks_per_seq, 0, scale, dtype, nullptr, workspace,
+                                    workspace_bytes, stream, "paged_attention_prefill_window_plan");
+}
+
+PA_API int pa_paged_attention_prefill_window_run(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, const int32_t* query_start, int window, int num_sinks,
+    int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  PA_TRACE("pa_paged_attention_prefill_window_run");
+  return pa::prefill::prefill_entry(pa::prefill::Mode::kRunOnly, window, num_sinks, q, k_cache,
+                                    v_cache, block_tables, context_lens, query_start, num_seqs,
+                                    total_q, num_q_heads, num_kv_heads, head_dim,
+                                    max_blocks_per_seq, num_blocks, scale, dtype, out, workspace,
+                                    workspace_bytes, stream, "paged_attention_prefill_window_run");
 }
 
 }  // extern "C"

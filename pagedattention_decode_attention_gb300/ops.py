@@ -73,9 +73,10 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         slot_mapping.data_ptr(), k.shape[0], hkv, d, nb, _dtype_code(k), _stream(dev, stream)))
 
 
-def _decode_args(q, k_cache, v_cache, block_tables, context_lens):
+def _decode_args(q, k_cache, v_cache, block_tables, context_lens, rows_are_seqs=True):
     """Checks the decode operands (context_lens None: not passed) and returns
-    (device, num_seqs, Hq, Hkv, d, num_blocks, max_blocks_per_seq)."""
+    (device, num_seqs, Hq, Hkv, d, num_blocks, max_blocks_per_seq);
+    rows_are_seqs False: q has any number of rows, not one per sequence."""
     dev = q.device
     for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
                     ("block_tables", block_tables), ("context_lens", context_lens)):
@@ -90,7 +91,7 @@ def _decode_args(q, k_cache, v_cache, block_tables, context_lens):
     nb, hkv, _, d = k_cache.shape
     _require(q.dim() == 3 and q.shape[2] == d, "q must be [num_seqs, num_q_heads, head_dim]")
     b, hq, _ = q.shape
-    _require(block_tables.dim() == 2 and block_tables.shape[0] == b,
+    _require(block_tables.dim() == 2 and (not rows_are_seqs or block_tables.shape[0] == b),
              "block_tables must be [num_seqs, max_blocks_per_seq]")
     _require(context_lens is None or context_lens.shape == (b,), "context_lens must be [num_seqs]")
     return dev, b, hq, hkv, d, nb, block_tables.shape[1]
@@ -208,11 +209,16 @@ class Prepared:
     The bound tensors are kept alive by this object.
     """
 
-    def __init__(self, fn, args, keep):
+    def __init__(self, fn, args, keep, device=None):
         self._fn, self._args, self._keep = fn, args, keep
+        self._device = device       # made current for the call (None: the caller's business)
 
     def __call__(self) -> None:
-        status = self._fn(*self._args)
+        if self._device is not None and torch.cuda.current_device() != self._device.index:
+            with torch.cuda.device(self._device):
+                status = self._fn(*self._args)
+        else:
+            status = self._fn(*self._args)
         if status:
             capi.check(status)
 
@@ -559,6 +565,332 @@ def paged_attention_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream(dev, stream)))
     return out
+
+
+def _call(dev, name: str, *args) -> None:
+    """The C entry point ``name`` with ``dev`` current."""
+    fn = getattr(capi.lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    capi.check(status)
+
+
+def paged_attention_decode_window_workspace_size(num_seqs: int, num_q_heads: int,
+                                                 num_kv_heads: int, head_dim: int,
+                                                 max_blocks_per_seq: int) -> int:
+    n = C.c_size_t(0)
+    capi.check(capi.lib().pa_paged_attention_decode_window_workspace_size(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, C.byref(n)))
+    return n.value
+
+
+def alloc_window_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                           device) -> torch.Tensor:
+    n = paged_attention_decode_window_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                     head_dim, max_blocks_per_seq)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def paged_attention_decode_window_plan(context_lens: torch.Tensor, window: int, num_sinks: int,
+                                       num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                       max_blocks_per_seq: int, workspace: torch.Tensor,
+                                       stream=None) -> None:
+    """The work list of a windowed (or 8-bit) decode step, into ``workspace``:
+    one plan serves every :func:`paged_attention_decode_window_run` and
+    :func:`paged_attention_decode_q8_run` of the step."""
+    dev = context_lens.device
+    _cuda_contig("context_lens", context_lens, dev)
+    _cuda_contig("workspace", workspace, dev)
+    _require(context_lens.dtype == torch.int32 and context_lens.dim() == 1,
+             "context_lens must be int32 [num_seqs]")
+    _call(dev, "pa_paged_attention_decode_window_plan", context_lens.data_ptr(), int(window),
+          int(num_sinks), context_lens.shape[0], int(num_q_heads), int(num_kv_heads),
+          int(head_dim), int(max_blocks_per_seq), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _stream(dev, stream))
+
+
+def _q8_cache_args(k_cache, v_cache, k_scale, v_scale, dev):
+    """Checks an 8-bit cache's four tensors; (num_blocks, Hkv, head_dim)."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
+                    ("v_scale", v_scale)):
+        _cuda_contig(name, t, dev)
+    _require(k_cache.dtype == v_cache.dtype == torch.float8_e4m3fn, "caches must be float8_e4m3fn")
+    _require(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[2] == 16,
+             "caches must be [num_blocks, num_kv_heads, 16, head_dim]")
+    nb, hkv, _, d = k_cache.shape
+    _require(k_scale.dtype == v_scale.dtype == torch.float32
+             and k_scale.shape == v_scale.shape == (nb, hkv),
+             "scales must be float32 [num_blocks, num_kv_heads]")
+    return nb, hkv, d
+
+
+def _window_args(q, k_cache, v_cache, scales, block_tables, context_lens, window, num_sinks, scale,
+                 workspace, out, stream):
+    """Checks a windowed decode's operands (scales None: a cache of q's dtype);
+    returns (device, C arguments, out, tensors to keep)."""
+    dev = q.device
+    if scales is None:
+        dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, context_lens)
+    else:
+        for name, t in (("q", q), ("block_tables", block_tables), ("context_lens", context_lens)):
+            _cuda_contig(name, t, dev)
+        nb, hkv, d = _q8_cache_args(k_cache, v_cache, *scales, dev)
+        _require(q.dtype in (torch.float16, torch.bfloat16), "q must be float16 or bfloat16")
+        _require(q.dim() == 3 and q.shape[2] == d, "q must be [num_seqs, num_q_heads, head_dim]")
+        b, hq, _ = q.shape
+        _require(block_tables.dtype == torch.int32 and block_tables.dim() == 2
+                 and block_tables.shape[0] == b,
+                 "block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+        _require(context_lens.dtype == torch.int32 and context_lens.shape == (b,),
+                 "context_lens must be int32 [num_seqs]")
+        mb = block_tables.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    _cuda_contig("out", out, dev)
+    _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    if workspace is None:
+        workspace = alloc_window_workspace(b, hq, hkv, d, mb, dev)
+    _cuda_contig("workspace", workspace, dev)
+    ptrs = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()]
+    ptrs += [] if scales is None else [t.data_ptr() for t in scales]
+    ptrs += [block_tables.data_ptr(), context_lens.data_ptr()]
+    args = ([C.c_void_p(p) for p in ptrs]
+            + [int(window), int(num_sinks), b, hq, hkv, d, mb, nb, C.c_float(scale),
+               _dtype_code(q), C.c_void_p(out.data_ptr()), C.c_void_p(workspace.data_ptr()),
+               C.c_size_t(workspace.numel() * workspace.element_size()),
+               C.c_void_p(_stream(dev, stream))])
+    return dev, args, out, (q, k_cache, v_cache, scales, block_tables, context_lens, workspace, out)
+
+
+def paged_attention_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                  window: int, num_sinks: int, scale: float,
+                                  out: torch.Tensor | None = None,
+                                  workspace: torch.Tensor | None = None,
+                                  stream=None) -> torch.Tensor:
+    """:func:`paged_attention_decode` whose queries see only the newest
+    ``window`` tokens (0: all) and the first ``num_sinks``.  Blocks with no
+    visible token are not read, nor are their table entries, so they may have
+    been freed.  Plans and runs in one call."""
+    dev, args, out, _ = _window_args(q, k_cache, v_cache, None, block_tables, context_lens, window,
+                                     num_sinks, scale, workspace, out, stream)
+    _call(dev, "pa_paged_attention_decode_window", *args)
+    return out
+
+
+def paged_attention_decode_window_run(q, k_cache, v_cache, block_tables, context_lens, window: int,
+                                      num_sinks: int, scale: float, workspace: torch.Tensor,
+                                      out=None, stream=None) -> torch.Tensor:
+    """:func:`paged_attention_decode_window` over a workspace that
+    :func:`paged_attention_decode_window_plan` filled for the same lengths,
+    window and first tokens."""
+    dev, args, out, _ = _window_args(q, k_cache, v_cache, None, block_tables, context_lens, window,
+                                     num_sinks, scale, workspace, out, stream)
+    _call(dev, "pa_paged_attention_decode_window_run", *args)
+    return out
+
+
+def prepare_decode_window_run(q, k_cache, v_cache, block_tables, context_lens, window: int,
+                              num_sinks: int, scale: float, workspace, out,
+                              stream=None) -> Prepared:
+    dev, args, _, keep = _window_args(q, k_cache, v_cache, None, block_tables, context_lens,
+                                      window, num_sinks, scale, workspace, out, stream)
+    return Prepared(capi.lib().pa_paged_attention_decode_window_run, args, keep, dev)
+
+
+def paged_attention_decode_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              k_scale: torch.Tensor, v_scale: torch.Tensor,
+                              block_tables: torch.Tensor, context_lens: torch.Tensor, window: int,
+                              num_sinks: int, scale: float, out: torch.Tensor | None = None,
+                              workspace: torch.Tensor | None = None,
+                              stream=None) -> torch.Tensor:
+    """:func:`paged_attention_decode_window` over a cache held in 8 bits:
+    ``k_cache`` / ``v_cache`` are float8_e4m3fn codes, ``k_scale`` / ``v_scale``
+    (float32 ``[num_blocks, num_kv_heads]``) what a code of each block and head
+    is multiplied by (:func:`kv_append_q8` writes both); ``window`` 0 sees the
+    whole context.  ``q`` is float16 or bfloat16."""
+    dev, args, out, _ = _window_args(q, k_cache, v_cache, (k_scale, v_scale), block_tables,
+                                     context_lens, window, num_sinks, scale, workspace, out, stream)
+    _call(dev, "pa_paged_attention_decode_q8", *args)
+    return out
+
+
+def paged_attention_decode_q8_run(q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                  context_lens, window: int, num_sinks: int, scale: float,
+                                  workspace: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """:func:`paged_attention_decode_q8` over a workspace that
+    :func:`paged_attention_decode_window_plan` filled for the same lengths,
+    window and first tokens."""
+    dev, args, out, _ = _window_args(q, k_cache, v_cache, (k_scale, v_scale), block_tables,
+                                     context_lens, window, num_sinks, scale, workspace, out, stream)
+    _call(dev, "pa_paged_attention_decode_q8_run", *args)
+    return out
+
+
+def prepare_decode_q8_run(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                          window: int, num_sinks: int, scale: float, workspace, out,
+                          stream=None) -> Prepared:
+    dev, args, _, keep = _window_args(q, k_cache, v_cache, (k_scale, v_scale), block_tables,
+                                      context_lens, window, num_sinks, scale, workspace, out,
+                                      stream)
+    return Prepared(capi.lib().pa_paged_attention_decode_q8_run, args, keep, dev)
+
+
+def paged_attention_prefill_window_plan(context_lens: torch.Tensor, query_start: torch.Tensor,
+                                        total_q: int, window: int, num_sinks: int,
+                                        num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                        max_blocks_per_seq: int, scale: float, dtype: torch.dtype,
+                                        workspace: torch.Tensor, stream=None) -> None:
+    """The work list of a windowed chunked-prefill batch, into ``workspace``:
+    one plan serves every :func:`paged_attention_prefill_window_run` over the
+    same chunks, window and first tokens."""
+    dev = context_lens.device
+    for name, t in (("context_lens", context_lens), ("query_start", query_start),
+                    ("workspace", workspace)):
+        _cuda_contig(name, t, dev)
+    _require(context_lens.dtype == torch.int32 and context_lens.dim() == 1
+             and query_start.dtype == torch.int32, "context_lens and query_start must be int32")
+    b = context_lens.shape[0]
+    _require(query_start.shape == (b + 1,), "query_start must be [num_seqs + 1]")
+    _require(dtype in _DTYPES, "dtype must be float32, float16 or bfloat16")
+    _call(dev, "pa_paged_attention_prefill_window_plan", context_lens.data_ptr(),
+          query_start.data_ptr(), int(window), int(num_sinks), b, int(total_q), int(num_q_heads),
+          int(num_kv_heads), int(head_dim), int(max_blocks_per_seq), float(scale), _DTYPES[dtype],
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _stream(dev, stream))
+
+
+def paged_attention_prefill_window_run(q, k_cache, v_cache, block_tables, context_lens,
+                                       query_start, window: int, num_sinks: int, scale: float,
+                                       workspace: torch.Tensor, out=None,
+                                       stream=None) -> torch.Tensor:
+    """:func:`paged_attention_prefill_window` over a workspace that
+    :func:`paged_attention_prefill_window_plan` filled for the same chunks,
+    window and first tokens: the attention kernel only."""
+    return paged_attention_prefill_window(q, k_cache, v_cache, block_tables, context_lens,
+                                          query_start, window, num_sinks, scale, out=out,
+                                          workspace=workspace, stream=stream,
+                                          _entry="pa_paged_attention_prefill_window_run")
+
+
+def paged_attention_prefill_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                   query_start: torch.Tensor, window: int, num_sinks: int,
+                                   scale: float, out: torch.Tensor | None = None,
+                                   workspace: torch.Tensor | None = None, stream=None,
+                                   _entry: str = "pa_paged_attention_prefill_window"
+                                   ) -> torch.Tensor:
+    """:func:`paged_attention_prefill` whose rows see only the newest
+    ``window`` tokens up to themselves (0: all) and the first ``num_sinks``.
+    Blocks that no row sees are not read, nor are their table entries."""
+    dev = q.device
+    _, _, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, None,
+                                            rows_are_seqs=False)
+    for name, t in (("context_lens", context_lens), ("query_start", query_start)):
+        _cuda_contig(name, t, dev)
+    b = block_tables.shape[0]
+    _require(context_lens.dtype == torch.int32 and context_lens.shape == (b,),
+             "context_lens must be int32 [num_seqs]")
+    _require(query_start.dtype == torch.int32 and query_start.shape == (b + 1,),
+             "query_start must be int32 [num_seqs + 1]")
+    if out is None:
+        out = torch.empty_like(q)
+    _cuda_contig("out", out, dev)
+    _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    if workspace is None:
+        workspace = alloc_prefill_workspace(b, q.shape[0], hq, hkv, d, dev)
+    _cuda_contig("workspace", workspace, dev)
+    _call(dev, _entry, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), int(window),
+          int(num_sinks), b, q.shape[0], hq, hkv, d, mb, nb, float(scale), _dtype_code(q),
+          out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _stream(dev, stream))
+    return out
+
+
+def _append_q8_args(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                    query_start, stream):
+    dev = k_cache.device
+    for name, t in (("k", k), ("v", v), ("block_tables", block_tables),
+                    ("context_lens", context_lens), ("query_start", query_start)):
+        _cuda_contig(name, t, dev)
+    nb, hkv, d = _q8_cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    _require(k.dtype == v.dtype and k.shape == v.shape and k.dim() == 3
+             and tuple(k.shape[1:]) == (hkv, d),
+             "k, v must be [num_tokens, num_kv_heads, head_dim] of one dtype")
+    _require(block_tables.dtype == torch.int32 and block_tables.dim() == 2,
+             "block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    b, mb = block_tables.shape
+    _require(context_lens.dtype == torch.int32 and context_lens.shape == (b,),
+             "context_lens must be int32 [num_seqs]")
+    _require(query_start.dtype == torch.int32 and query_start.shape == (b + 1,),
+             "query_start must be int32 [num_seqs + 1]")
+    ptrs = (k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    args = ([C.c_void_p(t.data_ptr()) for t in ptrs]
+            + [b, k.shape[0], hkv, d, mb, nb, _dtype_code(k), C.c_void_p(_stream(dev, stream))])
+    return dev, args, ptrs
+
+
+def kv_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                 context_lens: torch.Tensor, query_start: torch.Tensor, stream=None) -> None:
+    """Quantise new tokens into an 8-bit cache, in place.  Rows
+    ``query_start[b] .. query_start[b+1]-1`` of ``k`` / ``v`` (``[T, Hkv, d]``,
+    float32, float16 or bfloat16) are the newest tokens of sequence ``b``,
+    which ``context_lens[b]`` counts; each goes to its place in the sequence's
+    blocks as an e4m3 code times the power-of-two scale of its (block, head).
+    A block that begins within the new tokens takes the smallest scale that
+    holds them; one with older tokens keeps its scale or grows it, the older
+    codes rounded anew.  Slots behind the last token are left alone."""
+    dev, args, _ = _append_q8_args(k, v, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                   context_lens, query_start, stream)
+    _call(dev, "pa_kv_append_q8", *args)
+
+
+def prepare_kv_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                         query_start, stream=None) -> Prepared:
+    dev, args, keep = _append_q8_args(k, v, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                      context_lens, query_start, stream)
+    return Prepared(capi.lib().pa_kv_append_q8, args, keep, dev)
+
+
+def _dequantize_args(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, k_out, v_out, stream):
+    dev = k_cache.device
+    for name, t in (("src_dst_pairs", src_dst_pairs), ("k_out", k_out), ("v_out", v_out)):
+        _cuda_contig(name, t, dev)
+    nb, hkv, d = _q8_cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    _require(src_dst_pairs.dtype == torch.int64 and src_dst_pairs.dim() == 2
+             and src_dst_pairs.shape[1] == 2, "src_dst_pairs must be int64 [n, 2]")
+    _require(k_out.dtype == v_out.dtype and k_out.shape == v_out.shape and k_out.dim() == 4
+             and tuple(k_out.shape[1:]) == (hkv, 16, d),
+             "k_out, v_out must be [num_out_blocks, num_kv_heads, 16, head_dim] of one dtype")
+    args = ([C.c_void_p(t.data_ptr()) for t in (k_cache, v_cache, k_scale, v_scale, src_dst_pairs)]
+            + [src_dst_pairs.shape[0], hkv, d, nb, k_out.shape[0], _dtype_code(k_out),
+               C.c_void_p(k_out.data_ptr()), C.c_void_p(v_out.data_ptr()),
+               C.c_void_p(_stream(dev, stream))])
+    return dev, args, (k_cache, v_cache, k_scale, v_scale, src_dst_pairs, k_out, v_out)
+
+
+def block_dequantize(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                     v_scale: torch.Tensor, src_dst_pairs: torch.Tensor, k_out: torch.Tensor,
+                     v_out: torch.Tensor, stream=None) -> None:
+    """Whole blocks of an 8-bit cache as values: for every pair ``(src, dst)``
+    (int64 ``[n, 2]`` on the device) block ``dst`` of ``k_out`` / ``v_out``
+    (float32, float16 or bfloat16 caches) becomes code times scale of block
+    ``src``.  Chunked prefill over an 8-bit context runs on the result."""
+    dev, args, _ = _dequantize_args(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, k_out,
+                                    v_out, stream)
+    _call(dev, "pa_block_dequantize", *args)
+
+
+def prepare_block_dequantize(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, k_out, v_out,
+                             stream=None) -> Prepared:
+    dev, args, keep = _dequantize_args(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, k_out,
+                                       v_out, stream)
+    return Prepared(capi.lib().pa_block_dequantize, args, keep, dev)
 
 
 class LayerCaches:
