@@ -9,17 +9,48 @@
 // with K_t = k_scale * code for the 8-bit cache.  Blocks none of whose tokens
 // are visible are not read, nor are their table entries (a program that has
 // freed them may leave any value there).
+//
+// Bound by the bytes of the visible blocks: 4 G / elem flops per byte at most
+// (G query heads per KV head), far under the tensor cores' rate.
+//
+//  * The visible blocks of a sequence are numbered 0 .. nb - 1 without gaps
+//    (first tokens' blocks, then the window's); all (sequence, KV head, block)
+//    triples in that order form one line of N blocks, cut into equal shares,
+//    one per warp of a full grid (one CTA of 8 warps per SM), at least
+//    kMinShare blocks each.  Equal bytes for every warp whatever the lengths;
+//    a long context is spread over the GPU, many short ones share a warp.
+//    The plan kernel writes each warp's starting point.
+//  * A warp streams its share through its own shared-memory ring, one tensor
+//    copy per K and V tile (16 rows), filled as many blocks ahead as fit; it
+//    does not stop at the ends of sequences.
+//  * Per block: S^T = K Q^T (16 tokens x 8 heads, m16n8k16), a base-2 softmax
+//    against a running reference that moves only when a score exceeds it by
+//    more than 8 (so almost every block needs one vote and no shuffle), and
+//    O^T += V^T P^T.  The contraction order over head_dim and the order of
+//    O's rows are free, so K and V fragments are read in 16-byte chunks:
+//    lane (g, t) takes chunks of K's rows g and g + 8, and chunk g of V's rows
+//    2t, 2t + 1, 2t + 8, 2t + 9, whose bytes pair up by one permute.
+//  * Where a warp's share cuts a sequence, its partial sums meet the other
+//    warps' of the CTA in shared memory; where the CTA's share cuts it, the
+//    CTA's two open ends go to the workspace and the CTA that arrives last at
+//    a sequence merges its pieces in order (the result does not depend on
+//    which one that is).
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <mutex>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "pagedattn.h"
 #include "q8.cuh"
 #include "status.h"
+#include "tensor_map.h"
 #include "trace.h"
 
 namespace pa {
@@ -29,19 +60,42 @@ namespace {
 constexpr int kBlockSize = 16;
 constexpr int kMaxGroup = 8;
 
-// Workspace: header words, then each sequence's planned length.
-constexpr int kHdrSignature = 0;
+constexpr int kWarps = 8;            // warps per CTA
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCtas = 256;        // CTAs the workspace has room for
+constexpr int kMinShare = 4;         // blocks a warp takes at least
+constexpr float kRescale = 8.f;      // log2 by which a score may exceed the reference
+constexpr int kPlanThreads = 1024;
+
+// Workspace header words: what the plan was made for; blocks in all, blocks
+// per warp, whether a sequence has none (its output rows are zero).
+constexpr int kHdrSignature = 0, kHdrBlocks = 1, kHdrShare = 2, kHdrEmpty = 3;
+
+// A CTA's two open ends: the one it shares with earlier CTAs (slot 0) and the
+// one that goes on in later ones (slot 1): unnormalised output, reference of
+// the scores, reference of the weights, sum of the softmax.
+template <int D>
+struct Piece {
+  float o[kMaxGroup][D];
+  float m[kMaxGroup], w[kMaxGroup], l[kMaxGroup];
+  int id, starts, ends, used;  // sequence * KV heads + head; holds its first / last block
+  int pad[4];
+};
 
 struct Layout {
-  size_t ctx, total;
+  size_t seqs, starts, arrivals, pieces, total;
 };
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-Layout workspace_layout(int num_seqs) {
+Layout workspace_layout(int num_seqs, int head_dim) {
   Layout l;
-  l.ctx = 256;
-  l.total = align256(l.ctx + size_t(num_seqs) * 4);
+  l.seqs = 256;
+  l.starts = align256(l.seqs + size_t(num_seqs) * sizeof(int4));
+  l.arrivals = align256(l.starts + size_t(kMaxCtas) * kWarps * sizeof(int4));
+  l.pieces = align256(l.arrivals + size_t(kMaxCtas) * 4);
+  l.total = align256(l.pieces + size_t(kMaxCtas) * 2 *
+                                    (head_dim == 128 ? sizeof(Piece<128>) : sizeof(Piece<64>)));
   return l;
 }
 
@@ -57,50 +111,118 @@ struct Params {
   int window, num_sinks;
   int num_seqs, num_q_heads, num_kv_heads, group;
   int max_blocks, num_blocks;
-  float scale;
+  int ncta;
+  float scale, scale_log2;
   int signature;
   int* header;
-  int* ctx;
+  int4* seqs;        // per sequence: length, visible blocks, visible blocks before it, 0
+  int4* starts;      // per warp: sequence, KV head, block within it
+  int* arrivals;     // per CTA: arrivals at the sequence that begins in it and goes on
+  void* pieces;      // [kMaxCtas][2] Piece
   unsigned* status;
+  unsigned long long timeout_ns;
 };
 
-__global__ void plan_kernel(const Params p) {
-  dev::grid_launch_dependents();
-  dev::grid_dependency_wait();
-  for (int b = threadIdx.x; b < p.num_seqs; b += blockDim.x) {
-    int n = p.context_lens[b];
-    if (n < 0 || n > p.max_blocks * kBlockSize) {
-      dev::flag_status(p.status, kStatusBounds);
-      n = n < 0 ? 0 : p.max_blocks * kBlockSize;
-    }
-    p.ctx[b] = n;
-  }
-  if (threadIdx.x == 0) p.header[kHdrSignature] = p.signature;
+// Which blocks of n tokens are visible: blocks 0 .. first - 1 and first + skip
+// .. ceil(n / 16) - 1; tokens under `low` are visible below `sinks` only.
+struct Range {
+  int low, sinks, first, skip, count;
+};
+
+__device__ __forceinline__ Range visible_range(int n, int window, int num_sinks) {
+  Range r;
+  const int blocks = (n + kBlockSize - 1) / kBlockSize;
+  r.low = window > 0 && window < n ? n - window : 0;
+  r.sinks = min(num_sinks, r.low);
+  const int sink_blocks = (r.sinks + kBlockSize - 1) / kBlockSize, low_block = r.low / kBlockSize;
+  r.first = sink_blocks < low_block ? sink_blocks : blocks;
+  r.skip = sink_blocks < low_block ? low_block - sink_blocks : 0;
+  r.count = blocks - r.skip;
+  return r;
 }
 
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_float<uint8_t>(uint8_t x) { return q8::decode2_float(x).x; }
+// One CTA: visible blocks per sequence and their running sum, then each warp's
+// starting point by bisection.  Latency-bound; once per step, not per layer.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
+  __shared__ int s_warp[kPlanThreads / 32];
+  __shared__ int s_carry, s_empty;
+  dev::grid_launch_dependents();
+  dev::grid_dependency_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    s_carry = 0;
+    s_empty = 0;
+  }
+  __syncthreads();
+  for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
+    const int b = base + tid;
+    int n = 0, nb = 0;
+    if (b < p.num_seqs) {
+      n = p.context_lens[b];
+      if (n < 0 || n > p.max_blocks * kBlockSize) {
+        dev::flag_status(p.status, kStatusBounds);
+        n = n < 0 ? 0 : p.max_blocks * kBlockSize;
+      }
+      nb = visible_range(n, p.window, p.num_sinks).count;
+      if (nb == 0) s_empty = 1;
+    }
+    int sum = nb;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += up;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      int v = s_warp[lane];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += up;
+      }
+      s_warp[lane] = v;
+    }
+    __syncthreads();
+    const int before = s_carry + (warp ? s_warp[warp - 1] : 0) + sum - nb;
+    if (b < p.num_seqs) p.seqs[b] = make_int4(n, nb, before, 0);
+    __syncthreads();
+    if (tid == 0) s_carry += s_warp[kPlanThreads / 32 - 1];
+    __syncthreads();
+  }
+  const int total = s_carry * p.num_kv_heads;
+  const int warps = p.ncta * kWarps;
+  const int share = max(kMinShare, (total + warps - 1) / warps);
+  for (int w = tid; w < warps; w += kPlanThreads) {
+    const long long f = (long long)w * share;
+    int4 at = make_int4(0, 0, 0, 0);
+    if (f < total) {
+      // the last sequence whose blocks begin at or before f (it has some: an
+      // empty one's successor begins where it does)
+      int lo = 0, hi = p.num_seqs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)p.seqs[mid].z * p.num_kv_heads <= f) lo = mid;
+        else hi = mid - 1;
+      }
+      const int4 q = p.seqs[lo];
+      const int r = int(f - (long long)q.z * p.num_kv_heads);
+      at = make_int4(lo, r / q.y, r % q.y, 0);
+    }
+    p.starts[w] = at;
+  }
+  for (int c = tid; c < p.ncta; c += kPlanThreads) p.arrivals[c] = 0;
+  if (tid == 0) {
+    p.header[kHdrBlocks] = total;
+    p.header[kHdrShare] = share;
+    p.header[kHdrEmpty] = s_empty;
+    p.header[kHdrSignature] = p.signature;
+  }
+}
 
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ float from_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-// One warp per (sequence, query head), a token at a time, fp32 throughout.
-template <typename T, typename C, int D>
-__global__ void __launch_bounds__(128) simple_kernel(const Params p) {
+// fp32 caches: one warp per (sequence, query head), a token at a time.
+template <int D>
+__global__ void __launch_bounds__(128) f32_kernel(const Params p) {
   constexpr int E = D / 32;
   dev::grid_launch_dependents();
   dev::grid_dependency_wait();
@@ -111,16 +233,16 @@ __global__ void __launch_bounds__(128) simple_kernel(const Params p) {
     return;
   }
   const int b = unit / p.num_q_heads, h = unit % p.num_q_heads, g = h / p.group;
-  const int n = p.ctx[b];
+  const int n = p.seqs[b].x;
   const int lo = p.window ? max(n - p.window, 0) : 0;
   const int first = min(p.num_sinks, lo);
-  const T* q = static_cast<const T*>(p.q) + size_t(unit) * D + lane * E;
-  const C* kc = static_cast<const C*>(p.k_cache);
-  const C* vc = static_cast<const C*>(p.v_cache);
+  const float* q = static_cast<const float*>(p.q) + size_t(unit) * D + lane * E;
+  const float* kc = static_cast<const float*>(p.k_cache);
+  const float* vc = static_cast<const float*>(p.v_cache);
   float qr[E], acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    qr[e] = to_float<T>(q[e]);
+    qr[e] = q[e];
     acc[e] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
@@ -133,30 +255,728 @@ __global__ void __launch_bounds__(128) simple_kernel(const Params p) {
     }
     const size_t tile = size_t(phys) * p.num_kv_heads + g;
     const size_t at = (tile * kBlockSize + t % kBlockSize) * D + lane * E;
-    const float ks = p.k_scale ? p.k_scale[tile] : 1.f, vs = p.v_scale ? p.v_scale[tile] : 1.f;
     float dot = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) dot = fmaf(qr[e], to_float<C>(kc[at + e]), dot);
+    for (int e = 0; e < E; ++e) dot = fmaf(qr[e], kc[at + e], dot);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    const float s = dot * ks * p.scale;
+    const float s = dot * p.scale;
     const float mn = fmaxf(m, s);
     const float a = expf(m - mn), w = expf(s - mn);
     l = l * a + w;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * (to_float<C>(vc[at + e]) * vs);
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * vc[at + e];
     m = mn;
   }
-  T* out = static_cast<T*>(p.out) + size_t(unit) * D + lane * E;
+  float* out = static_cast<float*>(p.out) + size_t(unit) * D + lane * E;
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = from_float<T>(acc[e] * inv);
+  for (int e = 0; e < E; ++e) out[e] = acc[e] * inv;
+}
+
+// ------------------------------------------------------- tensor-core path
+// Tiles of the cache: C = the cache's element (uint8_t: e4m3 codes).
+template <typename T, bool Q8, int D>
+struct Tiles {
+  using Mm = dev::Mma<typename std::conditional<Q8, __half, T>::type>;
+  static constexpr int kElem = Q8 ? 1 : 2;
+  static constexpr int kRowBytes = D * kElem;               // of a token's row
+  static constexpr int kBox = kRowBytes < 128 ? 64 : 128;   // bytes of a row per copy box
+  static constexpr int kBoxes = kRowBytes / kBox;
+  static constexpr int kBoxBytes = kBox * kBlockSize;
+  static constexpr int kTile = kRowBytes * kBlockSize;
+  static constexpr int kStage = 2 * kTile;                  // K tile, V tile
+  static constexpr int kStages = 24576 / kStage;            // 24 KB a warp: 3, 6 or 12 blocks
+  static constexpr int kSteps = D / 16;                     // 16-wide steps of either product
+  static constexpr size_t kRing = size_t(kWarps) * kStages * kStage;
+  static constexpr size_t kPieces = kRing;                  // Piece[kWarps]
+  static constexpr size_t kBars = kPieces + kWarps * sizeof(Piece<D>);
+  static constexpr size_t kScales = kBars + size_t(kWarps) * kStages * 8;
+  static constexpr size_t kBytes = kScales + size_t(kWarps) * kStages * 8;
+  // merge of a sequence's pieces over CTAs, in the ring's place
+  static_assert(kRing >= size_t(kMaxCtas) * kMaxGroup * 12, "merge weights");
+  static_assert(size_t(kStages) * kStage >= sizeof(Piece<D>), "a warp's last piece");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// 4-byte asynchronous copy, counted on `bar` when it has landed (the
+// barrier's arrival count includes it).
+__device__ __forceinline__ void copy4_arrive(void* dst, const void* src, uint64_t* bar) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dev::smem_u32(dst)), "l"(src)
+               : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(dev::smem_u32(bar))
+               : "memory");
+}
+
+// The tokens of K's rows g, g + 8 as MMA A fragments, eight or four steps.
+template <bool Q8, int D>
+__device__ __forceinline__ void load_k(uint32_t tile, int g, int t, uint32_t (&f)[D / 16][4]) {
+  if constexpr (Q8) {
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      // head_dim 16 (2t + j) .. + 15 (128), 16 t .. + 15 (64)
+      const uint32_t at = D == 128 ? tile + g * 128 + (((2 * t + j) ^ g) << 4)
+                                   : tile + g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+      const uint4 a = lds128(at), b = lds128(at + 8 * D);
+      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[4 * j + i][0] = q8::decode2(uint16_t(wa[i]));
+        f[4 * j + i][1] = q8::decode2(uint16_t(wb[i]));
+        f[4 * j + i][2] = q8::decode2(uint16_t(wa[i] >> 16));
+        f[4 * j + i][3] = q8::decode2(uint16_t(wb[i] >> 16));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      // half j / 2 of the row, its elements 8 (2t + j % 2) .. + 7
+      const uint32_t at = tile + (j >> 1) * 2048 + g * 128 + (((2 * t + (j & 1)) ^ g) << 4);
+      const uint4 a = lds128(at), b = lds128(at + 1024);
+      f[2 * j][0] = a.x;
+      f[2 * j][1] = b.x;
+      f[2 * j][2] = a.y;
+      f[2 * j][3] = b.y;
+      f[2 * j + 1][0] = a.z;
+      f[2 * j + 1][1] = b.z;
+      f[2 * j + 1][2] = a.w;
+      f[2 * j + 1][3] = b.w;
+    }
+  }
+}
+
+// V's rows 2t, 2t + 1, 2t + 8, 2t + 9 as A fragments of V^T: fragment m's rows
+// g and g + 8 are head_dim dim_of(m) and dim_of(m) + 1.
+template <bool Q8, int D>
+__device__ __forceinline__ int dim_of(int g, int m) {
+  if (Q8 && D == 128) return 16 * g + 2 * m;
+  return (m >> 2) * 64 + 8 * g + 2 * (m & 3);
+}
+
+template <bool Q8, int D, int W>
+__device__ __forceinline__ void pair_rows(const uint32_t (&r)[4][W], uint32_t (&f)[D / 16][4], int m0) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if constexpr (Q8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t sel = h ? 0x7362 : 0x5140;
+        const uint32_t a = __byte_perm(r[0][i], r[1][i], sel), b = __byte_perm(r[2][i], r[3][i], sel);
+        f[m0 + 2 * i + h][0] = q8::decode2(uint16_t(a));
+        f[m0 + 2 * i + h][1] = q8::decode2(uint16_t(a >> 16));
+        f[m0 + 2 * i + h][2] = q8::decode2(uint16_t(b));
+        f[m0 + 2 * i + h][3] = q8::decode2(uint16_t(b >> 16));
+      }
+    } else {
+      f[m0 + i][0] = __byte_perm(r[0][i], r[1][i], 0x5410);
+      f[m0 + i][1] = __byte_perm(r[0][i], r[1][i], 0x7632);
+      f[m0 + i][2] = __byte_perm(r[2][i], r[3][i], 0x5410);
+      f[m0 + i][3] = __byte_perm(r[2][i], r[3][i], 0x7632);
+    }
+  }
+}
+
+// keep: bit i set when V row i of the four is visible (the others read as 0,
+// whatever the cache holds there).
+template <bool Q8, int D>
+__device__ __forceinline__ void load_v(uint32_t tile, int g, int t, uint32_t keep,
+                                       uint32_t (&f)[D / 16][4]) {
+  const int rows[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
+  if constexpr (Q8 && D == 64) {
+    uint32_t w[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = rows[i];
+      uint2 v = lds64(tile + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+      if (!(keep >> i & 1)) v = make_uint2(0, 0);
+      w[i][0] = v.x;
+      w[i][1] = v.y;
+    }
+    pair_rows<Q8, D, 2>(w, f, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < (Q8 ? 1 : D / 64); ++j) {
+      uint32_t w[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = rows[i];
+        uint4 v = lds128(tile + j * 2048 + r * 128 + ((g ^ (r & 7)) << 4));
+        if (!(keep >> i & 1)) v = make_uint4(0, 0, 0, 0);
+        w[i][0] = v.x;
+        w[i][1] = v.y;
+        w[i][2] = v.z;
+        w[i][3] = v.w;
+      }
+      pair_rows<Q8, D, 4>(w, f, 4 * j);
+    }
+  }
+}
+
+// Query rows of head g as B fragments in load_k's order; heads past the group
+// are zero.  For the 8-bit cache the row is brought to f16 by a power of two
+// (returned as its exponent): a bf16 row of any size keeps every bit down to
+// 2^-38 of its largest element.
+template <typename T, bool Q8, int D>
+__device__ __forceinline__ int load_q(const T* row, bool live, int t, uint32_t (&f)[D / 16][2]) {
+  if constexpr (!Q8) {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (live) v = *reinterpret_cast<const uint4*>(row + (j >> 1) * 64 + (2 * t + (j & 1)) * 8);
+      f[2 * j][0] = v.x;
+      f[2 * j][1] = v.y;
+      f[2 * j + 1][0] = v.z;
+      f[2 * j + 1][1] = v.w;
+    }
+    return 0;
+  } else {
+    uint32_t w[D / 64][8];
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (live) {
+        const uint4* src = reinterpret_cast<const uint4*>(row + (D == 128 ? 16 * (2 * t + j) : 16 * t));
+        a = src[0];
+        b = src[1];
+      }
+      w[j][0] = a.x; w[j][1] = a.y; w[j][2] = a.z; w[j][3] = a.w;
+      w[j][4] = b.x; w[j][5] = b.y; w[j][6] = b.z; w[j][7] = b.w;
+    }
+    int e = 0;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      // the largest magnitude of the row, as bf16 bits (its four lanes)
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[j][i] & 0x7FFF7FFFu);
+      top = max(top & 0xFFFFu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int x = int(top >> 7);  // biased exponent; 0: nothing, 255: not finite
+      e = x == 0 || x == 255 ? 0 : max(x - 127 - 13, -120);
+      const float down = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 v = dev::Mma<__nv_bfloat16>::unpack(w[j][i]);
+          w[j][i] = dev::Mma<__half>::pack(v.x * down, v.y * down);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[4 * j + i][0] = w[j][2 * i];
+        f[4 * j + i][1] = w[j][2 * i + 1];
+      }
+    return e;
+  }
+}
+
+template <typename T, bool Q8, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v, const Params p) {
+  using S = Tiles<T, Q8, D>;
+  using Mm = typename S::Mm;
+  constexpr int ST = S::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + size_t(warp) * ST * S::kStage;
+  Piece<D>* head_pieces = reinterpret_cast<Piece<D>*>(smem + S::kPieces);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * ST;
+  float2* scales = reinterpret_cast<float2*>(smem + S::kScales) + warp * ST;
+  if (lane == 0) {
+    // a stage is full when its copies have landed: the K / V tiles (counted
+    // in bytes behind one arrival) and, for codes, their two scales
+    for (int i = 0; i < ST; ++i) dev::mbar_init(&full[i], Q8 ? 3 : 1);
+    dev::mbar_fence_init();
+    dev::prefetch_tensormap(&tmap_k);
+    dev::prefetch_tensormap(&tmap_v);
+  }
+  __syncwarp();
+  dev::grid_launch_dependents();
+  dev::grid_dependency_wait();
+
+  const int Hkv = p.num_kv_heads, G = p.group;
+  if (*reinterpret_cast<volatile int*>(&p.header[kHdrSignature]) != p.signature) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_status(p.status, kStatusPlan);
+    return;
+  }
+  const int total = p.header[kHdrBlocks], share = p.header[kHdrShare];
+  if (p.header[kHdrEmpty]) {
+    // rows of sequences without tokens are zero
+    for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x)
+      if (p.seqs[b].y == 0) {
+        uint4* row = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + size_t(b) * p.num_q_heads * D);
+        for (int i = threadIdx.x; i < p.num_q_heads * D / 8; i += kThreads) row[i] = make_uint4(0, 0, 0, 0);
+      }
+  }
+  const long long begin = ((long long)blockIdx.x * kWarps + warp) * share;
+  const int count = begin >= total ? 0 : int(min((long long)share, total - begin));  // this warp's blocks
+  if ((long long)blockIdx.x * kWarps * share >= total) return;
+
+  const unsigned long long tmo = p.timeout_ns;
+  const uint64_t policy = dev::l2_policy_evict_first();
+  const int4 start = p.starts[blockIdx.x * kWarps + warp];
+
+  // ---- copies.  Lane j holds the (block, head) tile of the warp's block
+  // 32 c + j; those of the next 32 are read from the tables while the
+  // current ones are in use.
+  int fb = start.x, fg = start.y, fv = start.z, filled = 0;  // where the next fill begins
+  int4 fseq = count > 0 ? p.seqs[fb] : make_int4(0, 1, 0, 0);
+  Range frange = visible_range(fseq.x, p.window, p.num_sinks);
+  int next_phys = 0, next_head = 0;
+  auto fill = [&]() {
+    int entry = -1;
+    const int todo = min(32, count - filled);
+    for (int done = 0; done < todo;) {
+      const int n = min(todo - done, fseq.y - fv);
+      if (lane >= done && lane < done + n) {
+        const int v = fv + lane - done;
+        entry = p.block_tables[size_t(fb) * p.max_blocks + (v < frange.first ? v : v + frange.skip)];
+        next_head = fg;
+      }
+      done += n;
+      fv += n;
+      if (fv == fseq.y) {
+        fv = 0;
+        if (++fg == Hkv && filled + done < count) {
+          fg = 0;
+          do fseq = p.seqs[++fb];
+          while (fseq.y == 0);
+          frange = visible_range(fseq.x, p.window, p.num_sinks);
+        }
+      }
+    }
+    next_phys = entry;
+    filled += todo;
+  };
+  int tile = 0;
+  auto promote = [&]() {
+    int phys = next_phys;
+    if (phys < 0 || phys >= p.num_blocks) {
+      if (lane < filled - ((filled - 1) & ~31)) dev::flag_status(p.status, kStatusBounds);
+      phys = 0;
+    }
+    tile = phys * Hkv + next_head;
+  };
+  int issued = 0, put = 0;  // blocks copied so far, ring stage of the next
+  auto issue = [&]() {
+    if ((issued & 31) == 0) {
+      promote();
+      if (filled < count) fill();
+    }
+    const int at = __shfl_sync(0xffffffffu, tile, issued & 31);
+    uint8_t* dst = ring + put * S::kStage;
+    uint64_t* bar = &full[put];
+    if (lane == 0) {
+      dev::mbar_arrive_expect_tx(bar, S::kStage);
+#pragma unroll
+      for (int x = 0; x < S::kBoxes; ++x) {
+        dev::tma_load_2d(dst + x * S::kBoxBytes, &tmap_k, x * (S::kBox / S::kElem), at * kBlockSize, bar, policy);
+        dev::tma_load_2d(dst + S::kTile + x * S::kBoxBytes, &tmap_v, x * (S::kBox / S::kElem), at * kBlockSize, bar,
+                         policy);
+      }
+    }
+    if (Q8 && lane < 2)
+      copy4_arrive(lane ? &scales[put].y : &scales[put].x, (lane ? p.v_scale : p.k_scale) + at, bar);
+    ++issued;
+    if (++put == ST) put = 0;
+  };
+  if (count > 0) fill();
+  for (int i = 0; i < ST && issued < count; ++i) issue();
+
+  // ---- the warp's segments: runs of blocks of one (sequence, KV head)
+  int b = start.x, h = start.y, v = start.z;
+  int get = 0, parity = 0, done = 0;
+  bool ok = true;
+  Piece<D>* tail = reinterpret_cast<Piece<D>*>(ring);
+  if (lane == 0) head_pieces[warp].used = 0;
+  bool has_tail = false;
+  while (done < count) {
+    const int4 seq = p.seqs[b];
+    if (seq.y == 0) {
+      ++b;
+      continue;
+    }
+    const Range range = visible_range(seq.x, p.window, p.num_sinks);
+    const int run = min(seq.y - v, count - done);
+    const bool starts = v == 0, ends = v + run == seq.y;
+    uint32_t qf[S::kSteps][2];
+    const T* qrow = static_cast<const T*>(p.q) + (size_t(b) * p.num_q_heads + h * G + g) * D;
+    const int qexp = load_q<T, Q8, D>(qrow, g < G, t, qf);
+    float f0 = p.scale_log2, f1 = p.scale_log2;
+    if constexpr (Q8) {
+      f0 *= __uint_as_float(uint32_t(127 + __shfl_sync(0xffffffffu, qexp, 8 * t)) << 23);
+      f1 *= __uint_as_float(uint32_t(127 + __shfl_sync(0xffffffffu, qexp, 8 * t + 4)) << 23);
+    }
+    float o[S::kSteps][4];
+#pragma unroll
+    for (int m = 0; m < S::kSteps; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
+    // per head (2t, 2t + 1): reference of the scores, of the weights, and
+    // this lane's part of the softmax's sum
+    float m0 = -INFINITY, m1 = -INFINITY, w0 = -INFINITY, w1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    for (int i = 0; i < run; ++i, ++v) {
+      if (!dev::mbar_wait_bounded(&full[get], parity, tmo, p.status)) ok = false;
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const uint32_t kt = dev::smem_u32(ring + get * S::kStage), vt = kt + S::kTile;
+      const int t0 = (v < range.first ? v : v + range.skip) * kBlockSize;
+      // ---- S^T = K Q^T in two chains
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        uint32_t f[S::kSteps][4];
+        load_k<Q8, D>(kt, g, t, f);
+#pragma unroll
+        for (int k = 0; k < S::kSteps; k += 2) {
+          Mm::run(s, f[k][0], f[k][1], f[k][2], f[k][3], qf[k][0], qf[k][1]);
+          Mm::run(s2, f[k + 1][0], f[k + 1][1], f[k + 1][2], f[k + 1][3], qf[k + 1][0], qf[k + 1][1]);
+        }
+      }
+      float c0 = f0, c1 = f1, lv = 0.f;
+      if constexpr (Q8) {
+        const float2 sc = scales[get];
+        c0 *= sc.x;
+        c1 *= sc.x;
+        lv = log2f(sc.y);
+      }
+      // tokens t0 + g (x0, x1) and t0 + g + 8 (x2, x3), heads 2t and 2t + 1
+      float x0 = (s[0] + s2[0]) * c0, x1 = (s[1] + s2[1]) * c1;
+      float x2 = (s[2] + s2[2]) * c0, x3 = (s[3] + s2[3]) * c1;
+      uint32_t keep = 15;
+      if (t0 + kBlockSize > seq.x || (t0 < range.low && t0 + kBlockSize > range.sinks)) {
+        auto sees = [&](int r) { return t0 + r < seq.x && (t0 + r >= range.low || t0 + r < range.sinks); };
+        if (!sees(g)) x0 = x1 = -INFINITY;
+        if (!sees(g + 8)) x2 = x3 = -INFINITY;
+        keep = uint32_t(sees(2 * t)) | uint32_t(sees(2 * t + 1)) << 1 | uint32_t(sees(2 * t + 8)) << 2 |
+               uint32_t(sees(2 * t + 9)) << 3;
+      }
+      // ---- references
+      const float top0 = fmaxf(x0, x2), top1 = fmaxf(x1, x3);
+      bool grow = top0 > m0 + kRescale || top1 > m1 + kRescale;
+      if constexpr (Q8) grow = grow || top0 + lv > w0 + kRescale || top1 + lv > w1 + kRescale;
+      if (__any_sync(0xffffffffu, grow)) {
+        float n0 = top0, n1 = top1;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+          n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+        }
+        // (a reference of -inf stands for nothing yet: the sums are zero)
+        auto raise = [](float& ref, float to) {
+          const float old = ref;
+          ref = fmaxf(ref, to);
+          return old == -INFINITY ? 0.f : dev::fast_exp2(old - ref);
+        };
+        l0 *= raise(m0, n0);
+        l1 *= raise(m1, n1);
+        float a0, a1;
+        if constexpr (Q8) {
+          a0 = raise(w0, n0 + lv);
+          a1 = raise(w1, n1 + lv);
+        } else {
+          a0 = raise(w0, n0);
+          a1 = raise(w1, n1);
+        }
+#pragma unroll
+        for (int m = 0; m < S::kSteps; ++m) {
+          o[m][0] *= a0;
+          o[m][1] *= a1;
+          o[m][2] *= a0;
+          o[m][3] *= a1;
+        }
+      }
+      const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+      float p0 = dev::fast_exp2(x0 - r0), p1 = dev::fast_exp2(x1 - r1);
+      float p2 = dev::fast_exp2(x2 - r0), p3 = dev::fast_exp2(x3 - r1);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      if constexpr (Q8) {
+        // the weights carry the block's value scale: 2^(x + log2 scale), kept
+        // near 1 by a reference of their own, so f16 holds them whatever
+        // the scales are
+        const float d0 = lv - (w0 == -INFINITY ? 0.f : w0), d1 = lv - (w1 == -INFINITY ? 0.f : w1);
+        p0 = dev::fast_exp2(x0 + d0);
+        p1 = dev::fast_exp2(x1 + d1);
+        p2 = dev::fast_exp2(x2 + d0);
+        p3 = dev::fast_exp2(x3 + d1);
+      }
+      // rounded once to the tensor cores' 16-bit type; transposed so that the
+      // tokens are the contraction
+      const uint32_t b0 = dev::movmatrix_trans(Mm::pack(p0, p1));
+      const uint32_t b1 = dev::movmatrix_trans(Mm::pack(p2, p3));
+      {
+        uint32_t f[S::kSteps][4];
+        load_v<Q8, D>(vt, g, t, keep, f);
+#pragma unroll
+        for (int m = 0; m < S::kSteps; ++m) Mm::run(o[m], f[m][0], f[m][1], f[m][2], f[m][3], b0, b1);
+      }
+      // the stage is read: its next block
+      __syncwarp();
+      if (issued < count) issue();
+      if (++get == ST) {
+        get = 0;
+        parity ^= 1;
+      }
+    }
+    if (!ok) break;
+    done += run;
+
+    // ---- end of the segment: sums over the 8 lanes that share a head
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+    if (starts && ends) {
+      const float i0 = l0 != 0.f ? dev::fast_exp2(Q8 ? w0 - m0 : 0.f) / l0 : 0.f;
+      const float i1 = l1 != 0.f ? dev::fast_exp2(Q8 ? w1 - m1 : 0.f) / l1 : 0.f;
+      T* base = static_cast<T*>(p.out) + (size_t(b) * p.num_q_heads + h * G) * D;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (2 * t + k >= G) continue;
+        const float inv = k ? i1 : i0;
+        T* row = base + (2 * t + k) * D;
+#pragma unroll
+        for (int m = 0; m < S::kSteps; m += 4) {
+          uint32_t x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = dev::Mma<T>::pack(o[m + e][k] * inv, o[m + e][2 + k] * inv);
+          *reinterpret_cast<uint4*>(row + dim_of<Q8, D>(g, m)) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    } else {
+      Piece<D>* piece = starts ? tail : &head_pieces[warp];
+      if (starts) has_tail = true;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (2 * t + k >= G) continue;
+#pragma unroll
+        for (int m = 0; m < S::kSteps; ++m)
+          *reinterpret_cast<float2*>(&piece->o[2 * t + k][dim_of<Q8, D>(g, m)]) =
+              make_float2(o[m][k], o[m][2 + k]);
+        if (g == 0) {
+          piece->m[2 * t + k] = k ? m1 : m0;
+          piece->w[2 * t + k] = k ? w1 : w0;
+          piece->l[2 * t + k] = k ? l1 : l0;
+        }
+      }
+      if (lane == 0) {
+        piece->id = b * Hkv + h;
+        piece->starts = starts;
+        piece->ends = ends;
+        piece->used = 1;
+      }
+    }
+    if (ends) {
+      v = 0;
+      if (++h == Hkv) {
+        h = 0;
+        ++b;
+      }
+    }
+  }
+  if (!ok) {
+    // a wait ran out: let this warp's copies in flight land, then give up
+    for (int k = done; k < issued; ++k) {
+      const int st = k % ST;
+      dev::mbar_wait_bounded(&full[st], (k / ST) & 1, tmo, p.status);
+    }
+  }
+  if (!__syncthreads_and(ok)) return;
+
+  // ---- pieces of sequences cut between the CTA's warps, in the line's order
+  // (each warp's first piece, then its last); those cut between CTAs too go
+  // to the workspace
+  __shared__ int s_tail[kWarps];
+  __shared__ int s_last;
+  if (lane == 0) s_tail[warp] = has_tail;
+  __syncthreads();
+  auto piece_at = [&](int k) -> Piece<D>* {
+    if (!(k & 1)) return head_pieces[k >> 1].used ? &head_pieces[k >> 1] : nullptr;
+    return s_tail[k >> 1] ? reinterpret_cast<Piece<D>*>(smem + size_t(k >> 1) * ST * S::kStage) : nullptr;
+  };
+  Piece<D>* slots = static_cast<Piece<D>*>(p.pieces) + size_t(blockIdx.x) * 2;
+  int open[2] = {-1, -1};  // (sequence, KV head) of the CTA's open ends
+  for (int k = 0; k < 2 * kWarps;) {
+    Piece<D>* first = piece_at(k);
+    if (!first) {
+      ++k;
+      continue;
+    }
+    const int id = first->id;
+    int last = k;
+    for (int j = k + 1; j < 2 * kWarps; ++j) {
+      const Piece<D>* x = piece_at(j);
+      if (x && x->id == id) last = j;
+    }
+    const bool starts = first->starts, ends = piece_at(last)->ends;
+    Piece<D>* slot = &slots[starts ? 1 : 0];
+    for (int e = threadIdx.x; e < G * D / 4; e += kThreads) {
+      const int head = e / (D / 4), d = (e % (D / 4)) * 4;
+      float m = -INFINITY, w = -INFINITY;
+      for (int j = k; j <= last; ++j)
+        if (const Piece<D>* x = piece_at(j)) {
+          m = fmaxf(m, x->m[head]);
+          w = fmaxf(w, x->w[head]);
+        }
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+      for (int j = k; j <= last; ++j)
+        if (const Piece<D>* x = piece_at(j)) {
+          const float a = x->w[head] == -INFINITY ? 0.f : dev::fast_exp2(x->w[head] - w);
+          const float4 y = *reinterpret_cast<const float4*>(&x->o[head][d]);
+          sum.x += a * y.x;
+          sum.y += a * y.y;
+          sum.z += a * y.z;
+          sum.w += a * y.w;
+          l += x->m[head] == -INFINITY ? 0.f : dev::fast_exp2(x->m[head] - m) * x->l[head];
+        }
+      if (starts && ends) {
+        const float inv = l != 0.f ? dev::fast_exp2(Q8 ? w - m : 0.f) / l : 0.f;
+        T* row = static_cast<T*>(p.out) + (size_t(id / Hkv) * p.num_q_heads + id % Hkv * G + head) * D + d;
+        *reinterpret_cast<uint2*>(row) = make_uint2(dev::Mma<T>::pack(sum.x * inv, sum.y * inv),
+                                                    dev::Mma<T>::pack(sum.z * inv, sum.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(&slot->o[head][d]) = sum;
+        if (d == 0) {
+          slot->m[head] = m;
+          slot->w[head] = w;
+          slot->l[head] = l;
+        }
+      }
+    }
+    if (!(starts && ends)) open[starts ? 1 : 0] = id;
+    k = last + 1;
+  }
+
+  // ---- sequences cut between CTAs: the last to arrive merges the pieces
+  for (int side = 0; side < 2; ++side) {
+    const int id = open[side];
+    if (id < 0) continue;
+    const int4 seq = p.seqs[id / Hkv];
+    const long long f = (long long)seq.z * Hkv + (long long)(id % Hkv) * seq.y;
+    const int span = share * kWarps;
+    const int c0 = int(f / span), c1 = int((f + seq.y - 1) / span), n = c1 - c0 + 1;
+    __threadfence();
+    __syncthreads();  // every thread's part of the piece is written
+    if (threadIdx.x == 0) {
+      s_last = dev::atom_add_acq_rel_gpu(&p.arrivals[c0], 1) == n - 1;
+      if (s_last) p.arrivals[c0] = 0;  // ready for the next run
+    }
+    __syncthreads();
+    if (!s_last) continue;
+    __threadfence();
+    // piece k is CTA c0 + k's: its later end for k == 0, its earlier one else
+    const Piece<D>* all = static_cast<const Piece<D>*>(p.pieces) + size_t(c0) * 2 + 1;
+    auto nth = [&](int k) { return k ? all + 2 * k - 1 : all; };
+    float* wsm = reinterpret_cast<float*>(smem);  // [n][8] weights
+    if (warp < G) {  // one warp per head
+      float m = -INFINITY, w = -INFINITY;
+      for (int k = lane; k < n; k += 32) {
+        m = fmaxf(m, __ldcg(&nth(k)->m[warp]));
+        w = fmaxf(w, __ldcg(&nth(k)->w[warp]));
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, off));
+      }
+      float l = 0.f;
+      for (int k = lane; k < n; k += 32) {
+        const float x = __ldcg(&nth(k)->m[warp]);
+        l += x == -INFINITY ? 0.f : dev::fast_exp2(x - m) * __ldcg(&nth(k)->l[warp]);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+      const float inv = l != 0.f ? dev::fast_exp2(Q8 ? w - m : 0.f) / l : 0.f;
+      for (int k = lane; k < n; k += 32) {
+        const float x = __ldcg(&nth(k)->w[warp]);
+        wsm[k * kMaxGroup + warp] = x == -INFINITY ? 0.f : dev::fast_exp2(x - w) * inv;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < G * D / 4; e += kThreads) {
+      const int head = e / (D / 4), d = (e % (D / 4)) * 4;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float a = wsm[k * kMaxGroup + head];
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(&nth(k)->o[head][d]));
+        sum.x += a * y.x;
+        sum.y += a * y.y;
+        sum.z += a * y.z;
+        sum.w += a * y.w;
+      }
+      T* row = static_cast<T*>(p.out) + (size_t(id / Hkv) * p.num_q_heads + id % Hkv * G + head) * D + d;
+      *reinterpret_cast<uint2*>(row) =
+          make_uint2(dev::Mma<T>::pack(sum.x, sum.y), dev::Mma<T>::pack(sum.z, sum.w));
+    }
+    __syncthreads();  // the weights are read
+  }
+}
+
+constexpr int kMaxDevices = 64;
+
+struct DeviceState {
+  std::once_flag once;
+  int error = 0;
+  int sms = 0;
+};
+DeviceState g_dev[kMaxDevices];
+
+template <typename T, bool Q8, int D>
+cudaError_t configure() {
+  return cudaFuncSetAttribute(attend_kernel<T, Q8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              int(Tiles<T, Q8, D>::kBytes));
+}
+
+int device_setup(int* ncta, const char* who) {
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= kMaxDevices)
+    return fail(PA_ERR_CUDA, "%s: no current CUDA device", who);
+  DeviceState& st = g_dev[device];
+  std::call_once(st.once, [&] {
+    cudaError_t e = cudaDeviceGetAttribute(&st.sms, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess) e = configure<__half, false, 64>();
+    if (e == cudaSuccess) e = configure<__half, false, 128>();
+    if (e == cudaSuccess) e = configure<__nv_bfloat16, false, 64>();
+    if (e == cudaSuccess) e = configure<__nv_bfloat16, false, 128>();
+    if (e == cudaSuccess) e = configure<__half, true, 64>();
+    if (e == cudaSuccess) e = configure<__half, true, 128>();
+    if (e == cudaSuccess) e = configure<__nv_bfloat16, true, 64>();
+    if (e == cudaSuccess) e = configure<__nv_bfloat16, true, 128>();
+    st.error = e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  });
+  if (st.error != PA_OK) return fail(st.error, "%s: per-device set-up failed on device %d", who, device);
+  *ncta = st.sms < kMaxCtas ? st.sms : kMaxCtas;
+  return PA_OK;
 }
 
 int signature_of(int window, int num_sinks, int num_seqs, int num_q_heads, int num_kv_heads,
-                 int head_dim, int max_blocks) {
+                 int head_dim, int max_blocks, int ncta) {
   uint32_t h = 2166136261u;
-  const int v[8] = {window, num_sinks, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks, 0x51D3};
+  const int v[9] = {window, num_sinks, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks, ncta, 0x51D3};
   for (int x : v) {
     h ^= uint32_t(x);
     h *= 16777619u;
@@ -203,10 +1023,20 @@ int check_sizes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, i
   return PA_OK;
 }
 
-template <typename T, typename C>
-cudaError_t launch_simple(const cudaLaunchConfig_t& cfg, int head_dim, const Params& p) {
-  return head_dim == 128 ? cudaLaunchKernelEx(&cfg, simple_kernel<T, C, 128>, p)
-                         : cudaLaunchKernelEx(&cfg, simple_kernel<T, C, 64>, p);
+template <typename T, bool Q8, int D>
+cudaError_t launch_attend(cudaLaunchConfig_t cfg, const CUtensorMap& mk, const CUtensorMap& mv,
+                          const Params& p) {
+  cfg.gridDim = dim3(unsigned(p.ncta));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Tiles<T, Q8, D>::kBytes;
+  return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D>, mk, mv, p);
+}
+
+template <typename T, bool Q8>
+cudaError_t launch_attend(const cudaLaunchConfig_t& cfg, int head_dim, const CUtensorMap& mk,
+                          const CUtensorMap& mv, const Params& p) {
+  return head_dim == 128 ? launch_attend<T, Q8, 128>(cfg, mk, mv, p)
+                         : launch_attend<T, Q8, 64>(cfg, mk, mv, p);
 }
 
 int entry(const Call& c) {
@@ -235,12 +1065,15 @@ int entry(const Call& c) {
     if (c.num_blocks <= 0 || double(c.num_blocks) * c.num_kv_heads * kBlockSize >= 2147483647.0)
       return fail(PA_ERR_INVALID_ARG, "%s: bad num_blocks", who);
   }
-  const Layout lay = workspace_layout(c.num_seqs);
+  const Layout lay = workspace_layout(c.num_seqs, c.head_dim);
   if (!c.workspace || (reinterpret_cast<uintptr_t>(c.workspace) & 255))
     return fail(PA_ERR_INVALID_ARG, "%s: workspace must be non-NULL and 256-byte aligned", who);
   if (c.workspace_bytes < lay.total)
     return fail(PA_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", who, c.workspace_bytes,
                 lay.total);
+  int ncta = 0;
+  rc = device_setup(&ncta, who);
+  if (rc != PA_OK) return rc;
   unsigned* status = device_status_word();
   if (!status) return PA_ERR_CUDA;
   Params p = {};
@@ -260,13 +1093,19 @@ int entry(const Call& c) {
   p.group = group;
   p.max_blocks = c.max_blocks;
   p.num_blocks = c.num_blocks;
+  p.ncta = ncta;
   p.scale = c.scale;
+  p.scale_log2 = c.scale * 1.4426950408889634f;
   p.signature = signature_of(c.window, c.num_sinks, c.num_seqs, c.num_q_heads, c.num_kv_heads,
-                             c.head_dim, c.max_blocks);
+                             c.head_dim, c.max_blocks, ncta);
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   p.header = reinterpret_cast<int*>(ws);
-  p.ctx = reinterpret_cast<int*>(ws + lay.ctx);
+  p.seqs = reinterpret_cast<int4*>(ws + lay.seqs);
+  p.starts = reinterpret_cast<int4*>(ws + lay.starts);
+  p.arrivals = reinterpret_cast<int*>(ws + lay.arrivals);
+  p.pieces = ws + lay.pieces;
   p.status = status;
+  p.timeout_ns = 1000000000ull;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
   cfg.stream = static_cast<cudaStream_t>(c.stream);
@@ -274,22 +1113,34 @@ int entry(const Call& c) {
   cfg.numAttrs = 1;
   if (c.mode != Mode::kRunOnly) {
     cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kPlanThreads);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, p);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: plan launch failed: %s", who, cudaGetErrorString(e));
   }
   if (!runs) return PA_OK;
-  cfg.gridDim = dim3(unsigned((c.num_seqs * c.num_q_heads + 3) / 4));
-  cfg.blockDim = dim3(128);
   cudaError_t e;
-  if (c.dtype == PA_F32)
-    e = launch_simple<float, float>(cfg, c.head_dim, p);
-  else if (c.dtype == PA_F16)
-    e = c.q8 ? launch_simple<__half, uint8_t>(cfg, c.head_dim, p)
-             : launch_simple<__half, __half>(cfg, c.head_dim, p);
-  else
-    e = c.q8 ? launch_simple<__nv_bfloat16, uint8_t>(cfg, c.head_dim, p)
-             : launch_simple<__nv_bfloat16, __nv_bfloat16>(cfg, c.head_dim, p);
+  if (c.dtype == PA_F32) {
+    cfg.gridDim = dim3(unsigned((c.num_seqs * c.num_q_heads + 3) / 4));
+    cfg.blockDim = dim3(128);
+    e = c.head_dim == 128 ? cudaLaunchKernelEx(&cfg, f32_kernel<128>, p)
+                          : cudaLaunchKernelEx(&cfg, f32_kernel<64>, p);
+  } else {
+    alignas(64) CUtensorMap mk, mv;
+    auto encode = [&](CUtensorMap* map, const void* cache) {
+      return c.q8 ? q8_cache_tensor_map(map, cache, c.num_blocks, c.num_kv_heads, c.head_dim)
+                  : cache_tensor_map(map, cache, c.dtype == PA_BF16, c.num_blocks, c.num_kv_heads,
+                                     c.head_dim);
+    };
+    rc = encode(&mk, c.k_cache);
+    if (rc == PA_OK) rc = encode(&mv, c.v_cache);
+    if (rc != PA_OK) return rc;
+    if (c.dtype == PA_F16)
+      e = c.q8 ? launch_attend<__half, true>(cfg, c.head_dim, mk, mv, p)
+               : launch_attend<__half, false>(cfg, c.head_dim, mk, mv, p);
+    else
+      e = c.q8 ? launch_attend<__nv_bfloat16, true>(cfg, c.head_dim, mk, mv, p)
+               : launch_attend<__nv_bfloat16, false>(cfg, c.head_dim, mk, mv, p);
+  }
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
   return PA_OK;
 }
@@ -311,7 +1162,7 @@ PA_API int pa_paged_attention_decode_window_workspace_size(int num_seqs, int num
   const int rc = window::check_sizes(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                      max_blocks_per_seq, who);
   if (rc != PA_OK) return rc;
-  *bytes = window::workspace_layout(num_seqs).total;
+  *bytes = window::workspace_layout(num_seqs, head_dim).total;
   return PA_OK;
 }
 

@@ -16,6 +16,13 @@ namespace pa {
 int cache_tensor_map(CUtensorMap* out, const void* cache, bool bf16, int num_blocks,
                      int num_kv_heads, int head_dim);
 
+// The same of a cache of 8-bit codes: one copy box is a whole (block, head)
+// tile, 16 rows of head_dim bytes (128-byte swizzle for head_dim 128: the
+// 16-byte chunks of row r XOR-ed with r % 8; 64-byte swizzle for head_dim 64:
+// with (r / 2) % 4).
+int q8_cache_tensor_map(CUtensorMap* out, const void* cache, int num_blocks, int num_kv_heads,
+                        int head_dim);
+
 // Encodes the 3-D tensor map of a query tensor `[total_q][num_q_heads][head_dim]`
 // (16-bit) whose copy box is 64 elements x `group` heads x (rows / group)
 // tokens with 128-byte swizzle: one box fills `rows` consecutive 128-byte
