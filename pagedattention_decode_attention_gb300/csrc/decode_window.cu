@@ -92,7 +92,7 @@ Layout workspace_layout(int num_seqs, int head_dim) {
   Layout l;
   l.seqs = 256;
   l.starts = align256(l.seqs + size_t(num_seqs) * sizeof(int4));
-  l.arrivals = align256(l.starts + size_t(kMaxCtas) * kWarps * sizeof(int4));
+  l.arrivals = align256(l.starts + size_t(kMaxCtas) * kWarps * 2 * sizeof(int4));
   l.pieces = align256(l.arrivals + size_t(kMaxCtas) * 4);
   l.total = align256(l.pieces + size_t(kMaxCtas) * 2 *
                                     (head_dim == 128 ? sizeof(Piece<128>) : sizeof(Piece<64>)));
@@ -116,7 +116,7 @@ struct Params {
   int signature;
   int* header;
   int4* seqs;        // per sequence: length, visible blocks, visible blocks before it, 0
-  int4* starts;      // per warp: sequence, KV head, block within it
+  int4* starts;      // per warp: sequence, KV head, block within it, blocks; its seqs entry
   int* arrivals;     // per CTA: arrivals at the sequence that begins in it and goes on
   void* pieces;      // [kMaxCtas][2] Piece
   unsigned* status;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   const int share = max(kMinShare, (total + warps - 1) / warps);
   for (int w = tid; w < warps; w += kPlanThreads) {
     const long long f = (long long)w * share;
-    int4 at = make_int4(0, 0, 0, 0);
+    int4 at = make_int4(0, 0, 0, 0), q = make_int4(0, 1, 0, 0);
     if (f < total) {
       // the last sequence whose blocks begin at or before f (it has some: an
       // empty one's successor begins where it does)
@@ -205,11 +205,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
         if ((long long)p.seqs[mid].z * p.num_kv_heads <= f) lo = mid;
         else hi = mid - 1;
       }
-      const int4 q = p.seqs[lo];
+      q = p.seqs[lo];
       const int r = int(f - (long long)q.z * p.num_kv_heads);
-      at = make_int4(lo, r / q.y, r % q.y, 0);
+      at = make_int4(lo, r / q.y, r % q.y, int(min((long long)share, total - f)));
     }
-    p.starts[w] = at;
+    p.starts[2 * w] = at;
+    p.starts[2 * w + 1] = q;
   }
   for (int c = tid; c < p.ncta; c += kPlanThreads) p.arrivals[c] = 0;
   if (tid == 0) {
@@ -291,8 +292,7 @@ struct Tiles {
   static constexpr size_t kRing = size_t(kWarps) * kStages * kStage;
   static constexpr size_t kPieces = kRing;                  // Piece[kWarps]
   static constexpr size_t kBars = kPieces + kWarps * sizeof(Piece<D>);
-  static constexpr size_t kScales = kBars + size_t(kWarps) * kStages * 8;
-  static constexpr size_t kBytes = kScales + size_t(kWarps) * kStages * 8;
+  static constexpr size_t kBytes = kBars + size_t(kWarps) * kStages * 8;
   // merge of a sequence's pieces over CTAs, in the ring's place
   static_assert(kRing >= size_t(kMaxCtas) * kMaxGroup * 12, "merge weights");
   static_assert(size_t(kStages) * kStage >= sizeof(Piece<D>), "a warp's last piece");
@@ -312,13 +312,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
-// 4-byte asynchronous copy, counted on `bar` when it has landed (the
-// barrier's arrival count includes it).
-__device__ __forceinline__ void copy4_arrive(void* dst, const void* src, uint64_t* bar) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dev::smem_u32(dst)), "l"(src)
-               : "memory");
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(dev::smem_u32(bar))
-               : "memory");
+// log2 of a positive scale, exact for a power of two.
+__device__ __forceinline__ float log2_scale(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const int e = int(u >> 23) - 127;
+  if (e == -127 || e == 128) return log2f(x);  // zero, subnormal; infinity, NaN
+  return float(e) + __log2f(__uint_as_float((u & 0x7FFFFFu) | 0x3F800000u));
 }
 
 // The tokens of K's rows g, g + 8 as MMA A fragments, eight or four steps.
@@ -389,8 +388,17 @@ __device__ __forceinline__ void pair_rows(const uint32_t (&r)[4][W], uint32_t (&
   }
 }
 
+template <int W>
+__device__ __forceinline__ void hide_rows(uint32_t keep, uint32_t (&w)[4][W]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (!(keep >> i & 1)) w[i][j] = 0;
+}
+
 // keep: bit i set when V row i of the four is visible (the others read as 0,
-// whatever the cache holds there).
+// whatever the cache holds there); 15 for all but a few blocks.
 template <bool Q8, int D>
 __device__ __forceinline__ void load_v(uint32_t tile, int g, int t, uint32_t keep,
                                        uint32_t (&f)[D / 16][4]) {
@@ -400,11 +408,11 @@ __device__ __forceinline__ void load_v(uint32_t tile, int g, int t, uint32_t kee
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = rows[i];
-      uint2 v = lds64(tile + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
-      if (!(keep >> i & 1)) v = make_uint2(0, 0);
+      const uint2 v = lds64(tile + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
       w[i][0] = v.x;
       w[i][1] = v.y;
     }
+    if (keep != 15) hide_rows(keep, w);
     pair_rows<Q8, D, 2>(w, f, 0);
   } else {
 #pragma unroll
@@ -413,79 +421,68 @@ __device__ __forceinline__ void load_v(uint32_t tile, int g, int t, uint32_t kee
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = rows[i];
-        uint4 v = lds128(tile + j * 2048 + r * 128 + ((g ^ (r & 7)) << 4));
-        if (!(keep >> i & 1)) v = make_uint4(0, 0, 0, 0);
+        const uint4 v = lds128(tile + j * 2048 + r * 128 + ((g ^ (r & 7)) << 4));
         w[i][0] = v.x;
         w[i][1] = v.y;
         w[i][2] = v.z;
         w[i][3] = v.w;
       }
+      if (keep != 15) hide_rows(keep, w);
       pair_rows<Q8, D, 4>(w, f, 4 * j);
     }
   }
 }
 
-// Query rows of head g as B fragments in load_k's order; heads past the group
-// are zero.  For the 8-bit cache the row is brought to f16 by a power of two
-// (returned as its exponent): a bf16 row of any size keeps every bit down to
-// 2^-38 of its largest element.
+// Query row of head g in load_k's order, as loaded (heads past the group are
+// zero) ...
 template <typename T, bool Q8, int D>
-__device__ __forceinline__ int load_q(const T* row, bool live, int t, uint32_t (&f)[D / 16][2]) {
-  if constexpr (!Q8) {
+__device__ __forceinline__ void load_q(const T* row, bool live, int t, uint4 (&w)[D / 32]) {
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (live) v = *reinterpret_cast<const uint4*>(row + (j >> 1) * 64 + (2 * t + (j & 1)) * 8);
-      f[2 * j][0] = v.x;
-      f[2 * j][1] = v.y;
-      f[2 * j + 1][0] = v.z;
-      f[2 * j + 1][1] = v.w;
-    }
-    return 0;
-  } else {
-    uint32_t w[D / 64][8];
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (live) {
-        const uint4* src = reinterpret_cast<const uint4*>(row + (D == 128 ? 16 * (2 * t + j) : 16 * t));
-        a = src[0];
-        b = src[1];
-      }
-      w[j][0] = a.x; w[j][1] = a.y; w[j][2] = a.z; w[j][3] = a.w;
-      w[j][4] = b.x; w[j][5] = b.y; w[j][6] = b.z; w[j][7] = b.w;
-    }
-    int e = 0;
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-      // the largest magnitude of the row, as bf16 bits (its four lanes)
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[j][i] & 0x7FFF7FFFu);
-      top = max(top & 0xFFFFu, top >> 16);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int x = int(top >> 7);  // biased exponent; 0: nothing, 255: not finite
-      e = x == 0 || x == 255 ? 0 : max(x - 127 - 13, -120);
-      const float down = __uint_as_float(uint32_t(127 - e) << 23);
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 v = dev::Mma<__nv_bfloat16>::unpack(w[j][i]);
-          w[j][i] = dev::Mma<__half>::pack(v.x * down, v.y * down);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[4 * j + i][0] = w[j][2 * i];
-        f[4 * j + i][1] = w[j][2 * i + 1];
-      }
-    return e;
+  for (int j = 0; j < D / 32; ++j) {
+    const int at = Q8 ? (D == 128 ? 32 * t + 8 * j : 16 * t + 8 * j)
+                      : (j >> 1) * 64 + (2 * t + (j & 1)) * 8;
+    w[j] = make_uint4(0, 0, 0, 0);
+    if (live) w[j] = *reinterpret_cast<const uint4*>(row + at);
   }
+}
+
+// ... and as B fragments.  For the 8-bit cache a bf16 row is brought to f16 by
+// a power of two (returned as its exponent): a row of any size keeps every bit
+// down to 2^-38 of its largest element.
+template <typename T, bool Q8, int D>
+__device__ __forceinline__ int convert_q(const uint4 (&raw)[D / 32], uint32_t (&f)[D / 16][2]) {
+  uint32_t w[D / 8];
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    w[4 * j] = raw[j].x;
+    w[4 * j + 1] = raw[j].y;
+    w[4 * j + 2] = raw[j].z;
+    w[4 * j + 3] = raw[j].w;
+  }
+  int e = 0;
+  if constexpr (Q8 && std::is_same<T, __nv_bfloat16>::value) {
+    // the largest magnitude of the row, as bf16 bits (its four lanes)
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int x = int(top >> 7);  // biased exponent; 0: nothing, 255: not finite
+    e = x == 0 || x == 255 ? 0 : max(x - 127 - 13, -120);
+    const float down = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const float2 v = dev::Mma<__nv_bfloat16>::unpack(w[i]);
+      w[i] = dev::Mma<__half>::pack(v.x * down, v.y * down);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    f[i][0] = w[2 * i];
+    f[i][1] = w[2 * i + 1];
+  }
+  return e;
 }
 
 template <typename T, bool Q8, int D>
@@ -501,11 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + size_t(warp) * ST * S::kStage;
   Piece<D>* head_pieces = reinterpret_cast<Piece<D>*>(smem + S::kPieces);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * ST;
-  float2* scales = reinterpret_cast<float2*>(smem + S::kScales) + warp * ST;
   if (lane == 0) {
-    // a stage is full when its copies have landed: the K / V tiles (counted
-    // in bytes behind one arrival) and, for codes, their two scales
-    for (int i = 0; i < ST; ++i) dev::mbar_init(&full[i], Q8 ? 3 : 1);
+    for (int i = 0; i < ST; ++i) dev::mbar_init(&full[i], 1);
     dev::mbar_fence_init();
     dev::prefetch_tensormap(&tmap_k);
     dev::prefetch_tensormap(&tmap_v);
@@ -515,12 +509,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   dev::grid_dependency_wait();
 
   const int Hkv = p.num_kv_heads, G = p.group;
-  if (*reinterpret_cast<volatile int*>(&p.header[kHdrSignature]) != p.signature) {
+  // (all of the plan's words at once: one trip to memory)
+  const int4 hdr = *reinterpret_cast<const int4*>(p.header);
+  const int4 start = p.starts[2 * (blockIdx.x * kWarps + warp)];
+  const int4 start_seq = p.starts[2 * (blockIdx.x * kWarps + warp) + 1];
+  if (hdr.x != p.signature) {
     if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_status(p.status, kStatusPlan);
     return;
   }
-  const int total = p.header[kHdrBlocks], share = p.header[kHdrShare];
-  if (p.header[kHdrEmpty]) {
+  const int total = hdr.y, share = hdr.z;
+  if (hdr.w) {
     // rows of sequences without tokens are zero
     for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x)
       if (p.seqs[b].y == 0) {
@@ -528,19 +526,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = threadIdx.x; i < p.num_q_heads * D / 8; i += kThreads) row[i] = make_uint4(0, 0, 0, 0);
       }
   }
-  const long long begin = ((long long)blockIdx.x * kWarps + warp) * share;
-  const int count = begin >= total ? 0 : int(min((long long)share, total - begin));  // this warp's blocks
+  const int count = start.w;  // this warp's blocks
   if ((long long)blockIdx.x * kWarps * share >= total) return;
 
   const unsigned long long tmo = p.timeout_ns;
   const uint64_t policy = dev::l2_policy_evict_first();
-  const int4 start = p.starts[blockIdx.x * kWarps + warp];
 
   // ---- copies.  Lane j holds the (block, head) tile of the warp's block
   // 32 c + j; those of the next 32 are read from the tables while the
   // current ones are in use.
   int fb = start.x, fg = start.y, fv = start.z, filled = 0;  // where the next fill begins
-  int4 fseq = count > 0 ? p.seqs[fb] : make_int4(0, 1, 0, 0);
+  int4 fseq = start_seq;
   Range frange = visible_range(fseq.x, p.window, p.num_sinks);
   int next_phys = 0, next_head = 0;
   auto fill = [&]() {
@@ -569,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     filled += todo;
   };
   int tile = 0;
+  float next_ks = 0.f, next_vs = 0.f;  // their scales
   auto promote = [&]() {
     int phys = next_phys;
     if (phys < 0 || phys >= p.num_blocks) {
@@ -576,6 +573,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       phys = 0;
     }
     tile = phys * Hkv + next_head;
+    if constexpr (Q8) {
+      next_ks = p.k_scale[tile];
+      next_vs = p.v_scale[tile];
+    }
   };
   int issued = 0, put = 0;  // blocks copied so far, ring stage of the next
   auto issue = [&]() {
@@ -595,8 +596,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                          policy);
       }
     }
-    if (Q8 && lane < 2)
-      copy4_arrive(lane ? &scales[put].y : &scales[put].x, (lane ? p.v_scale : p.k_scale) + at, bar);
     ++issued;
     if (++put == ST) put = 0;
   };
@@ -605,23 +604,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- the warp's segments: runs of blocks of one (sequence, KV head)
   int b = start.x, h = start.y, v = start.z;
-  int get = 0, parity = 0, done = 0;
+  int4 seq = start_seq;
+  int get = 0, parity = 0, done = 0;  // done: blocks taken from the ring
   bool ok = true;
+  float ks = 0.f, lvs = 0.f;  // lane j: K scale and log2 of V's of block 32 c + j
   Piece<D>* tail = reinterpret_cast<Piece<D>*>(ring);
   if (lane == 0) head_pieces[warp].used = 0;
   bool has_tail = false;
+  // a segment's query rows are loaded a segment ahead
+  uint4 raw[D / 32];
+  auto fetch_q = [&](int qb, int qh) {
+    load_q<T, Q8, D>(static_cast<const T*>(p.q) + (size_t(qb) * p.num_q_heads + qh * G + g) * D, g < G, t, raw);
+  };
+  if (count > 0) fetch_q(b, h);
   while (done < count) {
-    const int4 seq = p.seqs[b];
-    if (seq.y == 0) {
-      ++b;
-      continue;
-    }
     const Range range = visible_range(seq.x, p.window, p.num_sinks);
     const int run = min(seq.y - v, count - done);
     const bool starts = v == 0, ends = v + run == seq.y;
     uint32_t qf[S::kSteps][2];
-    const T* qrow = static_cast<const T*>(p.q) + (size_t(b) * p.num_q_heads + h * G + g) * D;
-    const int qexp = load_q<T, Q8, D>(qrow, g < G, t, qf);
+    const int qexp = convert_q<T, Q8, D>(raw, qf);
+    // the next segment: the sequence's next head, or the next sequence that
+    // has tokens
+    int nb = b, nh = h + 1;
+    int4 nseq = seq;
+    if (run < count - done) {
+      if (nh == Hkv) {
+        nh = 0;
+        do nseq = p.seqs[++nb];
+        while (nseq.y == 0);
+      }
+      fetch_q(nb, nh);
+    }
     float f0 = p.scale_log2, f1 = p.scale_log2;
     if constexpr (Q8) {
       f0 *= __uint_as_float(uint32_t(127 + __shfl_sync(0xffffffffu, qexp, 8 * t)) << 23);
@@ -634,70 +647,99 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this lane's part of the softmax's sum
     float m0 = -INFINITY, m1 = -INFINITY, w0 = -INFINITY, w1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    for (int i = 0; i < run; ++i, ++v) {
-      if (!dev::mbar_wait_bounded(&full[get], parity, tmo, p.status)) ok = false;
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
+    // N blocks at once: their products interleave, and the wait, the vote and
+    // the loop are paid once
+    auto take = [&](auto number) -> bool {
+      constexpr int N = decltype(number)::value;
+      uint32_t kt[N];
+      float x[N][4], lv[N];
+      uint32_t keep[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (!dev::mbar_wait_bounded(&full[get], parity, tmo, p.status)) ok = false;
+        kt[i] = dev::smem_u32(ring + get * S::kStage);
+        if (++get == ST) {
+          get = 0;
+          parity ^= 1;
+        }
       }
-      const uint32_t kt = dev::smem_u32(ring + get * S::kStage), vt = kt + S::kTile;
-      const int t0 = (v < range.first ? v : v + range.skip) * kBlockSize;
-      // ---- S^T = K Q^T in two chains
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
-      {
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return false;
+      // ---- S^T = K Q^T, each block's in two chains
+      float s[N][4], s2[N][4];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] = s2[i][e] = 0.f;
         uint32_t f[S::kSteps][4];
-        load_k<Q8, D>(kt, g, t, f);
+        load_k<Q8, D>(kt[i], g, t, f);
 #pragma unroll
         for (int k = 0; k < S::kSteps; k += 2) {
-          Mm::run(s, f[k][0], f[k][1], f[k][2], f[k][3], qf[k][0], qf[k][1]);
-          Mm::run(s2, f[k + 1][0], f[k + 1][1], f[k + 1][2], f[k + 1][3], qf[k + 1][0], qf[k + 1][1]);
+          Mm::run(s[i], f[k][0], f[k][1], f[k][2], f[k][3], qf[k][0], qf[k][1]);
+          Mm::run(s2[i], f[k + 1][0], f[k + 1][1], f[k + 1][2], f[k + 1][3], qf[k + 1][0], qf[k + 1][1]);
         }
       }
-      float c0 = f0, c1 = f1, lv = 0.f;
-      if constexpr (Q8) {
-        const float2 sc = scales[get];
-        c0 *= sc.x;
-        c1 *= sc.x;
-        lv = log2f(sc.y);
-      }
-      // tokens t0 + g (x0, x1) and t0 + g + 8 (x2, x3), heads 2t and 2t + 1
-      float x0 = (s[0] + s2[0]) * c0, x1 = (s[1] + s2[1]) * c1;
-      float x2 = (s[2] + s2[2]) * c0, x3 = (s[3] + s2[3]) * c1;
-      uint32_t keep = 15;
-      if (t0 + kBlockSize > seq.x || (t0 < range.low && t0 + kBlockSize > range.sinks)) {
-        auto sees = [&](int r) { return t0 + r < seq.x && (t0 + r >= range.low || t0 + r < range.sinks); };
-        if (!sees(g)) x0 = x1 = -INFINITY;
-        if (!sees(g + 8)) x2 = x3 = -INFINITY;
-        keep = uint32_t(sees(2 * t)) | uint32_t(sees(2 * t + 1)) << 1 | uint32_t(sees(2 * t + 8)) << 2 |
-               uint32_t(sees(2 * t + 9)) << 3;
+      // ---- base-2 scores of tokens t0 + g (x[0], x[1]) and t0 + g + 8
+      // (x[2], x[3]), heads 2t and 2t + 1
+      float top0 = -INFINITY, top1 = -INFINITY, high0 = -INFINITY, high1 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float c0 = f0, c1 = f1;
+        lv[i] = 0.f;
+        if constexpr (Q8) {
+          if ((done & 31) == 0) {
+            ks = next_ks;
+            lvs = log2_scale(next_vs);
+          }
+          const float k = __shfl_sync(0xffffffffu, ks, done & 31);
+          lv[i] = __shfl_sync(0xffffffffu, lvs, done & 31);
+          c0 *= k;
+          c1 *= k;
+        }
+        ++done;
+        x[i][0] = (s[i][0] + s2[i][0]) * c0;
+        x[i][1] = (s[i][1] + s2[i][1]) * c1;
+        x[i][2] = (s[i][2] + s2[i][2]) * c0;
+        x[i][3] = (s[i][3] + s2[i][3]) * c1;
+        keep[i] = 15;
+        const int t0 = (v + i < range.first ? v + i : v + i + range.skip) * kBlockSize;
+        if (t0 + kBlockSize > seq.x || (t0 < range.low && t0 + kBlockSize > range.sinks)) {
+          auto sees = [&](int r) {
+            return t0 + r < seq.x && (t0 + r >= range.low || t0 + r < range.sinks);
+          };
+          if (!sees(g)) x[i][0] = x[i][1] = -INFINITY;
+          if (!sees(g + 8)) x[i][2] = x[i][3] = -INFINITY;
+          keep[i] = uint32_t(sees(2 * t)) | uint32_t(sees(2 * t + 1)) << 1 |
+                    uint32_t(sees(2 * t + 8)) << 2 | uint32_t(sees(2 * t + 9)) << 3;
+        }
+        const float a0 = fmaxf(x[i][0], x[i][2]), a1 = fmaxf(x[i][1], x[i][3]);
+        top0 = fmaxf(top0, a0);
+        top1 = fmaxf(top1, a1);
+        if constexpr (Q8) {
+          high0 = fmaxf(high0, a0 + lv[i]);
+          high1 = fmaxf(high1, a1 + lv[i]);
+        }
       }
       // ---- references
-      const float top0 = fmaxf(x0, x2), top1 = fmaxf(x1, x3);
       bool grow = top0 > m0 + kRescale || top1 > m1 + kRescale;
-      if constexpr (Q8) grow = grow || top0 + lv > w0 + kRescale || top1 + lv > w1 + kRescale;
+      if constexpr (Q8) grow = grow || high0 > w0 + kRescale || high1 > w1 + kRescale;
       if (__any_sync(0xffffffffu, grow)) {
-        float n0 = top0, n1 = top1;
+        auto all_max = [](float a) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
-          n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-        }
+          for (int off = 4; off < 32; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+          return a;
+        };
         // (a reference of -inf stands for nothing yet: the sums are zero)
         auto raise = [](float& ref, float to) {
           const float old = ref;
           ref = fmaxf(ref, to);
           return old == -INFINITY ? 0.f : dev::fast_exp2(old - ref);
         };
+        const float n0 = all_max(top0), n1 = all_max(top1);
         l0 *= raise(m0, n0);
         l1 *= raise(m1, n1);
-        float a0, a1;
-        if constexpr (Q8) {
-          a0 = raise(w0, n0 + lv);
-          a1 = raise(w1, n1 + lv);
-        } else {
-          a0 = raise(w0, n0);
-          a1 = raise(w1, n1);
-        }
+        const float a0 = raise(w0, Q8 ? all_max(high0) : n0);
+        const float a1 = raise(w1, Q8 ? all_max(high1) : n1);
 #pragma unroll
         for (int m = 0; m < S::kSteps; ++m) {
           o[m][0] *= a0;
@@ -707,40 +749,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-      float p0 = dev::fast_exp2(x0 - r0), p1 = dev::fast_exp2(x1 - r1);
-      float p2 = dev::fast_exp2(x2 - r0), p3 = dev::fast_exp2(x3 - r1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      if constexpr (Q8) {
-        // the weights carry the block's value scale: 2^(x + log2 scale), kept
-        // near 1 by a reference of their own, so f16 holds them whatever
-        // the scales are
-        const float d0 = lv - (w0 == -INFINITY ? 0.f : w0), d1 = lv - (w1 == -INFINITY ? 0.f : w1);
-        p0 = dev::fast_exp2(x0 + d0);
-        p1 = dev::fast_exp2(x1 + d1);
-        p2 = dev::fast_exp2(x2 + d0);
-        p3 = dev::fast_exp2(x3 + d1);
-      }
-      // rounded once to the tensor cores' 16-bit type; transposed so that the
-      // tokens are the contraction
-      const uint32_t b0 = dev::movmatrix_trans(Mm::pack(p0, p1));
-      const uint32_t b1 = dev::movmatrix_trans(Mm::pack(p2, p3));
-      {
-        uint32_t f[S::kSteps][4];
-        load_v<Q8, D>(vt, g, t, keep, f);
+      uint32_t b0[N], b1[N];
 #pragma unroll
-        for (int m = 0; m < S::kSteps; ++m) Mm::run(o[m], f[m][0], f[m][1], f[m][2], f[m][3], b0, b1);
+      for (int i = 0; i < N; ++i) {
+        float p0 = dev::fast_exp2(x[i][0] - r0), p1 = dev::fast_exp2(x[i][1] - r1);
+        float p2 = dev::fast_exp2(x[i][2] - r0), p3 = dev::fast_exp2(x[i][3] - r1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        if constexpr (Q8) {
+          // the weights carry the block's value scale: 2^(x + log2 scale),
+          // kept near 1 by a reference of their own, so f16 holds them
+          // whatever the scales are
+          const float d0 = lv[i] - (w0 == -INFINITY ? 0.f : w0), d1 = lv[i] - (w1 == -INFINITY ? 0.f : w1);
+          p0 = dev::fast_exp2(x[i][0] + d0);
+          p1 = dev::fast_exp2(x[i][1] + d1);
+          p2 = dev::fast_exp2(x[i][2] + d0);
+          p3 = dev::fast_exp2(x[i][3] + d1);
+        }
+        // rounded once to the tensor cores' 16-bit type; transposed so that
+        // the tokens are the contraction
+        b0[i] = dev::movmatrix_trans(Mm::pack(p0, p1));
+        b1[i] = dev::movmatrix_trans(Mm::pack(p2, p3));
       }
-      // the stage is read: its next block
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        uint32_t f[S::kSteps][4];
+        load_v<Q8, D>(kt[i] + S::kTile, g, t, keep[i], f);
+#pragma unroll
+        for (int m = 0; m < S::kSteps; ++m) Mm::run(o[m], f[m][0], f[m][1], f[m][2], f[m][3], b0[i], b1[i]);
+      }
+      v += N;
+      // the stages are read: their next blocks
       __syncwarp();
-      if (issued < count) issue();
-      if (++get == ST) {
-        get = 0;
-        parity ^= 1;
-      }
-    }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (issued < count) issue();
+      return true;
+    };
+    int left = run;
+    for (; left >= 2 && ok; left -= 2) take(std::integral_constant<int, 2>());
+    if (left && ok) take(std::integral_constant<int, 1>());
     if (!ok) break;
-    done += run;
 
     // ---- end of the segment: sums over the 8 lanes that share a head
 #pragma unroll
@@ -788,70 +837,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         piece->used = 1;
       }
     }
-    if (ends) {
-      v = 0;
-      if (++h == Hkv) {
-        h = 0;
-        ++b;
-      }
-    }
+    v = 0;
+    b = nb;
+    h = nh;
+    seq = nseq;
   }
   if (!ok) {
     // a wait ran out: let this warp's copies in flight land, then give up
-    for (int k = done; k < issued; ++k) {
+    for (int k = max(0, issued - ST); k < issued; ++k) {
       const int st = k % ST;
       dev::mbar_wait_bounded(&full[st], (k / ST) & 1, tmo, p.status);
     }
   }
+  // ---- sequences cut between the CTA's warps: the warp in which such a run
+  // of pieces begins merges it (warp 0 also the one that an earlier CTA
+  // began).  One cut between CTAs too goes to the workspace.
+  __shared__ int s_merge[2];
+  if (threadIdx.x < 2) s_merge[threadIdx.x] = -1;
   if (!__syncthreads_and(ok)) return;
-
-  // ---- pieces of sequences cut between the CTA's warps, in the line's order
-  // (each warp's first piece, then its last); those cut between CTAs too go
-  // to the workspace
-  __shared__ int s_tail[kWarps];
-  __shared__ int s_last;
-  if (lane == 0) s_tail[warp] = has_tail;
-  __syncthreads();
-  auto piece_at = [&](int k) -> Piece<D>* {
-    if (!(k & 1)) return head_pieces[k >> 1].used ? &head_pieces[k >> 1] : nullptr;
-    return s_tail[k >> 1] ? reinterpret_cast<Piece<D>*>(smem + size_t(k >> 1) * ST * S::kStage) : nullptr;
-  };
-  Piece<D>* slots = static_cast<Piece<D>*>(p.pieces) + size_t(blockIdx.x) * 2;
-  int open[2] = {-1, -1};  // (sequence, KV head) of the CTA's open ends
-  for (int k = 0; k < 2 * kWarps;) {
-    Piece<D>* first = piece_at(k);
-    if (!first) {
-      ++k;
-      continue;
-    }
+  const int span = share * kWarps;
+  auto tail_of = [&](int w) { return reinterpret_cast<Piece<D>*>(smem + size_t(w) * ST * S::kStage); };
+  // pieces: `first` of this warp, then the head pieces of warps warp + 1 .. last
+  auto merge = [&](const Piece<D>* first) {
     const int id = first->id;
-    int last = k;
-    for (int j = k + 1; j < 2 * kWarps; ++j) {
-      const Piece<D>* x = piece_at(j);
-      if (x && x->id == id) last = j;
-    }
-    const bool starts = first->starts, ends = piece_at(last)->ends;
-    Piece<D>* slot = &slots[starts ? 1 : 0];
-    for (int e = threadIdx.x; e < G * D / 4; e += kThreads) {
-      const int head = e / (D / 4), d = (e % (D / 4)) * 4;
+    const bool starts = first->starts;
+    bool ends = first->ends;
+    int last = warp;
+    while (!ends && last + 1 < kWarps && head_pieces[last + 1].used) ends = head_pieces[++last].ends;
+    Piece<D>* slot = static_cast<Piece<D>*>(p.pieces) + size_t(blockIdx.x) * 2 + (starts ? 1 : 0);
+    auto nth = [&](int j) { return j == warp ? first : &head_pieces[j]; };
+    // head i / (D / 4) of lane's float4 columns
+#pragma unroll 2
+    for (int i = lane; i < G * D / 4; i += 32) {
+      const int head = i / (D / 4), d = (i % (D / 4)) * 4;
       float m = -INFINITY, w = -INFINITY;
-      for (int j = k; j <= last; ++j)
-        if (const Piece<D>* x = piece_at(j)) {
-          m = fmaxf(m, x->m[head]);
-          w = fmaxf(w, x->w[head]);
-        }
+      for (int j = warp; j <= last; ++j) {
+        m = fmaxf(m, nth(j)->m[head]);
+        w = fmaxf(w, nth(j)->w[head]);
+      }
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f;
-      for (int j = k; j <= last; ++j)
-        if (const Piece<D>* x = piece_at(j)) {
-          const float a = x->w[head] == -INFINITY ? 0.f : dev::fast_exp2(x->w[head] - w);
-          const float4 y = *reinterpret_cast<const float4*>(&x->o[head][d]);
-          sum.x += a * y.x;
-          sum.y += a * y.y;
-          sum.z += a * y.z;
-          sum.w += a * y.w;
-          l += x->m[head] == -INFINITY ? 0.f : dev::fast_exp2(x->m[head] - m) * x->l[head];
-        }
+      for (int j = warp; j <= last; ++j) {
+        const Piece<D>* x = nth(j);
+        const float a = x->w[head] == -INFINITY ? 0.f : dev::fast_exp2(x->w[head] - w);
+        const float4 y = *reinterpret_cast<const float4*>(&x->o[head][d]);
+        sum.x += a * y.x;
+        sum.y += a * y.y;
+        sum.z += a * y.z;
+        sum.w += a * y.w;
+        l += x->m[head] == -INFINITY ? 0.f : dev::fast_exp2(x->m[head] - m) * x->l[head];
+      }
       if (starts && ends) {
         const float inv = l != 0.f ? dev::fast_exp2(Q8 ? w - m : 0.f) / l : 0.f;
         T* row = static_cast<T*>(p.out) + (size_t(id / Hkv) * p.num_q_heads + id % Hkv * G + head) * D + d;
@@ -866,27 +901,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (!(starts && ends)) open[starts ? 1 : 0] = id;
-    k = last + 1;
-  }
-
-  // ---- sequences cut between CTAs: the last to arrive merges the pieces
-  for (int side = 0; side < 2; ++side) {
-    const int id = open[side];
-    if (id < 0) continue;
-    const int4 seq = p.seqs[id / Hkv];
-    const long long f = (long long)seq.z * Hkv + (long long)(id % Hkv) * seq.y;
-    const int span = share * kWarps;
-    const int c0 = int(f / span), c1 = int((f + seq.y - 1) / span), n = c1 - c0 + 1;
+    if (starts && ends) return;
+    // the last CTA to arrive at the sequence merges its pieces
     __threadfence();
-    __syncthreads();  // every thread's part of the piece is written
-    if (threadIdx.x == 0) {
-      s_last = dev::atom_add_acq_rel_gpu(&p.arrivals[c0], 1) == n - 1;
-      if (s_last) p.arrivals[c0] = 0;  // ready for the next run
+    __syncwarp();
+    if (lane == 0) {
+      const int4 at = p.seqs[id / Hkv];
+      const long long f = (long long)at.z * Hkv + (long long)(id % Hkv) * at.y;
+      const int c0 = int(f / span), c1 = int((f + at.y - 1) / span);
+      if (dev::atom_add_acq_rel_gpu(&p.arrivals[c0], 1) == c1 - c0) {
+        p.arrivals[c0] = 0;  // ready for the next run
+        s_merge[starts ? 1 : 0] = id;
+      }
     }
-    __syncthreads();
-    if (!s_last) continue;
+  };
+  if (warp == 0 && head_pieces[0].used) merge(&head_pieces[0]);
+  if (has_tail) merge(tail_of(warp));
+  __syncthreads();
+
+  for (int side = 0; side < 2; ++side) {
+    const int id = s_merge[side];
+    if (id < 0) continue;
     __threadfence();
+    const int4 at = p.seqs[id / Hkv];
+    const long long f = (long long)at.z * Hkv + (long long)(id % Hkv) * at.y;
+    const int c0 = int(f / span), n = int((f + at.y - 1) / span) - c0 + 1;
     // piece k is CTA c0 + k's: its later end for k == 0, its earlier one else
     const Piece<D>* all = static_cast<const Piece<D>*>(p.pieces) + size_t(c0) * 2 + 1;
     auto nth = [&](int k) { return k ? all + 2 * k - 1 : all; };
