@@ -64,6 +64,7 @@ constexpr int kWarps = 8;            // warps per CTA
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 256;        // CTAs the workspace has room for
 constexpr int kMinShare = 4;         // blocks a warp takes at least
+constexpr int kFillAt = 16;          // where in its 32 blocks a warp reads the next 32's entries
 constexpr float kRescale = 8.f;      // log2 by which a score may exceed the reference
 constexpr int kPlanThreads = 1024;
 
@@ -296,7 +297,8 @@ struct Tiles {
   // merge of a sequence's pieces over CTAs, in the ring's place
   static_assert(kRing >= size_t(kMaxCtas) * kMaxGroup * 12, "merge weights");
   static_assert(size_t(kStages) * kStage >= sizeof(Piece<D>), "a warp's last piece");
-  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static_assert(kBytes + 1024 <= 227 * 1024, "shared memory");
+  static_assert(kThreads >= kMaxGroup * D / 4, "a column per thread");
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -580,10 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   int issued = 0, put = 0;  // blocks copied so far, ring stage of the next
   auto issue = [&]() {
-    if ((issued & 31) == 0) {
-      promote();
-      if (filled < count) fill();
-    }
+    if ((issued & 31) == 0) promote();
+    if ((issued & 31) == kFillAt && filled < count) fill();
     const int at = __shfl_sync(0xffffffffu, tile, issued & 31);
     uint8_t* dst = ring + put * S::kStage;
     uint64_t* bar = &full[put];
@@ -599,7 +599,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     ++issued;
     if (++put == ST) put = 0;
   };
-  if (count > 0) fill();
+  // a segment's query rows are loaded a segment ahead; the first one's before
+  // the table entries that the copies wait for
+  uint4 raw[D / 32];
+  auto fetch_q = [&](int qb, int qh) {
+    load_q<T, Q8, D>(static_cast<const T*>(p.q) + (size_t(qb) * p.num_q_heads + qh * G + g) * D, g < G, t, raw);
+  };
+  if (count > 0) {
+    fetch_q(start.x, start.y);
+    fill();
+  }
   for (int i = 0; i < ST && issued < count; ++i) issue();
 
   // ---- the warp's segments: runs of blocks of one (sequence, KV head)
@@ -611,12 +620,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   Piece<D>* tail = reinterpret_cast<Piece<D>*>(ring);
   if (lane == 0) head_pieces[warp].used = 0;
   bool has_tail = false;
-  // a segment's query rows are loaded a segment ahead
-  uint4 raw[D / 32];
-  auto fetch_q = [&](int qb, int qh) {
-    load_q<T, Q8, D>(static_cast<const T*>(p.q) + (size_t(qb) * p.num_q_heads + qh * G + g) * D, g < G, t, raw);
-  };
-  if (count > 0) fetch_q(b, h);
   while (done < count) {
     const Range range = visible_range(seq.x, p.window, p.num_sinks);
     const int run = min(seq.y - v, count - done);
@@ -849,45 +852,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       dev::mbar_wait_bounded(&full[st], (k / ST) & 1, tmo, p.status);
     }
   }
-  // ---- sequences cut between the CTA's warps: the warp in which such a run
-  // of pieces begins merges it (warp 0 also the one that an earlier CTA
-  // began).  One cut between CTAs too goes to the workspace.
-  __shared__ int s_merge[2];
-  if (threadIdx.x < 2) s_merge[threadIdx.x] = -1;
+  // ---- sequences cut between the CTA's warps: their pieces lie in a run of
+  // warps (a last piece, or for one that an earlier CTA began the first
+  // warp's, then first pieces), each of which merges a slice of the columns.
+  // One cut between CTAs too goes to the workspace.
+  __shared__ int s_tail[kWarps], s_open[2], s_merge[2];
+  if (lane == 0) s_tail[warp] = has_tail;
+  if (threadIdx.x < 2) s_open[threadIdx.x] = s_merge[threadIdx.x] = -1;
   if (!__syncthreads_and(ok)) return;
-  const int span = share * kWarps;
-  auto tail_of = [&](int w) { return reinterpret_cast<Piece<D>*>(smem + size_t(w) * ST * S::kStage); };
-  // pieces: `first` of this warp, then the head pieces of warps warp + 1 .. last
-  auto merge = [&](const Piece<D>* first) {
+  auto merge = [&](int from, bool from_tail) {
+    const Piece<D>* first =
+        from_tail ? reinterpret_cast<const Piece<D>*>(smem + size_t(from) * ST * S::kStage) : &head_pieces[from];
     const int id = first->id;
-    const bool starts = first->starts;
     bool ends = first->ends;
-    int last = warp;
+    int last = from;
     while (!ends && last + 1 < kWarps && head_pieces[last + 1].used) ends = head_pieces[++last].ends;
-    Piece<D>* slot = static_cast<Piece<D>*>(p.pieces) + size_t(blockIdx.x) * 2 + (starts ? 1 : 0);
-    auto nth = [&](int j) { return j == warp ? first : &head_pieces[j]; };
-    // head i / (D / 4) of lane's float4 columns
-#pragma unroll 2
-    for (int i = lane; i < G * D / 4; i += 32) {
+    const bool whole = from_tail && ends;
+    Piece<D>* slot = static_cast<Piece<D>*>(p.pieces) + size_t(blockIdx.x) * 2 + (from_tail ? 1 : 0);
+    const int n = last - from + 1;
+    for (int i = (warp - from) * 32 + lane; i < G * D / 4; i += 32 * n) {
       const int head = i / (D / 4), d = (i % (D / 4)) * 4;
-      float m = -INFINITY, w = -INFINITY;
-      for (int j = warp; j <= last; ++j) {
-        m = fmaxf(m, nth(j)->m[head]);
-        w = fmaxf(w, nth(j)->w[head]);
+      // (at most one piece per warp: every load in flight at once)
+      float pm[kWarps], pw[kWarps], pl[kWarps], m = -INFINITY, w = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        const Piece<D>* x = j ? &head_pieces[min(from + j, kWarps - 1)] : first;
+        pm[j] = j < n ? x->m[head] : -INFINITY;
+        pw[j] = j < n ? x->w[head] : -INFINITY;
+        pl[j] = j < n ? x->l[head] : 0.f;
+        m = fmaxf(m, pm[j]);
+        w = fmaxf(w, pw[j]);
       }
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f;
-      for (int j = warp; j <= last; ++j) {
-        const Piece<D>* x = nth(j);
-        const float a = x->w[head] == -INFINITY ? 0.f : dev::fast_exp2(x->w[head] - w);
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        if (j >= n) break;
+        const Piece<D>* x = j ? &head_pieces[min(from + j, kWarps - 1)] : first;
+        const float a = pw[j] == -INFINITY ? 0.f : dev::fast_exp2(pw[j] - w);
         const float4 y = *reinterpret_cast<const float4*>(&x->o[head][d]);
         sum.x += a * y.x;
         sum.y += a * y.y;
         sum.z += a * y.z;
         sum.w += a * y.w;
-        l += x->m[head] == -INFINITY ? 0.f : dev::fast_exp2(x->m[head] - m) * x->l[head];
+        l += pm[j] == -INFINITY ? 0.f : dev::fast_exp2(pm[j] - m) * pl[j];
       }
-      if (starts && ends) {
+      if (whole) {
         const float inv = l != 0.f ? dev::fast_exp2(Q8 ? w - m : 0.f) / l : 0.f;
         T* row = static_cast<T*>(p.out) + (size_t(id / Hkv) * p.num_q_heads + id % Hkv * G + head) * D + d;
         *reinterpret_cast<uint2*>(row) = make_uint2(dev::Mma<T>::pack(sum.x * inv, sum.y * inv),
@@ -901,38 +911,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (starts && ends) return;
-    // the last CTA to arrive at the sequence merges its pieces
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) {
-      const int4 at = p.seqs[id / Hkv];
-      const long long f = (long long)at.z * Hkv + (long long)(id % Hkv) * at.y;
-      const int c0 = int(f / span), c1 = int((f + at.y - 1) / span);
-      if (dev::atom_add_acq_rel_gpu(&p.arrivals[c0], 1) == c1 - c0) {
-        p.arrivals[c0] = 0;  // ready for the next run
-        s_merge[starts ? 1 : 0] = id;
-      }
-    }
+    if (!whole && warp == from && lane == 0) s_open[from_tail ? 1 : 0] = id;
   };
-  if (warp == 0 && head_pieces[0].used) merge(&head_pieces[0]);
-  if (has_tail) merge(tail_of(warp));
+  if (head_pieces[warp].used) {
+    int from = warp;
+    bool from_tail = false;
+    while (from > 0 && !from_tail) from_tail = s_tail[--from];
+    merge(from, from_tail);
+  }
+  if (has_tail) merge(warp, true);
   __syncthreads();
 
+  // ---- the last CTA to arrive at a sequence cut between CTAs merges it
+  const int span = share * kWarps;
+  auto first_cta = [&](int id, int& n) {
+    const int4 at = p.seqs[id / Hkv];
+    const long long f = (long long)at.z * Hkv + (long long)(id % Hkv) * at.y;
+    const int c0 = int(f / span);
+    n = int((f + at.y - 1) / span) - c0 + 1;
+    return c0;
+  };
+  const int open0 = s_open[0], open1 = s_open[1];
+  if (open0 < 0 && open1 < 0) return;
+  if (lane == 0 && warp < 2) {
+    const int id = warp ? open1 : open0;
+    int n;
+    if (id >= 0) {
+      const int c0 = first_cta(id, n);
+      if (dev::atom_add_acq_rel_gpu(&p.arrivals[c0], 1) == n - 1) {
+        p.arrivals[c0] = 0;  // ready for the next run
+        s_merge[warp] = id;
+      }
+    }
+  }
+  __syncthreads();
   for (int side = 0; side < 2; ++side) {
     const int id = s_merge[side];
     if (id < 0) continue;
-    __threadfence();
-    const int4 at = p.seqs[id / Hkv];
-    const long long f = (long long)at.z * Hkv + (long long)(id % Hkv) * at.y;
-    const int c0 = int(f / span), n = int((f + at.y - 1) / span) - c0 + 1;
+    int n;
+    const int c0 = first_cta(id, n);
     // piece k is CTA c0 + k's: its later end for k == 0, its earlier one else
     const Piece<D>* all = static_cast<const Piece<D>*>(p.pieces) + size_t(c0) * 2 + 1;
     auto nth = [&](int k) { return k ? all + 2 * k - 1 : all; };
     float* wsm = reinterpret_cast<float*>(smem);  // [n][8] weights
+    // the columns' first pieces are on their way while the weights are made
+    const int head = threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
+    const bool mine = threadIdx.x < G * D / 4;  // kThreads >= 8 D / 4
+    constexpr int kAhead = 4;
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (mine && k < n) ahead[k] = __ldcg(reinterpret_cast<const float4*>(&nth(k)->o[head][d]));
     if (warp < G) {  // one warp per head
-      float m = -INFINITY, w = -INFINITY;
-      for (int k = lane; k < n; k += 32) {
+      float m = -INFINITY, w = -INFINITY, l = 0.f;
+      float pm = -INFINITY, pw = -INFINITY, pl = 0.f;  // piece `lane`'s
+      if (lane < n) {
+        pm = __ldcg(&nth(lane)->m[warp]);
+        pw = __ldcg(&nth(lane)->w[warp]);
+        pl = __ldcg(&nth(lane)->l[warp]);
+        m = pm;
+        w = pw;
+      }
+      for (int k = lane + 32; k < n; k += 32) {
         m = fmaxf(m, __ldcg(&nth(k)->m[warp]));
         w = fmaxf(w, __ldcg(&nth(k)->w[warp]));
       }
@@ -941,32 +981,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, off));
       }
-      float l = 0.f;
-      for (int k = lane; k < n; k += 32) {
+      l = pm == -INFINITY ? 0.f : dev::fast_exp2(pm - m) * pl;
+      for (int k = lane + 32; k < n; k += 32) {
         const float x = __ldcg(&nth(k)->m[warp]);
         l += x == -INFINITY ? 0.f : dev::fast_exp2(x - m) * __ldcg(&nth(k)->l[warp]);
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
       const float inv = l != 0.f ? dev::fast_exp2(Q8 ? w - m : 0.f) / l : 0.f;
-      for (int k = lane; k < n; k += 32) {
+      if (lane < n) wsm[lane * kMaxGroup + warp] = pw == -INFINITY ? 0.f : dev::fast_exp2(pw - w) * inv;
+      for (int k = lane + 32; k < n; k += 32) {
         const float x = __ldcg(&nth(k)->w[warp]);
         wsm[k * kMaxGroup + warp] = x == -INFINITY ? 0.f : dev::fast_exp2(x - w) * inv;
       }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < G * D / 4; e += kThreads) {
-      const int head = e / (D / 4), d = (e % (D / 4)) * 4;
+    if (mine) {
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) {
+      auto add = [&](int k, const float4& y) {
         const float a = wsm[k * kMaxGroup + head];
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(&nth(k)->o[head][d]));
         sum.x += a * y.x;
         sum.y += a * y.y;
         sum.z += a * y.z;
         sum.w += a * y.w;
-      }
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k < n) add(k, ahead[k]);
+#pragma unroll 8
+      for (int k = kAhead; k < n; ++k) add(k, __ldcg(reinterpret_cast<const float4*>(&nth(k)->o[head][d])));
       T* row = static_cast<T*>(p.out) + (size_t(id / Hkv) * p.num_q_heads + id % Hkv * G + head) * D + d;
       *reinterpret_cast<uint2*>(row) =
           make_uint2(dev::Mma<T>::pack(sum.x, sum.y), dev::Mma<T>::pack(sum.z, sum.w));
