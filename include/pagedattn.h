@@ -480,7 +480,7 @@ PA_API int pa_paged_attention_prefill_run(const void* q, const void* k_cache, co
  * returns PA_ERR_INVALID_ARG).  The workspace
  * (pa_paged_attention_decode_window_workspace_size bytes, 256-byte aligned)
  * belongs to one call at a time and needs no initialisation.
- * num_seqs * num_kv_heads * max_blocks_per_seq must stay below 2^31.
+ * num_seqs * num_kv_heads * (max_blocks_per_seq + 32) must stay below 2^31.
  * ---------------------------------------------------------------------- */
 PA_API int pa_paged_attention_decode_window_workspace_size(int num_seqs, int num_q_heads,
                                                            int num_kv_heads, int head_dim,
