@@ -1347,29 +1347,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         float mx = dev::fmax3(dev::fmax3(m8[0], m8[1], m8[2]), dev::fmax3(m8[3], m8[4], m8[5]),
                               fmaxf(m8[6], m8[7])) * sl2;
-        if (mx > mref + kTcRescale) {  // also the row's first unmasked column
-          if (mref != -INFINITY) {
-            // O_w holds every earlier tile once the previous P V has finished
-            // (with two query tiles S_w was issued only after it; one tile's
-            // S runs ahead, so wait for it): rescale it in TMEM
-            if (!wait_prev_pv()) {
-              ok = false;
-              break;
-            }
-            const float a = dev::fast_exp2(mref - mx);
-            l *= a;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t ov[32];
-              dev::tmem_ld32(t_o + 32 * c, ov);
-              dev::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * a);
-              dev::tmem_st32(t_o + 32 * c, ov);
-            }
+        // also the row's first unmasked column.  The tensor-memory accesses are
+        // the whole warp's: it rescales when one of its rows does (the others
+        // by 1).
+        const bool raise = mx > mref + kTcRescale;
+        const bool rescale = raise && mref != -INFINITY;
+        if (__any_sync(0xffffffffu, rescale)) {
+          // O_w holds every earlier tile once the previous P V has finished
+          // (with two query tiles S_w was issued only after it; one tile's
+          // S runs ahead, so wait for it): rescale it in TMEM
+          if (!wait_prev_pv()) {
+            ok = false;
+            break;
           }
-          mref = mx;
+          __syncwarp();
+          const float a = rescale ? dev::fast_exp2(mref - mx) : 1.f;
+          l *= a;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t ov[32];
+            dev::tmem_ld32(t_o + 32 * c, ov);
+            dev::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * a);
+            dev::tmem_st32(t_o + 32 * c, ov);
+          }
         }
+        if (raise) mref = mx;
         // P = 2^(s scale log2 e - ref) in the input type, over S's first 64
         // columns; masked columns (-inf) give 0.  A row with nothing visible
         // yet (ref -inf) uses 0 as its reference: every p is 0 then.
