@@ -165,14 +165,37 @@ inline int signature_of(int num_seqs, int total_q, int num_q_heads, int num_kv_h
 // A query block qb of sequence b covers rows qb*64 .. of the sequence's
 // T_b * G rows; its last row's token sits at position ctx - T_b + i_last,
 // so it needs KV blocks 0 .. that position / 16.
+// With a window its rows see, between them, the first tokens and the tokens
+// from its first row's window on: blocks 0 .. first - 1 and first + skip ..;
+// a unit counts those without a gap ("virtual" blocks), so a token's virtual
+// index is its own, less 16 skip behind the gap.
+struct WindowRange {
+  int low;    // first token inside some row's window
+  int first;  // blocks of first tokens before the gap (no gap: all of them)
+  int skip;   // blocks in the gap
+};
+
+template <int ROWS>
+__device__ __forceinline__ WindowRange window_range(int ctx, int qlen, int group, int qb,
+                                                    int window, int num_sinks) {
+  WindowRange r;
+  r.low = max(0, ctx - qlen + qb * ROWS / group - window + 1);
+  const int sink_blocks = (min(num_sinks, r.low) + kBlockSize - 1) / kBlockSize;
+  const int low_block = r.low / kBlockSize;
+  r.first = sink_blocks < low_block ? sink_blocks : 0x7FFFFFFF;
+  r.skip = sink_blocks < low_block ? low_block - sink_blocks : 0;
+  return r;
+}
+
 template <int ROWS = kRows>
-__device__ __forceinline__ int qblock_blocks(int ctx, int qlen, int group, int qb,
-                                             bool all_tokens = false) {
+__device__ __forceinline__ int qblock_blocks(int ctx, int qlen, int group, int qb, bool all_tokens,
+                                             int window, int num_sinks) {
   if (all_tokens) return (ctx + kBlockSize - 1) / kBlockSize;
   const int rows = qlen * group;
   const int last_row = min((qb + 1) * ROWS, rows) - 1;
   const int pos = ctx - qlen + last_row / group;
-  return pos / kBlockSize + 1;
+  const int blocks = pos / kBlockSize + 1;
+  return window ? blocks - window_range<ROWS>(ctx, qlen, group, qb, window, num_sinks).skip : blocks;
 }
 
 __device__ __forceinline__ int size_bucket(int n) { return 31 - __clz(n); }  // floor(log2 n)
@@ -237,7 +260,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Params
     chunk(b, ctx, qlen);
     const int nq = (qlen * G + ROWS - 1) / ROWS;
     unsigned long long blocks = 0;
-    for (int qb = 0; qb < nq; ++qb) blocks += qblock_blocks<ROWS>(ctx, qlen, G, qb, shared);
+    for (int qb = 0; qb < nq; ++qb) blocks += qblock_blocks<ROWS>(ctx, qlen, G, qb, shared, p.window, p.num_sinks);
     if (nq) {
       atomicAdd(&s_qblocks, nq);
       atomicAdd(&s_blocks, blocks);
@@ -290,7 +313,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Params
       const int nq = (qlen * G + ROWS - 1) / ROWS;
       int units = 0;
       for (int qb = 0; qb < nq; ++qb) {
-        const int ns = nsplits_of(qblock_blocks<ROWS>(ctx, qlen, G, qb, shared), split);
+        const int ns = nsplits_of(qblock_blocks<ROWS>(ctx, qlen, G, qb, shared, p.window, p.num_sinks), split);
         if (ns > 1 && !p.defer_merge) units += ns * (ROWS / kRows);  // partial slots of kRows rows
       }
       if (units) atomicAdd(&s_split_units, units);
@@ -318,7 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Params
     count = 0;
     largest = 0;
     for (int qb = 0; qb < nq; ++qb) {
-      const int nb = qblock_blocks<ROWS>(ctx, qlen, G, qb, shared);
+      const int nb = qblock_blocks<ROWS>(ctx, qlen, G, qb, shared, p.window, p.num_sinks);
       const int ns = nsplits_of(nb, split);
       count += ns;
       largest = max(largest, (nb + ns - 1) / ns);
@@ -357,7 +380,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const Params
     chunk(b, ctx, qlen);
     const int nq = (qlen * G + ROWS - 1) / ROWS;
     for (int qb = nq - 1; qb >= 0; --qb) {
-      const int nb = qblock_blocks<ROWS>(ctx, qlen, G, qb, shared);
+      const int nb = qblock_blocks<ROWS>(ctx, qlen, G, qb, shared, p.window, p.num_sinks);
       const int ns = nsplits_of(nb, split);
       const int base = nb / ns, big = nb - base * ns;
       int slot = -1, grp = -1;
@@ -391,9 +414,11 @@ struct Smem {
 struct Item {
   int b, qb, first, nblk, s, ns, slot, grp, ctx, g;
   int q_first, qlen;
+  WindowRange win;
 };
 
-template <typename T, int D>
+// WIN: with a sliding window (p.window > 0).
+template <typename T, int D, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32, 3)
     prefill_kernel(const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const Params p) {
@@ -447,9 +472,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   auto issue = [&](const Item& it, int j, int k) -> bool {
     if ((j & ~31) != tbl_base) {
       tbl_base = j & ~31;
+      const int at = it.first + tbl_base + lane;
       tbl = tbl_base + lane < it.nblk
-                ? p.block_tables[size_t(shared ? it.q_first : it.b) * p.max_blocks + it.first +
-                                 tbl_base + lane]
+                ? p.block_tables[size_t(shared ? it.q_first : it.b) * p.max_blocks + at +
+                                 (WIN && at >= it.win.first ? it.win.skip : 0)]
                 : 0;
       if (tbl < 0 || tbl >= p.num_blocks) {
         dev::flag_status(p.status, kStatusBounds);
@@ -508,6 +534,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       const bool starts = !shared || p.shared_blocks;
       it.q_first = starts ? p.query_start[it.b] : 0;
       it.qlen = starts ? p.query_start[it.b + 1] - it.q_first : p.total_q;
+      if (WIN) it.win = window_range<kRows>(it.ctx, it.qlen, G, it.qb, p.window, p.num_sinks);
     }
     // the ring's first blocks of this item
     tbl_base = -32;
@@ -523,6 +550,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const bool va = ra < nrows, vb = rb < nrows;
     const int pos_a = va ? (shared ? it.ctx - 1 : it.ctx - it.qlen + ra / G) : -1;
     const int pos_b = vb ? (shared ? it.ctx - 1 : it.ctx - it.qlen + rb / G) : -1;
+    // (virtual tokens, as below)
+    const int gap = WIN ? it.win.skip * kBlockSize : 0;
+    const int end_a = pos_a - gap, end_b = pos_b - gap;
+    const int low_a = end_a - p.window + 1, low_b = end_b - p.window + 1;
     const T* qa = static_cast<const T*>(p.q) +
                   (size_t(it.q_first + (va ? ra / G : 0)) * Hq + it.g * G + (va ? ra % G : 0)) * D;
     const T* qbp = static_cast<const T*>(p.q) +
@@ -578,14 +609,17 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       // ---- causal / context mask, base-2 scores
       const int c0 = t0 + 2 * tq, c1 = c0 + 8;  // tokens of s0[0], s1[0]
       float xa[4], xb[4];
-      xa[0] = c0 <= pos_a ? s0[0] * sl2 : -INFINITY;
-      xa[1] = c0 + 1 <= pos_a ? s0[1] * sl2 : -INFINITY;
-      xa[2] = c1 <= pos_a ? s1[0] * sl2 : -INFINITY;
-      xa[3] = c1 + 1 <= pos_a ? s1[1] * sl2 : -INFINITY;
-      xb[0] = c0 <= pos_b ? s0[2] * sl2 : -INFINITY;
-      xb[1] = c0 + 1 <= pos_b ? s0[3] * sl2 : -INFINITY;
-      xb[2] = c1 <= pos_b ? s1[2] * sl2 : -INFINITY;
-      xb[3] = c1 + 1 <= pos_b ? s1[3] * sl2 : -INFINITY;
+      // (a window: from the row's first token in it on, or a first token)
+      auto see_a = [&](int c) { return c <= end_a && (!WIN || c >= low_a || c < p.num_sinks); };
+      auto see_b = [&](int c) { return c <= end_b && (!WIN || c >= low_b || c < p.num_sinks); };
+      xa[0] = see_a(c0) ? s0[0] * sl2 : -INFINITY;
+      xa[1] = see_a(c0 + 1) ? s0[1] * sl2 : -INFINITY;
+      xa[2] = see_a(c1) ? s1[0] * sl2 : -INFINITY;
+      xa[3] = see_a(c1 + 1) ? s1[1] * sl2 : -INFINITY;
+      xb[0] = see_b(c0) ? s0[2] * sl2 : -INFINITY;
+      xb[1] = see_b(c0 + 1) ? s0[3] * sl2 : -INFINITY;
+      xb[2] = see_b(c1) ? s1[2] * sl2 : -INFINITY;
+      xb[3] = see_b(c1 + 1) ? s1[3] * sl2 : -INFINITY;
       float bma = fmaxf(fmaxf(xa[0], xa[1]), fmaxf(xa[2], xa[3]));
       float bmb = fmaxf(fmaxf(xb[0], xb[1]), fmaxf(xb[2], xb[3]));
       bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 1));
@@ -619,6 +653,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       {
         const int mi = lane >> 3;
         const int tok = ((mi & 1) << 3) + (lane & 7);
+        // V of tokens that no row of the item sees (b0, b2: tokens c0, c0 + 1,
+        // b1, b3: c1, c1 + 1) reads as 0, whatever it is
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        const bool hides = WIN && (t0 + kBlockSize > it.ctx - gap ||
+                                   (t0 < it.win.low - gap && t0 + kBlockSize > p.num_sinks));
+        if (hides) {
+          auto half = [&](int c) {
+            return c < it.ctx - gap && (c >= it.win.low - gap || c < p.num_sinks) ? 0xffffu : 0u;
+          };
+          keep0 = half(c0) | half(c0 + 1) << 16;
+          keep1 = half(c1) | half(c1 + 1) << 16;
+        }
 #pragma unroll
         for (int nd = 0; nd < ND; nd += 2) {
           const int gc = nd + (mi >> 1);  // 16-byte chunk = 8 columns
@@ -626,6 +672,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
               vt + (gc >> 3) * 2048 + tok * 128 + ((((gc & 7) ^ (tok & 7))) << 4);
           uint32_t b0, b1, b2, b3;
           dev::ldmatrix_x4_trans(addr, b0, b1, b2, b3);
+          if (hides) {
+            b0 &= keep0;
+            b1 &= keep1;
+            b2 &= keep0;
+            b3 &= keep1;
+          }
           M::run(o[nd], pa01, pb01, pa23, pb23, b0, b1);
           M::run(o[nd + 1], pa01, pb01, pa23, pb23, b2, b3);
         }
@@ -897,7 +949,7 @@ struct TcSmem {  // head_dim 128, 16-bit: every chunk is [128 rows][128 bytes]
 };
 static_assert(TcSmem::kBytes <= 227 * 1024, "tcgen05 prefill shared memory");
 
-template <typename T>
+template <typename T, bool WIN>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_k,
@@ -982,6 +1034,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   struct Item {
     int b, qt, first, nblk, ctx, q_first, qlen, g, ntiles, s, ns, slot, grp;
     bool two;  // the second query tile holds valid rows
+    WindowRange win;
   };
   auto decode = [&](int x) {
     Item it;
@@ -1003,6 +1056,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     it.qlen = starts ? p.query_start[it.b + 1] - it.q_first : p.total_q;
     it.ntiles = (it.nblk + kTcBlocks - 1) / kTcBlocks;
     it.two = it.qt * kTcItemRows + kTcRows < it.qlen * G;
+    if (WIN) it.win = window_range<kTcItemRows>(it.ctx, it.qlen, G, it.qt, p.window, p.num_sinks);
     return it;
   };
 
@@ -1059,9 +1113,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int nb = min(kTcBlocks, it.nblk - j * kTcBlocks);
         if ((j * kTcBlocks & ~31) != tbl_base) {
           tbl_base = j * kTcBlocks & ~31;
+          const int at = it.first + tbl_base + lane;
           tbl = tbl_base + lane < it.nblk
-                    ? p.block_tables[size_t(shared ? it.q_first : it.b) * p.max_blocks + it.first +
-                                 tbl_base + lane]
+                    ? p.block_tables[size_t(shared ? it.q_first : it.b) * p.max_blocks + at +
+                                     (WIN && at >= it.win.first ? it.win.skip : 0)]
                     : 0;
           if (tbl < 0 || tbl >= p.num_blocks) {
             dev::flag_status(p.status, kStatusBounds);
@@ -1288,10 +1343,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool valid = gr < it.qlen * G;
       // tokens past the context or past the item's blocks (a split's last
       // tile) are never read into the result
-      const int bound = min(it.ctx, (it.first + it.nblk) * kBlockSize);
+      // (with a window, here and below: virtual tokens)
+      const int gap = WIN ? it.win.skip * kBlockSize : 0;
+      const int bound = min(it.ctx - gap, (it.first + it.nblk) * kBlockSize);
       // the row's last visible token: causal within the chunk; in
       // shared-prefix mode every row sees the (item's part of the) prefix
-      const int pos = valid ? min(shared ? it.ctx - 1 : it.ctx - it.qlen + gr / G, bound - 1) : -1;
+      const int own = shared ? it.ctx - 1 : it.ctx - it.qlen + gr / G - gap;
+      const int pos = valid ? min(own, bound - 1) : -1;
+      // a window: the row sees tokens low .. pos and the first num_sinks; no
+      // row of the item sees tokens num_sinks .. none - 1
+      const int low = WIN ? own - p.window + 1 : 0, none = WIN ? it.win.low - gap : 0;
       float mref = -INFINITY, l = 0.f;
       for (int j = 0; j < it.ntiles && ok; ++j, ++cnt) {
         // this tile's S buffer: the group's own, or (one query tile) the
@@ -1320,6 +1381,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (t0 + 32 * c + i > pos) sv[c][i] = __float_as_uint(-INFINITY);
+        }
+        if (WIN && t0 < low && t0 + kTcTokens > p.num_sinks) {
+          // columns before the row's window, past the first tokens
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (t0 + 32 * c + i < low && t0 + 32 * c + i >= p.num_sinks)
+                sv[c][i] = __float_as_uint(-INFINITY);
         }
         // One query tile: this tile's S did not wait for the previous P V.
         // Wait for it before touching O_w or announcing P, so that at most
@@ -1400,11 +1470,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         dev::tmem_st32(t_s, sv[0]);
         dev::tmem_st32(t_s + 32, sv[1]);
-        if (w == 0 && t0 + kTcTokens > bound) {
+        if (w == 0 && (t0 + kTcTokens > bound || (WIN && t0 < none && t0 + kTcTokens > p.num_sinks))) {
           // rows of the last V tile past the context or past the loaded
-          // blocks are zeroed, so whatever bits they hold meet only p = 0
+          // blocks (and those before every row's window) are zeroed, so
+          // whatever bits they hold meet only p = 0
           if (!dev::mbar_wait_bounded(&v_full[kt & 1], (kt >> 1) & 1, tmo, p.status)) ok = false;
-          if (ok && t0 + r >= bound) {
+          if (ok && (t0 + r >= bound || (WIN && t0 + r < none && t0 + r >= p.num_sinks))) {
             // (each row's 16-byte chunks in an order rotated by the row, so
             // the warp's 32 rows, 128 bytes apart, do not all hit one bank)
             uint8_t* vrow = smem + TcSmem::kV + (kt & 1) * 2 * TcSmem::kChunk + r * 128;
@@ -1615,15 +1686,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // --------------------------------------------------------------- fp32 path
 // One warp per (query row, query head): a decode over the tokens the row sees.
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void narrow(float& y, float x) { y = x; }
-__device__ __forceinline__ void narrow(__half& y, float x) { y = __float2half_rn(x); }
-__device__ __forceinline__ void narrow(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
-
-template <typename T, int D>
-__global__ void __launch_bounds__(128) prefill_simple_kernel(const Params p) {
+template <int D>
+__global__ void __launch_bounds__(128) prefill_f32_kernel(const Params p) {
   constexpr int E = D / 32;
   const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -1647,14 +1711,14 @@ __global__ void __launch_bounds__(128) prefill_simple_kernel(const Params p) {
   }
   const int pos = ctx - qlen + (row - p.query_start[b]);
   const int g = h / p.group;
-  const T* qv = static_cast<const T*>(p.q) + (size_t(row) * p.num_q_heads + h) * D + lane * E;
-  const T* k_cache = static_cast<const T*>(p.k_cache);
-  const T* v_cache = static_cast<const T*>(p.v_cache);
+  const float* qv = static_cast<const float*>(p.q) + (size_t(row) * p.num_q_heads + h) * D + lane * E;
+  const float* k_cache = static_cast<const float*>(p.k_cache);
+  const float* v_cache = static_cast<const float*>(p.v_cache);
   const int32_t* table = p.block_tables + size_t(b) * p.max_blocks;
   float qr[E], acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    qr[e] = widen(qv[e]);
+    qr[e] = qv[e];
     acc[e] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
@@ -1670,7 +1734,7 @@ __global__ void __launch_bounds__(128) prefill_simple_kernel(const Params p) {
     const size_t r = ((size_t(phys) * p.num_kv_heads + g) * kBlockSize + t % kBlockSize) * D + lane * E;
     float dot = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) dot = fmaf(qr[e], widen(k_cache[r + e]), dot);
+    for (int e = 0; e < E; ++e) dot = fmaf(qr[e], k_cache[r + e], dot);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     const float sc = dot * p.scale;
@@ -1678,12 +1742,12 @@ __global__ void __launch_bounds__(128) prefill_simple_kernel(const Params p) {
     const float a = expf(m - mn), pw = expf(sc - mn);
     l = l * a + pw;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + pw * widen(v_cache[r + e]);
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + pw * v_cache[r + e];
     m = mn;
   }
-  T* out = static_cast<T*>(p.out) + (size_t(row) * p.num_q_heads + h) * D + lane * E;
+  float* out = static_cast<float*>(p.out) + (size_t(row) * p.num_q_heads + h) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) narrow(out[e], acc[e] / l);
+  for (int e = 0; e < E; ++e) out[e] = acc[e] / l;
 }
 
 }  // namespace prefill
@@ -1700,7 +1764,7 @@ struct DeviceState {
   std::once_flag once;
   int error = 0;
   int sms = 0;
-  int ctas_per_sm[2][2] = {{0, 0}, {0, 0}};  // [bf16?][head_dim 128?]
+  int ctas_per_sm[2][2][2] = {};             // [window?][bf16?][head_dim 128?]
   bool tc_ok = false;                        // tcgen05 kernel configured
 };
 
@@ -1716,14 +1780,20 @@ bool tc_wanted() {
 }
 DeviceState g_dev[kMaxDevices];
 
-template <typename T, int D>
+template <typename T, int D, bool WIN>
 cudaError_t configure(int* ctas_per_sm) {
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T, D>,
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T, D, WIN>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(Smem<D>::kBytes));
   if (e != cudaSuccess) return e;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, prefill_kernel<T, D>,
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, prefill_kernel<T, D, WIN>,
                                                        kWarps * 32, Smem<D>::kBytes);
+}
+
+template <typename T, bool WIN>
+bool configure_tc() {
+  return cudaFuncSetAttribute(prefill_tc_kernel<T, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              TcSmem::kBytes) == cudaSuccess;
 }
 
 int device_setup(int device) {
@@ -1733,21 +1803,22 @@ int device_setup(int device) {
       st.error = PA_ERR_CUDA;
       return;
     }
-    cudaError_t e = configure<__nv_bfloat16, 128>(&st.ctas_per_sm[1][1]);
-    if (e == cudaSuccess) e = configure<__nv_bfloat16, 64>(&st.ctas_per_sm[1][0]);
-    if (e == cudaSuccess) e = configure<__half, 128>(&st.ctas_per_sm[0][1]);
-    if (e == cudaSuccess) e = configure<__half, 64>(&st.ctas_per_sm[0][0]);
+    cudaError_t e = cudaSuccess;
+    auto& n = st.ctas_per_sm;
+    if (e == cudaSuccess) e = configure<__nv_bfloat16, 128, false>(&n[0][1][1]);
+    if (e == cudaSuccess) e = configure<__nv_bfloat16, 64, false>(&n[0][1][0]);
+    if (e == cudaSuccess) e = configure<__half, 128, false>(&n[0][0][1]);
+    if (e == cudaSuccess) e = configure<__half, 64, false>(&n[0][0][0]);
+    if (e == cudaSuccess) e = configure<__nv_bfloat16, 128, true>(&n[1][1][1]);
+    if (e == cudaSuccess) e = configure<__nv_bfloat16, 64, true>(&n[1][1][0]);
+    if (e == cudaSuccess) e = configure<__half, 128, true>(&n[1][0][1]);
+    if (e == cudaSuccess) e = configure<__half, 64, true>(&n[1][0][0]);
     st.error = e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-    for (int a = 0; a < 2; ++a)
-      for (int d = 0; d < 2; ++d)
-        if (st.error == PA_OK && st.ctas_per_sm[a][d] < 1) st.error = PA_ERR_UNSUPPORTED;
+    for (int i = 0; i < 8; ++i)
+      if (st.error == PA_OK && n[i >> 2][i >> 1 & 1][i & 1] < 1) st.error = PA_ERR_UNSUPPORTED;
     if (st.error == PA_OK) {
-      st.tc_ok = cudaFuncSetAttribute(prefill_tc_kernel<__nv_bfloat16>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      TcSmem::kBytes) == cudaSuccess &&
-                 cudaFuncSetAttribute(prefill_tc_kernel<__half>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      TcSmem::kBytes) == cudaSuccess;
+      st.tc_ok = configure_tc<__nv_bfloat16, false>() && configure_tc<__half, false>() &&
+                 configure_tc<__nv_bfloat16, true>() && configure_tc<__half, true>();
       cudaGetLastError();
     }
   });
@@ -1886,19 +1957,15 @@ int prefill_entry(Mode mode, int window, int num_sinks, const void* q, const voi
   prm.status = status;
   prm.timeout_ns = 1000000000ull;
 
-  if (dtype == PA_F32 || window > 0) {
+  if (dtype == PA_F32) {
     // one warp per (row, head) needs no plan
     if (!runs) return PA_OK;
     const long long units = (long long)total_q * num_q_heads;
     const int blocks = int((units + 3) / 4);
-    auto launch = [&](auto* kernel) { kernel<<<blocks, 128, 0, s>>>(prm); };
-    if (dtype == PA_F32)
-      launch(head_dim == 64 ? prefill_simple_kernel<float, 64> : prefill_simple_kernel<float, 128>);
-    else if (dtype == PA_F16)
-      launch(head_dim == 64 ? prefill_simple_kernel<__half, 64> : prefill_simple_kernel<__half, 128>);
+    if (head_dim == 64)
+      prefill_f32_kernel<64><<<blocks, 128, 0, s>>>(prm);
     else
-      launch(head_dim == 64 ? prefill_simple_kernel<__nv_bfloat16, 64>
-                            : prefill_simple_kernel<__nv_bfloat16, 128>);
+      prefill_f32_kernel<128><<<blocks, 128, 0, s>>>(prm);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s (fp32): launch failed: %s", who, cudaGetErrorString(e));
     return PA_OK;
@@ -2014,7 +2081,7 @@ namespace {
 bool prepare(Params& prm, const Layout& lay, int device, int dtype, void* workspace) {
   const DeviceState& st = g_dev[device];
   const bool bf16 = dtype == PA_BF16;
-  const int per_sm = st.ctas_per_sm[bf16][prm.head_dim == 128];
+  const int per_sm = st.ctas_per_sm[prm.window > 0][bf16][prm.head_dim == 128];
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int G = prm.num_q_heads / prm.num_kv_heads;
   const bool use_tc = tc_wanted() && st.tc_ok && prm.head_dim == 128 && prm.scale_log2 > 0.f &&
@@ -2029,7 +2096,9 @@ bool prepare(Params& prm, const Layout& lay, int device, int dtype, void* worksp
   prm.signature = signature_of(prm.num_seqs, prm.total_q, prm.num_q_heads, prm.num_kv_heads,
                                prm.head_dim, prm.max_blocks) ^
                   (prm.shared_ctx << 1) ^ (use_tc ? 0x2A000000 : 0) ^
-                  (prm.shared_blocks ? 0x15000000 : 0);
+                  (prm.shared_blocks ? 0x15000000 : 0) ^
+                  (prm.window ? int(uint32_t(prm.window) * 0x9E3779B1u ^
+                                    uint32_t(prm.num_sinks) * 0x85EBCA6Bu) : 0);
   prm.header = reinterpret_cast<int*>(ws + lay.header);
   prm.units = reinterpret_cast<int4*>(ws + lay.units);
   prm.arrivals = reinterpret_cast<int*>(ws + lay.arrivals);
@@ -2092,8 +2161,10 @@ int launch_attention(const Params& prm_in, bool use_tc, int dtype, cudaStream_t 
     tc.stream = s;
     tc.attrs = attr;
     tc.numAttrs = 1;
-    e = bf16 ? cudaLaunchKernelEx(&tc, prefill_tc_kernel<__nv_bfloat16>, mq, mk, mv, mo, prm)
-             : cudaLaunchKernelEx(&tc, prefill_tc_kernel<__half>, mq, mk, mv, mo, prm);
+    auto* kernel = bf16 ? (prm.window ? prefill_tc_kernel<__nv_bfloat16, true>
+                                      : prefill_tc_kernel<__nv_bfloat16, false>)
+                        : (prm.window ? prefill_tc_kernel<__half, true> : prefill_tc_kernel<__half, false>);
+    e = cudaLaunchKernelEx(&tc, kernel, mq, mk, mv, mo, prm);
   } else {
     cudaLaunchConfig_t kc = {};
     kc.gridDim = dim3(prm.ncta);
@@ -2101,15 +2172,19 @@ int launch_attention(const Params& prm_in, bool use_tc, int dtype, cudaStream_t 
     kc.stream = s;
     kc.attrs = attr;
     kc.numAttrs = 1;
-    if (prm.head_dim == 128) {
-      kc.dynamicSmemBytes = Smem<128>::kBytes;
-      e = bf16 ? cudaLaunchKernelEx(&kc, prefill_kernel<__nv_bfloat16, 128>, mk, mv, prm)
-               : cudaLaunchKernelEx(&kc, prefill_kernel<__half, 128>, mk, mv, prm);
-    } else {
-      kc.dynamicSmemBytes = Smem<64>::kBytes;
-      e = bf16 ? cudaLaunchKernelEx(&kc, prefill_kernel<__nv_bfloat16, 64>, mk, mv, prm)
-               : cudaLaunchKernelEx(&kc, prefill_kernel<__half, 64>, mk, mv, prm);
-    }
+    auto launch = [&](auto type, auto dim) {
+      using T = decltype(type);
+      constexpr int D = decltype(dim)::value;
+      kc.dynamicSmemBytes = Smem<D>::kBytes;
+      auto* kernel = prm.window ? prefill_kernel<T, D, true> : prefill_kernel<T, D, false>;
+      return cudaLaunchKernelEx(&kc, kernel, mk, mv, prm);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (prm.head_dim == 128)
+      e = bf16 ? launch(__nv_bfloat16(), D128()) : launch(__half(), D128());
+    else
+      e = bf16 ? launch(__nv_bfloat16(), D64()) : launch(__half(), D64());
   }
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
   return PA_OK;

@@ -338,7 +338,7 @@ def test_prefill_masked_slots_may_hold_anything(gpu, dtype, head_dim):
 
 def test_prefill_plan_and_rows_of_no_sequence(gpu):
     """One plan, several runs; rows behind the last sequence and of an idle
-    one are left as they were."""
+    one are left as they were; a run without its plan does nothing."""
     q, kc, vc, tables, lens, qs = prefill_case(gpu, PLENS, PNEW, 8, 2, 128, "bf16", 90, 4, seed=73)
     total = int(qs[-1]) + 11
     q = torch.cat([q, torch.full((11, 8, 128), float("nan"), dtype=q.dtype, device=gpu)])
@@ -355,6 +355,11 @@ def test_prefill_plan_and_rows_of_no_sequence(gpu):
     pa.check_status()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
     assert (outs[0][-11:] == 5.0).all() and torch.isfinite(outs[0][:-11]).all()
+    pa.paged_attention_prefill_window_run(q, kc, vc, bt, cl, st, 91, 4, 0.1, ws, out=outs[1])
+    with pytest.raises(pa.PagedAttnError) as e:
+        pa.check_status()
+    assert e.value.status == 1
+    assert torch.equal(outs[0], outs[1])
 
 
 @pytest.mark.parametrize("lens,new", [([9000, 12345], [3, 16]), ([5000], [700]),
