@@ -15,13 +15,13 @@
 //
 //  * The visible blocks of a sequence are numbered 0 .. nb - 1 without gaps
 //    (first tokens' blocks, then the window's); all (sequence, KV head, block)
-//    triples in that order form one line of N blocks, cut into equal shares,
-//    one per warp of a full grid (one CTA of 8 warps per SM), at least
-//    kMinShare blocks each.  Equal work for every warp whatever the lengths (a
-//    (sequence, KV head) counts kSegmentCost blocks more than it has, for its
-//    query rows, first references and output); a long context is spread over
-//    the GPU, many short ones share a warp.  The plan kernel writes each
-//    warp's starting point.
+//    triples in that order form one line, cut into equal shares, one per CTA
+//    of a full grid (one CTA per SM), at least kMinPlaces each, and those into
+//    one per warp.  Equal work for every warp whatever the lengths (a
+//    (sequence, KV head) takes kSegmentCost places more than it has blocks,
+//    for its query rows, first references and output); a long context is
+//    spread over the GPU, many short ones share a warp.  The plan kernel
+//    writes each warp's starting point.
 //  * A warp streams its share through its own shared-memory ring, one tensor
 //    copy per K and V tile (16 rows), filled as many blocks ahead as fit; it
 //    does not stop at the ends of sequences.
@@ -62,19 +62,24 @@ namespace {
 constexpr int kBlockSize = 16;
 constexpr int kMaxGroup = 8;
 
-constexpr int kWarps = 8;            // warps per CTA
-constexpr int kThreads = kWarps * 32;
+// Warps per CTA.  A warp takes a block in about the same time whatever its
+// bytes (a chain of latencies: copy, product, softmax, product), so the fewer
+// bytes a block has, the more warps it takes to keep HBM busy; registers and
+// rings allow 8 of 16-bit tiles of head_dim 128, 12 of 8-bit ones, 16 of
+// head_dim 64.
+__host__ __device__ constexpr int warps_of(bool q8, int head_dim) {
+  return head_dim == 64 ? (q8 ? 16 : 12) : (q8 ? 12 : 8);
+}
 constexpr int kMaxCtas = 256;        // CTAs the workspace has room for
-constexpr int kMinShare = 4;         // blocks a warp takes at least
+constexpr int kMinPlaces = 32;       // places on the line a CTA takes at least
 constexpr int kSegmentCost = 2;      // what a (sequence, KV head) costs beside its blocks, in blocks
-static_assert(kMinShare > kSegmentCost, "every warp has a block");
 constexpr int kFillAt = 16;          // where in its 32 blocks a warp reads the next 32's entries
 constexpr float kRescale = 8.f;      // log2 by which a score may exceed the reference
 constexpr int kPlanThreads = 1024;
 
-// Workspace header words: what the plan was made for; blocks in all, blocks
-// per warp, whether a sequence has none (its output rows are zero).
-constexpr int kHdrSignature = 0, kHdrBlocks = 1, kHdrShare = 2, kHdrEmpty = 3;
+// Workspace header words: what the plan was made for; places in all, places
+// per CTA, whether a sequence has no blocks (its output rows are zero).
+constexpr int kHdrSignature = 0, kHdrPlaces = 1, kHdrShare = 2, kHdrEmpty = 3;
 
 // A CTA's two open ends: the one it shares with earlier CTAs (slot 0) and the
 // one that goes on in later ones (slot 1): unnormalised output, reference of
@@ -97,7 +102,8 @@ Layout workspace_layout(int num_seqs, int head_dim) {
   Layout l;
   l.seqs = 256;
   l.starts = align256(l.seqs + size_t(num_seqs) * sizeof(int4));
-  l.arrivals = align256(l.starts + size_t(kMaxCtas) * kWarps * 2 * sizeof(int4));
+  l.arrivals = align256(l.starts + size_t(kMaxCtas) * (warps_of(false, head_dim) + warps_of(true, head_dim)) *
+                                       2 * sizeof(int4));
   l.pieces = align256(l.arrivals + size_t(kMaxCtas) * 4);
   l.total = align256(l.pieces + size_t(kMaxCtas) * 2 *
                                     (head_dim == 128 ? sizeof(Piece<128>) : sizeof(Piece<64>)));
@@ -123,7 +129,10 @@ struct Params {
   // per sequence: length, visible blocks, places of a KV head's blocks before
   // the sequence's and of its own on the line
   int4* seqs;
-  int4* starts;      // per warp: sequence, KV head, block within it, blocks; its seqs entry
+  // per warp: sequence, KV head, block within it, blocks; its seqs entry (for
+  // the warp counts of 16-bit and 8-bit caches, one after the other)
+  int4* starts;
+  int head_dim;
   int* arrivals;     // per CTA: arrivals at the sequence that begins in it and goes on
   void* pieces;      // [kMaxCtas][2] Piece
   unsigned* status;
@@ -152,9 +161,8 @@ __device__ __forceinline__ Range visible_range(int n, int window, int num_sinks)
 // starting point by bisection.  Latency-bound; once per step, not per layer.
 //
 // Where the batch is so small that every (sequence, KV head) can have CTAs of
-// its own (at kMinShare blocks a warp), it gets them: up to
-// kWarps * kMinShare - kSegmentCost blocks then meet in one CTA's shared
-// memory, which saves the trip through the workspace (one sequence of 101
+// its own (at kMinPlaces a CTA), it gets them: up to kMinPlaces -
+// kSegmentCost blocks then meet in one CTA's shared memory, which saves the trip through the workspace (one sequence of 101
 // tokens, 8 KV heads: 6.5 us, 9.6 us packed).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   __shared__ int s_warp[kPlanThreads / 32];
@@ -172,18 +180,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     const int n = p.context_lens[b];
     return n < 0 ? 0 : min(n, p.max_blocks * kBlockSize);
   };
-  constexpr int kCtaPlaces = kWarps * kMinShare;
   int ctas = 0;
   for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
     const int n = p.context_lens[b];
     if (n < 0 || n > p.max_blocks * kBlockSize) dev::flag_status(p.status, kStatusBounds);
     const int nb = visible_range(length(b), p.window, p.num_sinks).count;
     if (nb == 0) s_empty = 1;
-    else if (ctas <= kMaxCtas) ctas += (nb + kSegmentCost + kCtaPlaces - 1) / kCtaPlaces;
+    else if (ctas <= kMaxCtas) ctas += (nb + kSegmentCost + kMinPlaces - 1) / kMinPlaces;
   }
   if (ctas) atomicAdd(&s_ctas, min(ctas, kMaxCtas + 1));
   __syncthreads();
-  const int pad = (long long)s_ctas * p.num_kv_heads <= p.ncta ? kCtaPlaces : 1;
+  const int pad = (long long)s_ctas * p.num_kv_heads <= p.ncta ? kMinPlaces : 1;
   for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
     const int b = base + tid;
     int n = 0, nb = 0;
@@ -217,8 +224,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     __syncthreads();
   }
   const int total = s_carry * p.num_kv_heads;
-  const int warps = p.ncta * kWarps;
-  const int share = max(kMinShare, (total + warps - 1) / warps);
+  const int share = max(kMinPlaces, (total + p.ncta - 1) / p.ncta);
   // Place f of the line: the sequence it falls in, and how many of its blocks
   // (KV head by KV head) lie before it.  A KV head's first kSegmentCost places
   // and those behind its last block hold none.
@@ -236,30 +242,43 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
     block = r / q.w * q.y + min(max(r % q.w - kSegmentCost, 0), q.y);
     return lo;
   };
-  for (int w = tid; w < warps; w += kPlanThreads) {
-    const long long f = (long long)w * share;
-    int4 at = make_int4(0, 0, 0, 0), q = make_int4(0, 1, 0, 0);
-    if (f < total) {
-      int block, block2 = 0;
-      const int b = locate(f, q, block);
-      int4 q2;
-      int count = 0, b2 = p.num_seqs;
-      if (f + share < total) b2 = locate(f + share, q2, block2);
-      // blocks up to the next warp's first, sequence by sequence
-      if (b2 == b) {
-        count = block2 - block;
-      } else {
-        count = q.y * p.num_kv_heads - block + block2;
-        for (int i = b + 1; i < b2; ++i) count += p.seqs[i].y * p.num_kv_heads;
+  int4* starts = p.starts;
+  for (int q8 = 0; q8 < 2; ++q8) {
+    const int warps = warps_of(q8, p.head_dim);
+    auto place = [&](int w) { return (long long)(w / warps) * share + w % warps * share / warps; };
+    for (int w = tid; w < p.ncta * warps; w += kPlanThreads) {
+      const long long f = place(w), end = place(w + 1);
+      int4 at = make_int4(0, 0, 0, 0), q = make_int4(0, 1, 0, 1);
+      if (f < total) {
+        int block, block2 = 0;
+        const int b = locate(f, q, block);
+        int4 q2;
+        int count = 0, b2 = p.num_seqs;
+        if (end < total) b2 = locate(end, q2, block2);
+        // blocks up to the next warp's first, sequence by sequence
+        if (b2 == b) {
+          count = block2 - block;
+        } else {
+          count = q.y * p.num_kv_heads - block + block2;
+          for (int i = b + 1; i < b2; ++i) count += p.seqs[i].y * p.num_kv_heads;
+        }
+        at = make_int4(b, block / q.y, block % q.y, count);
+        // (between two sequences: the next one's first block is the first)
+        if (count > 0 && at.y == p.num_kv_heads) {
+          int i = b + 1;
+          while (p.seqs[i].y == 0) ++i;
+          q = p.seqs[i];
+          at = make_int4(i, 0, 0, count);
+        }
       }
-      at = make_int4(b, block / q.y, block % q.y, count);
+      starts[2 * w] = at;
+      starts[2 * w + 1] = q;
     }
-    p.starts[2 * w] = at;
-    p.starts[2 * w + 1] = q;
+    starts += size_t(kMaxCtas) * warps * 2;
   }
   for (int c = tid; c < p.ncta; c += kPlanThreads) p.arrivals[c] = 0;
   if (tid == 0) {
-    p.header[kHdrBlocks] = total;
+    p.header[kHdrPlaces] = total;
     p.header[kHdrShare] = share;
     p.header[kHdrEmpty] = s_empty;
     p.header[kHdrSignature] = p.signature;
@@ -327,21 +346,26 @@ struct Tiles {
   using Mm = dev::Mma<typename std::conditional<Q8, __half, T>::type>;
   static constexpr int kElem = Q8 ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;               // of a token's row
-  static constexpr int kBox = kRowBytes < 128 ? 64 : 128;   // bytes of a row per copy box
-  static constexpr int kBoxes = kRowBytes / kBox;
-  static constexpr int kBoxBytes = kBox * kBlockSize;
+  // a copy box is 128 bytes wide: half a row, a row, or two tokens' rows
+  static constexpr int kBoxes = kRowBytes / 128 > 1 ? kRowBytes / 128 : 1;
   static constexpr int kTile = kRowBytes * kBlockSize;
+  static constexpr int kBoxBytes = kTile / kBoxes;
+  static constexpr int kBoxRows = kBoxBytes / 128;
   static constexpr int kStage = 2 * kTile;                  // K tile, V tile
-  static constexpr int kStages = 24576 / kStage;            // 24 KB a warp: 3, 6 or 12 blocks
+  static constexpr int kWarps = warps_of(Q8, D);
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kStages = (kWarps == 8 ? 24576 : !Q8 ? 16384 : 12288) / kStage;
   static constexpr int kSteps = D / 16;                     // 16-wide steps of either product
   static constexpr size_t kRing = size_t(kWarps) * kStages * kStage;
   static constexpr size_t kPieces = kRing;                  // Piece[kWarps]
   static constexpr size_t kBars = kPieces + kWarps * sizeof(Piece<D>);
-  static constexpr size_t kBytes = kBars + size_t(kWarps) * kStages * 8;
+  static constexpr size_t kFlags = kBars + size_t(kWarps) * kStages * 8;  // int[kWarps + 4]
+  static constexpr size_t kBytes = kFlags + (kWarps + 4) * 4;
   // merge of a sequence's pieces over CTAs, in the ring's place
   static_assert(kRing >= size_t(kMaxCtas) * kMaxGroup * 12, "merge weights");
   static_assert(size_t(kStages) * kStage >= sizeof(Piece<D>), "a warp's last piece");
-  static_assert(kBytes + 1024 <= 227 * 1024, "shared memory");
+  static_assert(kStages >= 3, "two blocks in use, one on its way");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
   static_assert(kThreads >= kMaxGroup * D / 4, "a column per thread");
 };
 
@@ -373,9 +397,10 @@ __device__ __forceinline__ void load_k(uint32_t tile, int g, int t, uint32_t (&f
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       // head_dim 16 (2t + j) .. + 15 (128), 16 t .. + 15 (64)
+      // (64: two tokens to a 128-byte row)
       const uint32_t at = D == 128 ? tile + g * 128 + (((2 * t + j) ^ g) << 4)
-                                   : tile + g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
-      const uint4 a = lds128(at), b = lds128(at + 8 * D);
+                                   : tile + (g >> 1) * 128 + ((((g & 1) * 4 + t) ^ (g >> 1)) << 4);
+      const uint4 a = lds128(at), b = lds128(D == 128 ? at + 1024 : (at + 512) ^ 64);
       const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -454,7 +479,7 @@ __device__ __forceinline__ void load_v(uint32_t tile, int g, int t, uint32_t kee
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = rows[i];
-      const uint2 v = lds64(tile + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+      const uint2 v = lds64(tile + (r >> 1) * 128 + ((((r & 1) * 4 + (g >> 1)) ^ (r >> 1)) << 4) + (g & 1) * 8);
       w[i][0] = v.x;
       w[i][1] = v.y;
     }
@@ -532,12 +557,12 @@ __device__ __forceinline__ int convert_q(const uint4 (&raw)[D / 32], uint32_t (&
 }
 
 template <typename T, bool Q8, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const Params p) {
   using S = Tiles<T, Q8, D>;
   using Mm = typename S::Mm;
-  constexpr int ST = S::kStages;
+  constexpr int ST = S::kStages, kWarps = S::kWarps, kThreads = S::kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -557,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int Hkv = p.num_kv_heads, G = p.group;
   // (all of the plan's words at once: one trip to memory)
   const int4 hdr = *reinterpret_cast<const int4*>(p.header);
-  const int4 start = p.starts[2 * (blockIdx.x * kWarps + warp)];
-  const int4 start_seq = p.starts[2 * (blockIdx.x * kWarps + warp) + 1];
+  const int4* mine = p.starts + 2 * (blockIdx.x * kWarps + warp);
+  const int4 start = mine[0], start_seq = mine[1];
   if (hdr.x != p.signature) {
     if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_status(p.status, kStatusPlan);
     return;
@@ -573,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   }
   const int count = start.w;  // this warp's blocks
-  if ((long long)blockIdx.x * kWarps * share >= total) return;
+  if ((long long)blockIdx.x * share >= total) return;
 
   const unsigned long long tmo = p.timeout_ns;
   const uint64_t policy = dev::l2_policy_evict_first();
@@ -635,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       dev::mbar_arrive_expect_tx(bar, S::kStage);
 #pragma unroll
       for (int x = 0; x < S::kBoxes; ++x) {
-        dev::tma_load_2d(dst + x * S::kBoxBytes, &tmap_k, x * (S::kBox / S::kElem), at * kBlockSize, bar, policy);
-        dev::tma_load_2d(dst + S::kTile + x * S::kBoxBytes, &tmap_v, x * (S::kBox / S::kElem), at * kBlockSize, bar,
+        dev::tma_load_2d(dst + x * S::kBoxBytes, &tmap_k, x * (128 / S::kElem), at * S::kBoxRows, bar, policy);
+        dev::tma_load_2d(dst + S::kTile + x * S::kBoxBytes, &tmap_v, x * (128 / S::kElem), at * S::kBoxRows, bar,
                          policy);
       }
     }
@@ -900,7 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // warps (a last piece, or for one that an earlier CTA began the first
   // warp's, then first pieces), each of which merges a slice of the columns.
   // One cut between CTAs too goes to the workspace.
-  __shared__ int s_tail[kWarps], s_open[2], s_merge[2];
+  int* s_tail = reinterpret_cast<int*>(smem + S::kFlags);
+  int *s_open = s_tail + kWarps, *s_merge = s_open + 2;
   if (lane == 0) s_tail[warp] = has_tail;
   if (threadIdx.x < 2) s_open[threadIdx.x] = s_merge[threadIdx.x] = -1;
   if (!__syncthreads_and(ok)) return;
@@ -916,30 +942,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = last - from + 1;
     for (int i = (warp - from) * 32 + lane; i < G * D / 4; i += 32 * n) {
       const int head = i / (D / 4), d = (i % (D / 4)) * 4;
-      // (at most one piece per warp: every load in flight at once)
-      float pm[kWarps], pw[kWarps], pl[kWarps], m = -INFINITY, w = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < kWarps; ++j) {
-        const Piece<D>* x = j ? &head_pieces[min(from + j, kWarps - 1)] : first;
-        pm[j] = j < n ? x->m[head] : -INFINITY;
-        pw[j] = j < n ? x->w[head] : -INFINITY;
-        pl[j] = j < n ? x->l[head] : 0.f;
-        m = fmaxf(m, pm[j]);
-        w = fmaxf(w, pw[j]);
+      auto nth = [&](int j) { return j ? &head_pieces[from + j] : first; };
+      float m = -INFINITY, w = -INFINITY;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        m = fmaxf(m, nth(j)->m[head]);
+        w = fmaxf(w, nth(j)->w[head]);
       }
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float l = 0.f;
-#pragma unroll
-      for (int j = 0; j < kWarps; ++j) {
-        if (j >= n) break;
-        const Piece<D>* x = j ? &head_pieces[min(from + j, kWarps - 1)] : first;
-        const float a = pw[j] == -INFINITY ? 0.f : dev::fast_exp2(pw[j] - w);
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const Piece<D>* x = nth(j);
+        const float a = x->w[head] == -INFINITY ? 0.f : dev::fast_exp2(x->w[head] - w);
         const float4 y = *reinterpret_cast<const float4*>(&x->o[head][d]);
         sum.x += a * y.x;
         sum.y += a * y.y;
         sum.z += a * y.z;
         sum.w += a * y.w;
-        l += pm[j] == -INFINITY ? 0.f : dev::fast_exp2(pm[j] - m) * pl[j];
+        l += x->m[head] == -INFINITY ? 0.f : dev::fast_exp2(x->m[head] - m) * x->l[head];
       }
       if (whole) {
         const float inv = l != 0.f ? dev::fast_exp2(Q8 ? w - m : 0.f) / l : 0.f;
@@ -967,12 +988,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   // ---- the last CTA to arrive at a sequence cut between CTAs merges it
-  const int span = share * kWarps;
   auto first_cta = [&](int id, int& n) {
     const int4 at = p.seqs[id / Hkv];
     const long long f = (long long)at.z * Hkv + (long long)(id % Hkv) * at.w + kSegmentCost;
-    const int c0 = int(f / span);
-    n = int((f + at.y - 1) / span) - c0 + 1;
+    const int c0 = int(f / share);
+    n = int((f + at.y - 1) / share) - c0 + 1;
     return c0;
   };
   const int open0 = s_open[0], open1 = s_open[1];
@@ -1143,7 +1163,7 @@ int check_sizes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, i
   if (num_q_heads % num_kv_heads != 0)
     return fail(PA_ERR_INVALID_ARG, "%s: num_q_heads %% num_kv_heads != 0", who);
   if (double(max_blocks) * kBlockSize >= 2147483647.0 ||
-      double(num_seqs) * num_kv_heads * (double(max_blocks) + kWarps * kMinShare) >= 2147483647.0 ||
+      double(num_seqs) * num_kv_heads * (double(max_blocks) + kMinPlaces) >= 2147483647.0 ||
       double(num_seqs) * num_q_heads >= 2147483647.0)
     return fail(PA_ERR_INVALID_ARG, "%s: sizes too large for the workspace", who);
   return PA_OK;
@@ -1153,7 +1173,7 @@ template <typename T, bool Q8, int D>
 cudaError_t launch_attend(cudaLaunchConfig_t cfg, const CUtensorMap& mk, const CUtensorMap& mv,
                           const Params& p) {
   cfg.gridDim = dim3(unsigned(p.ncta));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Tiles<T, Q8, D>::kThreads);
   cfg.dynamicSmemBytes = Tiles<T, Q8, D>::kBytes;
   return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D>, mk, mv, p);
 }
@@ -1219,6 +1239,7 @@ int entry(const Call& c) {
   p.group = group;
   p.max_blocks = c.max_blocks;
   p.num_blocks = c.num_blocks;
+  p.head_dim = c.head_dim;
   p.ncta = ncta;
   p.scale = c.scale;
   p.scale_log2 = c.scale * 1.4426950408889634f;
@@ -1227,7 +1248,9 @@ int entry(const Call& c) {
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   p.header = reinterpret_cast<int*>(ws);
   p.seqs = reinterpret_cast<int4*>(ws + lay.seqs);
+  // (the plan writes both warp counts' starts, a run reads its own)
   p.starts = reinterpret_cast<int4*>(ws + lay.starts);
+  int4* q8_starts = p.starts + size_t(kMaxCtas) * warps_of(false, c.head_dim) * 2;
   p.arrivals = reinterpret_cast<int*>(ws + lay.arrivals);
   p.pieces = ws + lay.pieces;
   p.status = status;
@@ -1244,6 +1267,7 @@ int entry(const Call& c) {
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: plan launch failed: %s", who, cudaGetErrorString(e));
   }
   if (!runs) return PA_OK;
+  if (c.q8) p.starts = q8_starts;
   cudaError_t e;
   if (c.dtype == PA_F32) {
     cfg.gridDim = dim3(unsigned((c.num_seqs * c.num_q_heads + 3) / 4));

@@ -47,19 +47,19 @@ int encode_cache_map(CUtensorMap* map, const void* cache, bool bf16, int num_blo
   return PA_OK;
 }
 
-// The same of a cache of 8-bit codes: a box is 16 rows x head_dim bytes, a
-// whole (block, head) tile.
+// The same of a cache of 8-bit codes, as 128-byte rows (a token's row of
+// head_dim 128, or two tokens' of 64): a box is a whole (block, head) tile.
 int encode_q8_map(CUtensorMap* map, const void* cache, int num_blocks, int num_kv_heads,
                   int head_dim) {
-  const cuuint64_t dims[2] = {cuuint64_t(head_dim),
-                              cuuint64_t(num_blocks) * num_kv_heads * kTokensPerBlock};
-  const cuuint64_t strides[1] = {cuuint64_t(head_dim)};
-  const cuuint32_t box[2] = {cuuint32_t(head_dim), kTokensPerBlock};
+  const int rows = kTokensPerBlock * head_dim / 128;
+  const cuuint64_t dims[2] = {128, cuuint64_t(num_blocks) * num_kv_heads * rows};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, cuuint32_t(rows)};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(cache), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled (8-bit) failed (%d)", int(r));
   return PA_OK;
 }

@@ -17,9 +17,8 @@ int cache_tensor_map(CUtensorMap* out, const void* cache, bool bf16, int num_blo
                      int num_kv_heads, int head_dim);
 
 // The same of a cache of 8-bit codes: one copy box is a whole (block, head)
-// tile, 16 rows of head_dim bytes (128-byte swizzle for head_dim 128: the
-// 16-byte chunks of row r XOR-ed with r % 8; 64-byte swizzle for head_dim 64:
-// with (r / 2) % 4).
+// tile as 128-byte rows with 128-byte swizzle (head_dim 128: a token's row;
+// 64: those of tokens 2r and 2r + 1), 16 * head_dim / 128 of them.
 int q8_cache_tensor_map(CUtensorMap* out, const void* cache, int num_blocks, int num_kv_heads,
                         int head_dim);
 
