@@ -10,6 +10,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "pagedattn.h"
 #include "q8.cuh"
@@ -23,38 +25,75 @@ namespace {
 constexpr int kBlockSize = 16;
 constexpr int kAppendWarps = 8;
 
-// Eight consecutive elements of a row in 32 bits.
+// Eight consecutive elements of a row, as they lie in memory: a 16-bit type's
+// stay packed between finding the largest and encoding (half the registers,
+// twice the warps).
 template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&x)[8]);
+struct Row8 {
+  static constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+  uint4 v;
+  __device__ __forceinline__ void load(const T* src) { v = *reinterpret_cast<const uint4*>(src); }
+  // largest magnitude, in the type's bits; not `finite`: infinities and NaN
+  // count too (they are above every finite one)
+  __device__ __forceinline__ uint32_t top(bool finite) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t x = w[i] & 0x7FFF7FFFu;
+      if (finite) {
+        if ((x & 0xFFFFu) >= kInf) x &= 0xFFFF0000u;
+        if ((x >> 16) >= kInf) x &= 0xFFFFu;
+      }
+      m = __vmaxu2(m, x);
+    }
+    return max(m & 0xFFFFu, m >> 16);
+  }
+  __device__ static __forceinline__ uint32_t float_bits(uint32_t top) {
+    if constexpr (std::is_same<T, __half>::value)
+      return __float_as_uint(__half2float(__ushort_as_half(uint16_t(top))));
+    return top << 16;
+  }
+  __device__ __forceinline__ uint2 encode(float inv) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = dev::Mma<T>::unpack(w[i]);
+      c[i] = encode2(f.x * inv, f.y * inv);
+    }
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  }
+};
 
 template <>
-__device__ __forceinline__ void load8<float>(const float* src, float (&x)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* src, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(src);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = dev::Mma<__half>::unpack(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+struct Row8<float> {
+  static constexpr uint32_t kInf = 0x7F800000u;
+  uint4 v[2];
+  __device__ __forceinline__ void load(const float* src) {
+    v[0] = reinterpret_cast<const uint4*>(src)[0];
+    v[1] = reinterpret_cast<const uint4*>(src)[1];
   }
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* src, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(src);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  __device__ __forceinline__ uint32_t top(bool finite) const {
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = dev::Mma<__nv_bfloat16>::unpack(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = w[i] & 0x7FFFFFFFu;
+      if (!finite || x < kInf) m = max(m, x);
+    }
+    return m;
   }
-}
+  __device__ static __forceinline__ uint32_t float_bits(uint32_t top) { return top; }
+  __device__ __forceinline__ uint2 encode(float inv) const {
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = encode2(__uint_as_float(w[2 * i]) * inv, __uint_as_float(w[2 * i + 1]) * inv);
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  }
+};
 
 // Eight codes times `factor`, as codes again.
 __device__ __forceinline__ uint2 rescale8(uint2 c, float factor) {
@@ -88,71 +127,72 @@ struct AppendParams {
 // the scale grows.  Bound by bytes (2 head_dim elements read and as many
 // codes written per token and head); for a decode step by latency.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : 4)
+    append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 8;             // lanes per row, eight elements each
   constexpr int kRows = 32 / kLanes;        // rows per pass
   constexpr int kPasses = kBlockSize / kRows;
   dev::grid_launch_dependents();
   dev::grid_dependency_wait();
   // the unit's sequence: the last one whose first unit is not past it
+  __shared__ int4 s_seq;  // it, its first and last query row, its length
   const int unit = blockIdx.x;
   auto invalid = [&](int q0, int q1, int ctx) {
     return q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > ctx ||
            ctx > p.max_blocks * kBlockSize;
   };
-  int mine = 0;
-  for (int base = 0; base < p.num_seqs; base += kAppendWarps * 32) {
-    const int b = base + threadIdx.x;
-    const int q0 = b < p.num_seqs ? p.query_start[b] : 0;
-    mine += __syncthreads_count(b < p.num_seqs && q0 / kBlockSize + 3 * b <= unit);
-    if (unit == 0 && blockIdx.y == 0 && b < p.num_seqs &&
-        invalid(q0, p.query_start[b + 1], p.context_lens[b]))
-      dev::flag_status(p.status, kStatusBounds);
+  if (threadIdx.x == 0) s_seq = make_int4(-1, 0, 0, 0);
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.num_seqs; b += kAppendWarps * 32) {
+    const int q0 = p.query_start[b], q1 = p.query_start[b + 1], ctx = p.context_lens[b];
+    if (q0 / kBlockSize + 3 * b <= unit && (b + 1 == p.num_seqs || q1 / kBlockSize + 3 * (b + 1) > unit))
+      s_seq = make_int4(b, q0, q1, ctx);
+    if (unit == 0 && blockIdx.y == 0 && invalid(q0, q1, ctx)) dev::flag_status(p.status, kStatusBounds);
   }
-  const int b = mine - 1;
-  if (b < 0) return;
-  const int q0 = p.query_start[b], q1 = p.query_start[b + 1], ctx = p.context_lens[b];
+  __syncthreads();
+  const int b = s_seq.x, q0 = s_seq.y, q1 = s_seq.z, ctx = s_seq.w;
   const int fresh_tokens = q1 - q0;
-  if (fresh_tokens == 0 || invalid(q0, q1, ctx)) return;
+  if (b < 0 || fresh_tokens == 0 || invalid(q0, q1, ctx)) return;
   const int begin = ctx - fresh_tokens;     // first new token's position
   const int blk = begin / kBlockSize + (unit - (q0 / kBlockSize + 3 * b));
   if (blk > (ctx - 1) / kBlockSize) return;
-  const int phys = p.block_tables[size_t(b) * p.max_blocks + blk];
-  if (phys < 0 || phys >= p.num_blocks) {
-    if (threadIdx.x == 0) dev::flag_status(p.status, kStatusBounds);
-    return;
-  }
   const int job = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
   if (job >= 2 * p.num_kv_heads) return;
   const int kv = job & 1, head = job >> 1, lane = threadIdx.x & 31;
   const int lo = max(begin - blk * kBlockSize, 0);                 // rows lo .. hi - 1 are new
   const int hi = min(ctx - blk * kBlockSize, kBlockSize);
   const int row0 = lane / kLanes, col = (lane % kLanes) * 8;
-  // the new rows, and the largest finite magnitude among them
-  float x[kPasses][8];
-  float peak = 0.f;
+  // the new rows (on their way while the table entry is), and the largest
+  // finite magnitude among them
+  Row8<T> x[kPasses];
   // (row 0 of the block, which lies before the tokens when lo > 0)
-  const T* src = static_cast<const T*>((kv ? p.src[1] : p.src[0])) +
+  const T* src = static_cast<const T*>(kv ? p.src[1] : p.src[0]) +
                  ((int64_t(q0) + blk * kBlockSize - begin) * p.num_kv_heads + head) * D + col;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = i * kRows + row0;
-    if (r >= lo && r < hi) load8<T>(src + int64_t(r) * p.num_kv_heads * D, x[i]);
+    if (r >= lo && r < hi) x[i].load(src + int64_t(r) * p.num_kv_heads * D);
+  }
+  const int phys = p.block_tables[size_t(b) * p.max_blocks + blk];
+  if (phys < 0 || phys >= p.num_blocks) {
+    if (lane == 0) dev::flag_status(p.status, kStatusBounds);
+    return;
   }
   const size_t tile = size_t(phys) * p.num_kv_heads + head;
-  const float old = lo > 0 ? (kv ? p.scale[1] : p.scale[0])[tile] : 0.f;
+  float* scale_at = (kv ? p.scale[1] : p.scale[0]) + tile;
+  const float old = lo > 0 ? *scale_at : 0.f;
+  auto largest = [&](bool finite) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = i * kRows + row0;
-    if (r >= lo && r < hi) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = fabsf(x[i][e]);
-        if (a <= 3.402823466e38f) peak = fmaxf(peak, a);
-      }
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = i * kRows + row0;
+      if (r >= lo && r < hi) m = max(m, x[i].top(finite));
     }
-  }
-  const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(peak));
+    return __reduce_max_sync(0xffffffffu, m);
+  };
+  uint32_t top = largest(false);
+  if (top >= Row8<T>::kInf) top = largest(true);
+  top = Row8<T>::float_bits(top);
   const float want = __uint_as_float(pow2_bits(scale_exponent(top)));
   const float scale = lo > 0 ? fmaxf(old, want) : want;
   const float inv = 1.f / scale;            // exact: a power of two (or the caller's own scale)
@@ -172,31 +212,35 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendP
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = i * kRows + row0;
-    if (r >= lo && r < hi) {
-      uint2 c;
-      c.x = uint32_t(encode2(x[i][0] * inv, x[i][1] * inv)) |
-            uint32_t(encode2(x[i][2] * inv, x[i][3] * inv)) << 16;
-      c.y = uint32_t(encode2(x[i][4] * inv, x[i][5] * inv)) |
-            uint32_t(encode2(x[i][6] * inv, x[i][7] * inv)) << 16;
-      *reinterpret_cast<uint2*>(codes + r * D) = c;
-    }
+    if (r >= lo && r < hi) *reinterpret_cast<uint2*>(codes + r * D) = x[i].encode(inv);
   }
-  if (lane == 0 && (lo == 0 || scale > old)) (kv ? p.scale[1] : p.scale[0])[tile] = scale;
+  if (lane == 0 && (lo == 0 || scale > old)) *scale_at = scale;
 }
 
-// Sixteen codes times their scale, as sixteen elements.
-__device__ __forceinline__ void store16(float* dst, const float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(dst)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-}
+// Sixteen values as elements of the output's type: whole 32-byte sectors per
+// store where the output is 32-byte aligned.
 template <typename T>
-__device__ __forceinline__ void store16(T* dst, const float (&x)[16]) {
-  uint32_t w[8];
+__device__ __forceinline__ void store16(T* dst, const float (&x)[16], bool wide) {
+  constexpr int kWords = sizeof(T) == 4 ? 16 : 8;
+  uint32_t w[kWords];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = dev::Mma<T>::pack(x[2 * i], x[2 * i + 1]);
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  for (int i = 0; i < kWords; ++i) {
+    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
+    else w[i] = dev::Mma<T>::pack(x[2 * i], x[2 * i + 1]);
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; i += 8) {
+    uint32_t* at = reinterpret_cast<uint32_t*>(dst) + i;
+    if (wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[i]),
+                   "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]),
+                   "r"(w[i + 6]), "r"(w[i + 7])
+                   : "memory");
+    } else {
+      reinterpret_cast<uint4*>(at)[0] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+      reinterpret_cast<uint4*>(at)[1] = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
+    }
+  }
 }
 
 constexpr int kReadThreads = 256;
@@ -229,6 +273,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadParams p) 
   const uint4* from = reinterpret_cast<const uint4*>((kv ? p.cache[1] : p.cache[0])) + src * p.chunks;
   const float* scale = (kv ? p.scale[1] : p.scale[0]) + src * p.num_kv_heads;
   T* to = static_cast<T*>((kv ? p.out[1] : p.out[0])) + dst * p.chunks * 16;
+  const bool wide = (reinterpret_cast<uintptr_t>(to) & 31) == 0;
   for (int base = blockIdx.z * kReadThreads * kReadBatch; base < p.chunks;
        base += gridDim.z * kReadThreads * kReadBatch) {
     uint4 c[kReadBatch];
@@ -255,7 +300,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadParams p) 
         x[4 * k + 2] = b.x * s[u];
         x[4 * k + 3] = b.y * s[u];
       }
-      store16(to + int64_t(i) * 16, x);
+      store16<T>(to + int64_t(i) * 16, x, wide);
     }
   }
 }

@@ -110,6 +110,22 @@ def test_append_token_by_token(gpu):
     pa.check_status()
 
 
+def test_append_many_sequences(gpu):
+    """More sequences than a thread block has threads, most of them idle or
+    with a token or two."""
+    gen = np.random.default_rng(21)
+    new = np.minimum(gen.integers(0, 4, 700), 2)
+    new[[3, 400, 699]] = [40, 17, 100]
+    lens = new + gen.integers(0, 40, 700)
+    tables, nb = window_tables(lens, lens, 0, 0, gen)
+    qs = np.concatenate([[0], np.cumsum(new)])
+    m = Mirror(nb, 2, 64, 15, gpu)
+    k, v = (wl.normal((int(qs[-1]), 2, 64), torch.bfloat16, 17 + i, gpu) * 3 for i in range(2))
+    m.append(k, v, tables, lens, qs, gpu)
+    m.check()
+    pa.check_status()
+
+
 def test_append_bad_input(gpu):
     """Bad lengths, rows and table entries skip what they concern, set the
     status and change nothing else."""
@@ -164,6 +180,23 @@ def test_dequantize_is_exact(gpu, dtype, hkv, head_dim):
     assert torch.equal(out[0][1].cpu(), torch.from_numpy(want).to(TORCH_DTYPES[dtype]))
     assert torch.equal(out[0][0].cpu(), torch.from_numpy(
         oq.decode(m.codes[0][3]) * m.scales[0][3].astype(np.float64)[:, None, None]).to(TORCH_DTYPES[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_dequantize_into_unaligned_sectors(gpu, dtype):
+    """Outputs that begin 16 bytes past a 32-byte boundary."""
+    m = Mirror(4, 2, 64, 25, gpu)
+    t = TORCH_DTYPES[dtype]
+    skip = 16 // t.itemsize
+    n = 3 * 2 * 16 * 64
+    out = [torch.zeros(n + 2 * skip, dtype=t, device=gpu)[skip:skip + n].view(3, 2, 16, 64) for _ in range(2)]
+    assert out[0].data_ptr() % 32 == 16
+    pairs = torch.tensor([[2, 0], [0, 1], [3, 2]], device=gpu)
+    pa.block_dequantize(*m.dcodes, *m.dscales, pairs, *out)
+    pa.check_status()
+    for i in range(2):
+        want = torch.stack([m.dcodes[i].float()[j] * m.dscales[i][j][:, None, None] for j in (2, 0, 3)])
+        assert torch.equal(out[i], want.to(t))
 
 
 # -------------------------------------------------------------------- decode
