@@ -23,7 +23,12 @@ def _dtype_code(t: torch.Tensor) -> int:
     return _DTYPES[t.dtype]
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device, stream=None) -> int:
+    if stream is None and _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)     # the current stream without a Stream object around it
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return s.cuda_stream
 
@@ -34,8 +39,12 @@ def _require(cond: bool, msg: str) -> None:
 
 
 def _cuda_contig(name: str, t: torch.Tensor, device: torch.device) -> None:
-    _require(t.is_cuda and t.device == device, f"{name} must be on {device}")
-    _require(t.is_contiguous(), f"{name} must be contiguous")
+    # (the messages are put together only when needed: this runs for every
+    # tensor of every call)
+    if t.get_device() != device.index:      # -1 for a host tensor, a device's index is never None
+        raise ValueError(f"{name} must be on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

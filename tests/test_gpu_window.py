@@ -374,3 +374,33 @@ def test_prefill_long_contexts(gpu, lens, new):
     check_prefill(out, q, kc, vc, tables, lens, qs, 3000, 200, "bf16", rows)
     again = pa.paged_attention_prefill_window(q, kc, vc, bt, cl, st, 3000, 200, 128 ** -0.5)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("window,sinks", [(100, 4), (600, 30)])
+@pytest.mark.parametrize("heads", [(8, 8), (8, 2)], ids=["g1", "g4"])
+def test_prefill_rows_rescale_apart(gpu, heads, window, sinks):
+    """Keys grow along the sequence and few rows have large queries: within a
+    warp some rows' softmax references move, others' do not, and rows whose
+    window begins later have seen nothing yet."""
+    hq, hkv = heads
+    lens, new = [900, 1500, 130], [260, 700, 130]
+    gen = np.random.default_rng(5)
+    tables, nb = window_tables(lens, new, window, sinks, gen)
+    grow = np.ones(nb, dtype=np.float32)
+    for b, n in enumerate(lens):
+        for j in range((n + 15) // 16):
+            if tables[b, j] >= 0:
+                grow[tables[b, j]] = 2.0 ** min(3.0, j / 12)
+    shape = (nb, hkv, 16, 128)
+    kc = (wl.normal(shape, torch.float32, 213, gpu) * torch.from_numpy(grow).to(gpu)[:, None, None, None]).bfloat16()
+    vc = wl.normal(shape, torch.bfloat16, 214, gpu)
+    qs = np.concatenate([[0], np.cumsum(new)])
+    size = np.where(gen.random((int(qs[-1]), hq, 1)) < 0.1, 4.0, 0.25).astype(np.float32)
+    q = (wl.normal((int(qs[-1]), hq, 128), torch.float32, 215, gpu) * torch.from_numpy(size).to(gpu)).bfloat16()
+    lens = np.asarray(lens)
+    bt, cl, st = to_dev(gpu, tables, lens, qs)
+    out = pa.paged_attention_prefill_window(q, kc, vc, bt, cl, st, window, sinks, 128 ** -0.5)
+    pa.check_status()
+    check_prefill(out, q, kc, vc, tables, lens, qs, window, sinks, "bf16", set(range(0, int(qs[-1]), 13)))
+    again = pa.paged_attention_prefill_window(q, kc, vc, bt, cl, st, window, sinks, 128 ** -0.5)
+    assert torch.equal(out, again)
