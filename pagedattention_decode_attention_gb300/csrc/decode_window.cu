@@ -88,8 +88,9 @@ template <int D>
 struct Piece {
   float o[kMaxGroup][D];
   float m[kMaxGroup], w[kMaxGroup], l[kMaxGroup];
-  int id, starts, ends, used;  // sequence * KV heads + head; holds its first / last block
-  int pad[4];
+  int id, ends, used;  // sequence * KV heads + head; holds its last block
+  int c0, ctas;        // first CTA of the sequence's KV head, and how many share it
+  int pad[3];
 };
 
 struct Layout {
@@ -904,9 +905,11 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
       }
       if (lane == 0) {
         piece->id = b * Hkv + h;
-        piece->starts = starts;
         piece->ends = ends;
         piece->used = 1;
+        const int f = seq.z * Hkv + h * seq.w + kSegmentCost;  // its first block's place
+        piece->c0 = f / share;
+        piece->ctas = (f + seq.y - 1) / share - f / share + 1;
       }
     }
     v = 0;
@@ -930,13 +933,26 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
   if (lane == 0) s_tail[warp] = has_tail;
   if (threadIdx.x < 2) s_open[threadIdx.x] = s_merge[threadIdx.x] = -1;
   if (!__syncthreads_and(ok)) return;
+  // bit w: warp w has a last piece, a first piece, a first piece that ends its
+  // sequence
+  const uint32_t tails = __ballot_sync(0xffffffffu, lane < kWarps && s_tail[lane % kWarps]);
+  const uint32_t heads = __ballot_sync(0xffffffffu, lane < kWarps && head_pieces[lane % kWarps].used);
+  const uint32_t ending =
+      __ballot_sync(0xffffffffu, lane < kWarps && head_pieces[lane % kWarps].used && head_pieces[lane % kWarps].ends);
+  auto last_piece = [&](int w) { return reinterpret_cast<const Piece<D>*>(smem + size_t(w) * ST * S::kStage); };
+  // the run of pieces that begins in warp `from`: it goes on through the first
+  // pieces of the warps behind until one ends the sequence or has none
   auto merge = [&](int from, bool from_tail) {
-    const Piece<D>* first =
-        from_tail ? reinterpret_cast<const Piece<D>*>(smem + size_t(from) * ST * S::kStage) : &head_pieces[from];
+    const Piece<D>* first = from_tail ? last_piece(from) : &head_pieces[from];
     const int id = first->id;
     bool ends = first->ends;
     int last = from;
-    while (!ends && last + 1 < kWarps && head_pieces[last + 1].used) ends = head_pieces[++last].ends;
+    if (!ends) {
+      const uint32_t more = ~heads >> (from + 1), stop = ending >> (from + 1);  // (bit kWarps of ~heads is set)
+      const int without = __ffs(more) - 1, with = stop ? __ffs(stop) - 1 : 32;
+      ends = with < without;
+      last = from + (ends ? with + 1 : without);
+    }
     const bool whole = from_tail && ends;
     Piece<D>* slot = static_cast<Piece<D>*>(p.pieces) + size_t(blockIdx.x) * 2 + (from_tail ? 1 : 0);
     const int n = last - from + 1;
@@ -976,48 +992,45 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
         }
       }
     }
-    if (!whole && warp == from && lane == 0) s_open[from_tail ? 1 : 0] = id;
+    if (!whole && warp == from && lane == 0) s_open[from_tail ? 1 : 0] = from;
   };
-  if (head_pieces[warp].used) {
-    int from = warp;
-    bool from_tail = false;
-    while (from > 0 && !from_tail) from_tail = s_tail[--from];
-    merge(from, from_tail);
+  if (heads >> warp & 1) {
+    // it goes on from the nearest last piece before it, or from an earlier CTA
+    const uint32_t before = tails & ((1u << warp) - 1);
+    merge(before ? 31 - __clz(before) : 0, before != 0);
   }
   if (has_tail) merge(warp, true);
   __syncthreads();
 
   // ---- the last CTA to arrive at a sequence cut between CTAs merges it
-  auto first_cta = [&](int id, int& n) {
-    const int4 at = p.seqs[id / Hkv];
-    const long long f = (long long)at.z * Hkv + (long long)(id % Hkv) * at.w + kSegmentCost;
-    const int c0 = int(f / share);
-    n = int((f + at.y - 1) / share) - c0 + 1;
-    return c0;
-  };
+  // (ends of the CTA that are open, by the warp in which their pieces begin)
   const int open0 = s_open[0], open1 = s_open[1];
   if (open0 < 0 && open1 < 0) return;
   if (lane == 0 && warp < 2) {
-    const int id = warp ? open1 : open0;
-    int n;
-    if (id >= 0) {
-      const int c0 = first_cta(id, n);
-      if (dev::atom_add_acq_rel_gpu(&p.arrivals[c0], 1) == n - 1) {
-        p.arrivals[c0] = 0;  // ready for the next run
-        s_merge[warp] = id;
+    const int from = warp ? open1 : open0;
+    if (from >= 0) {
+      const Piece<D>* x = warp ? last_piece(from) : &head_pieces[from];
+      if (dev::atom_add_acq_rel_gpu(&p.arrivals[x->c0], 1) == x->ctas - 1) {
+        p.arrivals[x->c0] = 0;  // ready for the next run
+        s_merge[warp] = from;
       }
     }
   }
   __syncthreads();
+  const int merge0 = s_merge[0], merge1 = s_merge[1];
+  if (merge0 < 0 && merge1 < 0) return;
+  const Piece<D>* left = merge0 < 0 ? nullptr : &head_pieces[merge0];
+  const Piece<D>* right = merge1 < 0 ? nullptr : last_piece(merge1);
+  const int left_id = left ? left->id : -1, left_c0 = left ? left->c0 : 0, left_n = left ? left->ctas : 0;
+  const int right_id = right ? right->id : -1, right_c0 = right ? right->c0 : 0, right_n = right ? right->ctas : 0;
+  __syncthreads();  // (the weights below overwrite the rings)
   for (int side = 0; side < 2; ++side) {
-    const int id = s_merge[side];
+    const int id = side ? right_id : left_id, c0 = side ? right_c0 : left_c0, n = side ? right_n : left_n;
     if (id < 0) continue;
-    int n;
-    const int c0 = first_cta(id, n);
     // piece k is CTA c0 + k's: its later end for k == 0, its earlier one else
     const Piece<D>* all = static_cast<const Piece<D>*>(p.pieces) + size_t(c0) * 2 + 1;
     auto nth = [&](int k) { return k ? all + 2 * k - 1 : all; };
-    float* wsm = reinterpret_cast<float*>(smem);  // [n][8] weights
+    float* wsm = reinterpret_cast<float*>(smem);  // [n][8] weights, in the rings' place
     // the columns' first pieces are on their way while the weights are made
     const int head = threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
     const bool mine = threadIdx.x < G * D / 4;  // kThreads >= 8 D / 4
