@@ -576,6 +576,14 @@ def paged_attention_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     return out
 
 
+def _window_ints(window, num_sinks):
+    """Both as C ints: a value past them would wrap around silently."""
+    window, num_sinks = int(window), int(num_sinks)
+    _require(-(1 << 31) <= window < 1 << 31 and -(1 << 31) <= num_sinks < 1 << 31,
+             "window and num_sinks must fit 32 bits")
+    return window, num_sinks
+
+
 def _call(dev, name: str, *args) -> None:
     """The C entry point ``name`` with ``dev`` current."""
     fn = getattr(capi.lib(), name)
@@ -615,8 +623,9 @@ def paged_attention_decode_window_plan(context_lens: torch.Tensor, window: int, 
     _cuda_contig("workspace", workspace, dev)
     _require(context_lens.dtype == torch.int32 and context_lens.dim() == 1,
              "context_lens must be int32 [num_seqs]")
-    _call(dev, "pa_paged_attention_decode_window_plan", context_lens.data_ptr(), int(window),
-          int(num_sinks), context_lens.shape[0], int(num_q_heads), int(num_kv_heads),
+    window, num_sinks = _window_ints(window, num_sinks)
+    _call(dev, "pa_paged_attention_decode_window_plan", context_lens.data_ptr(), window,
+          num_sinks, context_lens.shape[0], int(num_q_heads), int(num_kv_heads),
           int(head_dim), int(max_blocks_per_seq), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), _stream(dev, stream))
 
@@ -663,11 +672,12 @@ def _window_args(q, k_cache, v_cache, scales, block_tables, context_lens, window
     if workspace is None:
         workspace = alloc_window_workspace(b, hq, hkv, d, mb, dev)
     _cuda_contig("workspace", workspace, dev)
+    window, num_sinks = _window_ints(window, num_sinks)
     ptrs = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()]
     ptrs += [] if scales is None else [t.data_ptr() for t in scales]
     ptrs += [block_tables.data_ptr(), context_lens.data_ptr()]
     args = ([C.c_void_p(p) for p in ptrs]
-            + [int(window), int(num_sinks), b, hq, hkv, d, mb, nb, C.c_float(scale),
+            + [window, num_sinks, b, hq, hkv, d, mb, nb, C.c_float(scale),
                _dtype_code(q), C.c_void_p(out.data_ptr()), C.c_void_p(workspace.data_ptr()),
                C.c_size_t(workspace.numel() * workspace.element_size()),
                C.c_void_p(_stream(dev, stream))])
@@ -765,8 +775,9 @@ def paged_attention_prefill_window_plan(context_lens: torch.Tensor, query_start:
     b = context_lens.shape[0]
     _require(query_start.shape == (b + 1,), "query_start must be [num_seqs + 1]")
     _require(dtype in _DTYPES, "dtype must be float32, float16 or bfloat16")
+    window, num_sinks = _window_ints(window, num_sinks)
     _call(dev, "pa_paged_attention_prefill_window_plan", context_lens.data_ptr(),
-          query_start.data_ptr(), int(window), int(num_sinks), b, int(total_q), int(num_q_heads),
+          query_start.data_ptr(), window, num_sinks, b, int(total_q), int(num_q_heads),
           int(num_kv_heads), int(head_dim), int(max_blocks_per_seq), float(scale), _DTYPES[dtype],
           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
           _stream(dev, stream))
@@ -812,9 +823,10 @@ def paged_attention_prefill_window(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     if workspace is None:
         workspace = alloc_prefill_workspace(b, q.shape[0], hq, hkv, d, dev)
     _cuda_contig("workspace", workspace, dev)
+    window, num_sinks = _window_ints(window, num_sinks)
     _call(dev, _entry, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), int(window),
-          int(num_sinks), b, q.shape[0], hq, hkv, d, mb, nb, float(scale), _dtype_code(q),
+          block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), window,
+          num_sinks, b, q.shape[0], hq, hkv, d, mb, nb, float(scale), _dtype_code(q),
           out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
           _stream(dev, stream))
     return out

@@ -305,6 +305,65 @@ def test_decode_many_and_long(gpu):
     check_decode(out, q, m, tables, lens, 0, 0, "bf16", rows={0, 250, 499, 500, 501, 502, 701})
 
 
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_decode_one_sequence_over_every_sm(gpu, head_dim):
+    gen = np.random.default_rng(75)
+    tables, nb = window_tables([70001], [1], 0, 0, gen)
+    m = Mirror(nb, 1, head_dim, 77, gpu)
+    q = wl.normal((1, 8, head_dim), torch.bfloat16, 85, gpu)
+    bt, cl = to_dev(gpu, tables, [70001])
+    out = pa.paged_attention_decode_q8(q, *m.dcodes, *m.dscales, bt, cl, 0, 0, head_dim ** -0.5)
+    pa.check_status()
+    check_decode(out, q, m, tables, [70001], 0, 0, "bf16")
+
+
+@pytest.mark.parametrize("hkv,head_dim", [(2, 64), (4, 128)])
+def test_forked_sequences_copy_on_write(gpu, hkv, head_dim):
+    """A fork of a sequence in an 8-bit cache: the shared last block is copied
+    (block_copy over the codes viewed as 16-bit elements, the scales by
+    index), then both branches append and decode."""
+    hq = 2 * hkv
+    m = Mirror(12, hkv, head_dim, 121, gpu)
+    tables = np.array([[3, 7, 1], [3, 7, 5]], dtype=np.int32)
+    prompt = wl.normal((40, hkv, head_dim), torch.bfloat16, 123, gpu)
+    m.append(prompt, prompt, tables[:1], [40], [0, 40], gpu)
+    as16 = [c.view(torch.uint8).view(12, -1).view(torch.float16).view(12, -1, 16, 64) for c in m.dcodes]
+    pa.block_copy(as16[:1], as16[1:], torch.tensor([[1, 5]], device=gpu))
+    for i in range(2):
+        m.dscales[i][5] = m.dscales[i][1]
+        m.codes[i][5], m.scales[i][5] = m.codes[i][1], m.scales[i][1]
+    m.check()
+    for step in range(4):
+        lens = np.array([41 + step, 41 + step])
+        k, v = (wl.normal((2, hkv, head_dim), torch.bfloat16, 125 + 2 * step + i, gpu) * 2.0 ** step
+                for i in range(2))
+        m.append(k, v, tables, lens, [0, 1, 2], gpu)
+        m.check()
+        q = wl.normal((2, hq, head_dim), torch.bfloat16, 141 + step, gpu)
+        bt, cl = to_dev(gpu, tables, lens)
+        out = pa.paged_attention_decode_q8(q, *m.dcodes, *m.dscales, bt, cl, 0, 0, 0.1)
+        pa.check_status()
+        check_decode(out, q, m, tables, lens, 0, 0, "bf16", scale=0.1)
+
+
+def test_decode_scale_of_zero(gpu):
+    """A block whose scale is zero holds zeros: it keeps its share of the
+    softmax (its scores are 0) and adds nothing."""
+    gen = np.random.default_rng(143)
+    tables, nb = window_tables([60, 20], [1, 1], 0, 0, gen)
+    m = Mirror(nb, 2, 128, 145, gpu)
+    for i in range(2):
+        m.scales[i][tables[0, 1]] = 0
+        m.scales[i][tables[1, :2]] = 0
+        m.dscales[i].copy_(torch.from_numpy(m.scales[i]))
+    q = wl.normal((2, 8, 128), torch.bfloat16, 147, gpu)
+    bt, cl = to_dev(gpu, tables, [60, 20])
+    out = pa.paged_attention_decode_q8(q, *m.dcodes, *m.dscales, bt, cl, 0, 0, 128 ** -0.5)
+    pa.check_status()
+    check_decode(out, q, m, tables, [60, 20], 0, 0, "bf16")
+    assert (out[1] == 0).all()
+
+
 def test_q8_cache_past_32_bit_offsets(gpu):
     nb = (1 << 32) // (8 * 16 * 128) + 64
     m = Mirror(40, 8, 128, 89, gpu)

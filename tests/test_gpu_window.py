@@ -227,6 +227,65 @@ def test_many_and_long_sequences(gpu, dtype):
     check_decode(out, q[700:701], kc, vc, tables[700:701], lens[700:701], 9000, 33, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_one_sequence_over_every_sm(gpu, dtype, head_dim):
+    """One KV head, one context long enough to be cut into a piece per CTA."""
+    q, kc, vc, tables, lens = decode_case(gpu, [70001], 8, 1, head_dim, dtype, 69990, 7, seed=81)
+    bt, cl = to_dev(gpu, tables, lens)
+    out = pa.paged_attention_decode_window(q, kc, vc, bt, cl, 69990, 7, head_dim ** -0.5)
+    pa.check_status()
+    check_decode(out, q, kc, vc, tables, lens, 69990, 7, dtype)
+    again = pa.paged_attention_decode_window(q, kc, vc, bt, cl, 69990, 7, head_dim ** -0.5)
+    assert torch.equal(out, again)
+
+
+def test_nothing_to_attend(gpu):
+    """Every sequence empty: zeros, whatever out held."""
+    q, kc, vc, tables, _ = decode_case(gpu, [1, 1, 1], 8, 2, 64, "bf16", 0, 0, seed=87)
+    bt, cl = to_dev(gpu, tables, [0, 0, 0])
+    out = torch.full_like(q, float("nan"))
+    pa.paged_attention_decode_window(q, kc, vc, bt, cl, 3, 1, 0.1, out=out)
+    pa.check_status()
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("scale", [-0.11, 0.0])
+def test_any_sign_of_scale(gpu, scale):
+    q, kc, vc, tables, lens = decode_case(gpu, [300, 17], 8, 2, 128, "bf16", 100, 4, seed=91)
+    bt, cl = to_dev(gpu, tables, lens)
+    out = pa.paged_attention_decode_window(q, kc, vc, bt, cl, 100, 4, scale)
+    check_decode(out, q, kc, vc, tables, lens, 100, 4, "bf16", scale=scale)
+    st = to_dev(gpu, [0, 1, 2])[0]
+    pre = pa.paged_attention_prefill_window(q, kc, vc, bt, cl, st, 100, 4, scale)
+    pa.check_status()
+    check_decode(pre, q, kc, vc, tables, lens, 100, 4, "bf16", scale=scale)
+
+
+def test_two_streams_at_once(gpu):
+    """Two steps on two streams with a workspace each, interleaved."""
+    cases = [decode_case(gpu, lens, 32, 8, 128, "bf16", w, 4, seed=93 + w)
+             for lens, w in (([3000, 50, 700], 600), ([90, 2500, 1, 40], 1000))]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want, got, keep = [], [[], []], []
+    for (q, kc, vc, tables, lens), w in zip(cases, (600, 1000)):
+        bt, cl = to_dev(gpu, tables, lens)
+        ws = pa.alloc_window_workspace(len(lens), 32, 8, 128, tables.shape[1], gpu)
+        keep.append((bt, cl, ws))
+        want.append(pa.paged_attention_decode_window(q, kc, vc, bt, cl, w, 4, 0.1))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, ((q, kc, vc, tables, lens), w) in enumerate(zip(cases, (600, 1000))):
+            with torch.cuda.stream(streams[i]):
+                bt, cl, ws = keep[i]
+                got[i].append(pa.paged_attention_decode_window(q, kc, vc, bt, cl, w, 4, 0.1, workspace=ws))
+    torch.cuda.synchronize()
+    pa.check_status()
+    for i in range(2):
+        for out in got[i]:
+            assert torch.equal(out, want[i])
+
+
 def test_cache_past_32_bit_offsets(gpu):
     """A cache of more than 2^32 elements, the visible blocks at its end."""
     nb = (1 << 32) // (8 * 16 * 128) + 64

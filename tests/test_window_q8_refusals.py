@@ -139,3 +139,10 @@ def test_python_binding_refuses_host_tensors():
         pa.kv_append_q8(q, q, c8, c8, s, s, bt, cl, qs)
     with pytest.raises(ValueError):
         pa.block_dequantize(c8, c8, s, s, torch.zeros(1, 2, dtype=torch.int64), c16, c16)
+
+
+@pytest.mark.parametrize("window,sinks", [(1 << 32, 0), ((1 << 32) + 5, 0), (4, 1 << 31), (-(1 << 31) - 1, 0)])
+def test_windows_past_32_bits_do_not_wrap(window, sinks):
+    from pagedattention_decode_attention_gb300 import ops
+    with pytest.raises(ValueError, match="32 bits"):
+        ops._window_ints(window, sinks)
