@@ -827,9 +827,9 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
       for (int i = 0; i < N; ++i) {
         float p0 = dev::fast_exp2(x[i][0] - r0), p1 = dev::fast_exp2(x[i][1] - r1);
         float p2 = dev::fast_exp2(x[i][2] - r0), p3 = dev::fast_exp2(x[i][3] - r1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
         if constexpr (Q8) {
+          l0 += p0 + p2;
+          l1 += p1 + p3;
           // the weights carry the block's value scale: 2^(x + log2 scale),
           // kept near 1 by a reference of their own, so f16 holds them
           // whatever the scales are
@@ -841,8 +841,16 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
         }
         // rounded once to the tensor cores' 16-bit type; transposed so that
         // the tokens are the contraction
-        b0[i] = dev::movmatrix_trans(Mm::pack(p0, p1));
-        b1[i] = dev::movmatrix_trans(Mm::pack(p2, p3));
+        const uint32_t first = Mm::pack(p0, p1), second = Mm::pack(p2, p3);
+        if constexpr (!Q8) {
+          // the sum takes the weights as rounded: the output stays a mean of
+          // V's rows, and where one weight dominates its rounding cancels
+          const float2 a = Mm::unpack(first), c = Mm::unpack(second);
+          l0 += a.x + c.x;
+          l1 += a.y + c.y;
+        }
+        b0[i] = dev::movmatrix_trans(first);
+        b1[i] = dev::movmatrix_trans(second);
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
