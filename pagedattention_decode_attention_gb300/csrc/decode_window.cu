@@ -557,6 +557,34 @@ __device__ __forceinline__ int convert_q(const uint4 (&raw)[D / 32], uint32_t (&
   return e;
 }
 
+// While the kernel before this one finishes (its last CTAs leave most of HBM
+// idle): brings the warp's first blocks into L2.  Hints only, made from
+// whatever the workspace and tables hold at this moment: every index is
+// checked, everything is read again after the dependency wait, and these reads
+// go through L2 so that no L1 line of theirs can serve a later one.
+template <int TILE>
+__device__ __forceinline__ void warm_l2(const Params& p, const int4* mine, int lane, int blocks) {
+  const int4 hdr = __ldcg(reinterpret_cast<const int4*>(p.header));
+  const int4 at = __ldcg(mine), seq = __ldcg(mine + 1);
+  if (hdr.x != p.signature || lane >= blocks || lane >= at.w) return;
+  const int b = at.x, h = at.y, v = at.z + lane;
+  if (b < 0 || b >= p.num_seqs || h < 0 || h >= p.num_kv_heads || at.z < 0 || v >= seq.y ||
+      seq.x <= 0 || seq.x > p.max_blocks * kBlockSize)
+    return;
+  const Range r = visible_range(seq.x, p.window, p.num_sinks);
+  const int block = v < r.first ? v : v + r.skip;
+  if (block < 0 || block >= p.max_blocks) return;
+  const int phys = __ldcg(p.block_tables + size_t(b) * p.max_blocks + block);
+  if (phys < 0 || phys >= p.num_blocks) return;
+  const size_t tile = (size_t(phys) * p.num_kv_heads + h) * TILE;
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const uint8_t*>(p.k_cache) + tile),
+               "n"(TILE)
+               : "memory");
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const uint8_t*>(p.v_cache) + tile),
+               "n"(TILE)
+               : "memory");
+}
+
 template <typename T, bool Q8, int D>
 __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -578,9 +606,10 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
   }
   __syncwarp();
   dev::grid_launch_dependents();
+  const int Hkv = p.num_kv_heads, G = p.group;
+  warm_l2<S::kTile>(p, p.starts + 2 * (blockIdx.x * kWarps + warp), lane, 2 * ST);
   dev::grid_dependency_wait();
 
-  const int Hkv = p.num_kv_heads, G = p.group;
   // (all of the plan's words at once: one trip to memory)
   const int4 hdr = *reinterpret_cast<const int4*>(p.header);
   const int4* mine = p.starts + 2 * (blockIdx.x * kWarps + warp);
