@@ -30,7 +30,9 @@
  *   Every device-side wait is bounded; a wait that runs out sets
  *   PA_ERR_DEVICE_TIMEOUT in the same word instead of hanging.
  * - Element types: PA_F32, PA_F16, PA_BF16.  Caches, queries, new K/V and the
- *   output all share one dtype per call.  head_dim is 64 or 128.
+ *   output all share one dtype per call (but for the calls on an 8-bit cache,
+ *   whose caches hold e4m3 codes with a scale per block and KV head).
+ *   head_dim is 64 or 128.
  * - Shapes whose workspace would come near the range of size_t are refused
  *   (PA_ERR_INVALID_ARG) by every entry point and workspace-size query.
  * - Every compute entry point opens an NVTX range named after itself in the

@@ -858,6 +858,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 // in base 2 against a reference that moves only when a row's maximum grows by
 // more than 2^8 (O_w is then rescaled in TMEM; the result is the same either
 // way).
+// With a sliding window (WIN) an item's KV range is its rows' union of windows
+// and first tokens, numbered without the gap between them, so everything but the
+// table reads and two masks is as above: columns before a row's own window, and
+// V rows that no row of the item sees (zeroed, whatever they hold).  16 chunks of
+// 512, window 2048: 191 us, 1.11 PFLOP/s of visible work (0.58 of the measured
+// bf16 rate); two long prompts, window 4096: 236 us, 1.05 PFLOP/s.  S in half
+// tiles of 64 tokens, double-buffered so that it runs ahead of the softmax,
+// took 239 and 304 us (twice the waits, products half as wide).
 // Optional per-role wait counters (SM cycles), compiled in only with
 // -DPA_PROFILE_TIMES (a separate build; the default build has none of it).
 // Per CTA 32 slots of 8: MMA thread, softmax group 0 (its thread 0), group 1,
