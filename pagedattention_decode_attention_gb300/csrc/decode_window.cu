@@ -76,15 +76,20 @@ constexpr int kMaxGroup = 8;
 
 // Warps per CTA.  A warp takes a block in about the same time whatever its
 // bytes (a chain of latencies: copy, product, softmax, product), so the fewer
-// bytes a block has, the more warps it takes to keep HBM busy; registers and
-// rings allow 8 of 16-bit tiles of head_dim 128, 12 of 8-bit ones, 16 of
-// head_dim 64.
+// bytes a block has, the more warps it takes to keep HBM busy.  Registers and
+// rings of three blocks allow 8 for 16-bit tiles of head_dim 128, 12 for 8-bit
+// ones (8: 92.1 us on the 8-bit batch, 90.3 with 12), 16 for 8-bit tiles of 64
+// (8: 18.0 us on the long window, 16.7); 16-bit tiles of 64 do best with 12 and
+// rings of four (16 with three: 16.2 us on the odd window, 15.3).
 __host__ __device__ constexpr int warps_of(bool q8, int head_dim) {
   return head_dim == 64 ? (q8 ? 16 : 12) : (q8 ? 12 : 8);
 }
 constexpr int kMaxCtas = 256;        // CTAs the workspace has room for
 constexpr int kMinPlaces = 32;       // places on the line a CTA takes at least
-constexpr int kSegmentCost = 2;      // what a (sequence, KV head) costs beside its blocks, in blocks
+// what a (sequence, KV head) costs beside its blocks, in blocks (none: 100.6 us
+// on the 8-bit batch, 57.6 on the MHA one; 1: 95.5, 44.8; 2: 92.1, 42.9; 3: 92.8,
+// 44.1)
+constexpr int kSegmentCost = 2;
 constexpr int kFillAt = 16;          // where in its 32 blocks a warp reads the next 32's entries
 constexpr float kRescale = 8.f;      // log2 by which a score may exceed the reference
 constexpr int kPlanThreads = 1024;
@@ -176,8 +181,9 @@ __device__ __forceinline__ Range visible_range(int n, int window, int num_sinks)
 //
 // Where the batch is so small that every (sequence, KV head) can have CTAs of
 // its own (at kMinPlaces a CTA), it gets them: up to kMinPlaces -
-// kSegmentCost blocks then meet in one CTA's shared memory, which saves the trip through the workspace (one sequence of 101
-// tokens, 8 KV heads: 6.5 us, 9.6 us packed).
+// kSegmentCost blocks then meet in one CTA's shared memory, which saves the
+// trip through the workspace (one sequence of 101 tokens, 8 KV heads: 5.6 us,
+// 9.6 us packed).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   __shared__ int s_warp[kPlanThreads / 32];
   __shared__ int s_carry, s_empty, s_ctas;
@@ -259,7 +265,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   int4* starts = p.starts;
   for (int q8 = 0; q8 < 2; ++q8) {
     const int warps = warps_of(q8, p.head_dim);
-    auto place = [&](int w) { return (long long)(w / warps) * share + w % warps * share / warps; };
+    auto place = [&](int w) {
+      return (long long)(w / warps) * share + (long long)(w % warps) * share / warps;
+    };
     for (int w = tid; w < p.ncta * warps; w += kPlanThreads) {
       const long long f = place(w), end = place(w + 1);
       int4 at = make_int4(0, 0, 0, 0), q = make_int4(0, 1, 0, 1);
