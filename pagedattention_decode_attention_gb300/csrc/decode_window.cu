@@ -367,6 +367,13 @@ template <typename T, bool Q8, int D>
 struct Tiles {
   using Mm = dev::Mma<typename std::conditional<Q8, __half, T>::type>;
   static constexpr int kElem = Q8 ? 1 : 2;
+  // The softmax's weights enter V's product rounded to its 16-bit type.  f16's
+  // 2^-12 is under the rounding of any output; bf16's 2^-9 is as large as that
+  // of a bf16 output, so there what it leaves over goes through a second
+  // product: the windowed batch's output is 0.0017 (one rounding) from 64-bit
+  // arithmetic, 0.0023 without, for 89.4 us, 89.2 without (the tensor cores
+  // idle at 9 %).
+  static constexpr bool kTwoParts = !Q8 && std::is_same<T, __nv_bfloat16>::value;
   static constexpr int kRowBytes = D * kElem;               // of a token's row
   // a copy box is 128 bytes wide: half a row, a row, or two tokens' rows
   static constexpr int kBoxes = kRowBytes / 128 > 1 ? kRowBytes / 128 : 1;
@@ -613,6 +620,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
   using S = Tiles<T, Q8, D>;
   using Mm = typename S::Mm;
   constexpr int ST = S::kStages, kWarps = S::kWarps, kThreads = S::kThreads;
+  constexpr bool kTwoParts = S::kTwoParts;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -872,14 +880,14 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
         }
       }
       const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-      uint32_t b0[N], b1[N];
+      uint32_t b0[N], b1[N], e0[N], e1[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         float p0 = dev::fast_exp2(x[i][0] - r0), p1 = dev::fast_exp2(x[i][1] - r1);
         float p2 = dev::fast_exp2(x[i][2] - r0), p3 = dev::fast_exp2(x[i][3] - r1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
         if constexpr (Q8) {
-          l0 += p0 + p2;
-          l1 += p1 + p3;
           // the weights carry the block's value scale: 2^(x + log2 scale),
           // kept near 1 by a reference of their own, so f16 holds them
           // whatever the scales are
@@ -889,18 +897,17 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
           p2 = dev::fast_exp2(x[i][2] + d0);
           p3 = dev::fast_exp2(x[i][3] + d1);
         }
-        // rounded once to the tensor cores' 16-bit type; transposed so that
-        // the tokens are the contraction
+        // to the tensor cores' 16-bit type, transposed so that the tokens are
+        // the contraction
         const uint32_t first = Mm::pack(p0, p1), second = Mm::pack(p2, p3);
-        if constexpr (!Q8) {
-          // the sum takes the weights as rounded: the output stays a mean of
-          // V's rows, and where one weight dominates its rounding cancels
-          const float2 a = Mm::unpack(first), c = Mm::unpack(second);
-          l0 += a.x + c.x;
-          l1 += a.y + c.y;
-        }
         b0[i] = dev::movmatrix_trans(first);
         b1[i] = dev::movmatrix_trans(second);
+        if constexpr (kTwoParts) {
+          // what the rounding left over, rounded in turn
+          const float2 a = Mm::unpack(first), c = Mm::unpack(second);
+          e0[i] = dev::movmatrix_trans(Mm::pack(p0 - a.x, p1 - a.y));
+          e1[i] = dev::movmatrix_trans(Mm::pack(p2 - c.x, p3 - c.y));
+        }
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -908,6 +915,10 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
         load_v<Q8, D>(kt[i] + S::kTile, g, t, keep[i], f);
 #pragma unroll
         for (int m = 0; m < S::kSteps; ++m) Mm::run(o[m], f[m][0], f[m][1], f[m][2], f[m][3], b0[i], b1[i]);
+        if constexpr (kTwoParts) {
+#pragma unroll
+          for (int m = 0; m < S::kSteps; ++m) Mm::run(o[m], f[m][0], f[m][1], f[m][2], f[m][3], e0[i], e1[i]);
+        }
       }
       v += N;
       // the stages are read: their next blocks
