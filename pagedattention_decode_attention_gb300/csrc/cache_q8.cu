@@ -119,8 +119,9 @@ struct AppendParams {
 };
 
 // A unit is one (sequence, block the call writes to); blockIdx.x numbers them
-// with gaps: sequence b's begin at query_start[b] / 16 + 3 b, and T new tokens
-// touch at most (T + 30) / 16 blocks, so two sequences' units never meet.  A
+// with gaps: sequence b's begin at query_start[b] / 16 + 2 b, so the next one's
+// begin at least T / 16 + 2 later, and T new tokens touch at most (T + 14) / 16
+// + 1 <= T / 16 + 2 blocks: two sequences' units never meet.  A
 // warp owns one (unit, KV head, K or V): it alone reads and writes that
 // scale, holds the new rows in registers between finding their largest
 // magnitude and encoding them, and rescales the older rows of the block when
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : 4)
   __syncthreads();
   for (int b = threadIdx.x; b < p.num_seqs; b += kAppendWarps * 32) {
     const int q0 = p.query_start[b], q1 = p.query_start[b + 1], ctx = p.context_lens[b];
-    if (q0 / kBlockSize + 3 * b <= unit && (b + 1 == p.num_seqs || q1 / kBlockSize + 3 * (b + 1) > unit))
+    if (q0 / kBlockSize + 2 * b <= unit && (b + 1 == p.num_seqs || q1 / kBlockSize + 2 * (b + 1) > unit))
       s_seq = make_int4(b, q0, q1, ctx);
     if (unit == 0 && blockIdx.y == 0 && invalid(q0, q1, ctx)) dev::flag_status(p.status, kStatusBounds);
   }
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : 4)
   const int fresh_tokens = q1 - q0;
   if (b < 0 || fresh_tokens == 0 || invalid(q0, q1, ctx)) return;
   const int begin = ctx - fresh_tokens;     // first new token's position
-  const int blk = begin / kBlockSize + (unit - (q0 / kBlockSize + 3 * b));
+  const int blk = begin / kBlockSize + (unit - (q0 / kBlockSize + 2 * b));
   if (blk > (ctx - 1) / kBlockSize) return;
   const int job = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
   if (job >= 2 * p.num_kv_heads) return;
@@ -350,7 +351,7 @@ PA_API int pa_kv_append_q8(const void* k, const void* v, void* k_cache, void* v_
   if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq <= 0)
     return fail(PA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
   if (double(max_blocks_per_seq) * kBlockSize >= 2147483647.0 ||
-      double(num_tokens) / kBlockSize + 3.0 * num_seqs >= 2147483647.0)
+      double(num_tokens) / kBlockSize + 2.0 * num_seqs >= 2147483647.0)
     return fail(PA_ERR_INVALID_ARG, "%s: sizes too large", who);
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables ||
@@ -378,7 +379,7 @@ PA_API int pa_kv_append_q8(const void* k, const void* v, void* k_cache, void* v_
   p.status = status;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(num_tokens / kBlockSize + 3 * num_seqs),
+  cfg.gridDim = dim3(unsigned(num_tokens / kBlockSize + 2 * num_seqs),
                      unsigned((2 * num_kv_heads + kAppendWarps - 1) / kAppendWarps));
   cfg.blockDim = dim3(kAppendWarps * 32);
   cfg.stream = static_cast<cudaStream_t>(stream);
