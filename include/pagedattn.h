@@ -530,6 +530,30 @@ PA_API int pa_paged_attention_decode_q8_run(
     size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * pa_paged_attention_decode_q8_append_run -- pa_kv_append_q8 of one new token
+ * per sequence followed by pa_paged_attention_decode_q8_run, in one launch.
+ * (No counterpart on the pages.)
+ *
+ * Row b of k_new / v_new ([num_seqs][num_kv_heads][head_dim], q's dtype,
+ * 16-byte aligned) is the newest token of sequence b, which the planned
+ * length counts; codes, scales and output are bit for bit those of the two
+ * calls (query_start 0, 1, 2, ...).  A sequence planned with no tokens gets a
+ * zero output row and stores nothing.  A block outside [0, num_blocks) sets
+ * PA_ERR_DEVICE_BOUNDS and nothing is stored for it; nor is it when the
+ * sequence's length is more than its table holds (the plan sets
+ * PA_ERR_DEVICE_BOUNDS) or no longer the planned one (PA_ERR_INVALID_ARG from
+ * pa_check_status): its query then attends to the cache as it is.  No other
+ * sequence of the batch may read the block that takes a sequence's new token
+ * (copy-on-write guarantees this).
+ * ---------------------------------------------------------------------- */
+PA_API int pa_paged_attention_decode_q8_append_run(
+    const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+    float* k_scale, float* v_scale, const int32_t* block_tables, const int32_t* context_lens,
+    int window, int num_sinks, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * pa_paged_attention_prefill_window -- pa_paged_attention_prefill with a
  * sliding window and a few first tokens that stay visible.  (No counterpart
  * on the pages.)

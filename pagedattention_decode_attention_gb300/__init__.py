@@ -51,6 +51,7 @@ from .ops import (LayerCaches, Prepared, alloc_prefill_workspace, alloc_workspac
                   paged_attention_decode_window_plan, paged_attention_decode_window_run,
                   paged_attention_decode_window_workspace_size, prepare_decode_window_run,
                   paged_attention_decode_q8, paged_attention_decode_q8_run, prepare_decode_q8_run,
+                  paged_attention_decode_q8_append_run, prepare_decode_q8_append_run,
                   paged_attention_prefill_window, paged_attention_prefill_window_plan,
                   paged_attention_prefill_window_run, kv_append_q8, prepare_kv_append_q8,
                   block_dequantize, prepare_block_dequantize)

@@ -111,6 +111,8 @@ SIGNATURES = {
                                                                  _vp]),
     "pa_paged_attention_decode_q8_run": (_i, [_vp] * 7 + [_i] * 8 + [C.c_float, _i, _vp, _vp, _sz,
                                                                      _vp]),
+    "pa_paged_attention_decode_q8_append_run": (_i, [_vp] * 9 + [_i] * 8 + [C.c_float, _i, _vp,
+                                                                            _vp, _sz, _vp]),
     "pa_paged_attention_prefill_window": (_i, [_vp] * 6 + [_i] * 9 + [C.c_float, _i, _vp, _vp,
                                                                       _sz, _vp]),
     "pa_paged_attention_prefill_window_plan": (_i, [_vp] * 2 + [_i] * 8 + [C.c_float, _i, _vp,

@@ -37,6 +37,11 @@
 //    CTA's two open ends go to the workspace and the CTA that arrives last at
 //    a sequence merges its pieces in order (the result does not depend on
 //    which one that is).
+//  * pa_paged_attention_decode_q8_append_run: the warp that takes a sequence's
+//    last block quantises the new token into the tile it has in shared memory
+//    (and the older rows anew when the scale grows) and stores the same bytes
+//    to the cache, so no copy waits for the append.  This stands outside
+//    the loop over blocks: 90.7 us on the first batch below, 92.1 inside it.
 //  * Before it waits for the kernel in front of it, a launch brings its first
 //    blocks into L2 (hints only): 1.3 - 3.4 us less for launches in a row, 0.7 us
 //    more for one on an idle GPU.
@@ -46,9 +51,11 @@
 // launch cannot do without (0.92); 64 sequences, window 4096 + 64, bf16: 89.3
 // us, 6.53 TB/s (0.96); 64 sequences of 16 .. 2048 tokens, 32/32 heads, 8-bit:
 // 38.1 us, 5.46 TB/s (0.80: 2048 short segments); one sequence of 101 tokens:
-// 5.8 us; one stream with a window of 1024: 8.7 us.  The loop itself runs at the
-// copy rate; start (plan words, table entries, first copies: 2 us) and end
-// (warps' slack, merges within and between CTAs: 3 - 5 us) are what is left.
+// 5.8 us; one stream with a window of 1024: 8.7 us.  With the append, two
+// launches and one: 94.2 and 90.7 us (first batch), 45.1 and 42.0 (third).  The
+// loop itself runs at the copy rate; start (plan words, table entries, first
+// copies: 2 us) and end (warps' slack, merges within and between CTAs: 3 - 5 us)
+// are what is left.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -134,6 +141,11 @@ struct Params {
   const void* v_cache;
   const float* k_scale;
   const float* v_scale;
+  // fused append: the new tokens' rows, [num_seqs][num_kv_heads][head_dim], and
+  // the cache and scales again, to write
+  const void* new_rows[2];
+  uint8_t* codes[2];
+  float* scales[2];
   void* out;
   const int32_t* block_tables;
   const int32_t* context_lens;
@@ -613,7 +625,55 @@ __device__ __forceinline__ void warm_l2(const Params& p, const int4* mine, int l
                : "memory");
 }
 
-template <typename T, bool Q8, int D>
+// Where 8 bytes of row r of an 8-bit tile, columns 8 c .. 8 c + 7, sit in it.
+template <int D>
+__device__ __forceinline__ int q8_offset(int r, int c) {
+  return D == 128 ? r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8
+                  : (r >> 1) * 128 + ((((r & 1) * 4 + (c >> 1)) ^ (r >> 1)) << 4) + (c & 1) * 8;
+}
+
+// kv_append_q8 of one token, into a tile pair in shared memory (`tiles`: K, then
+// V) and the cache: row `off` of block `tile` of K (lanes 0 - 15) and V (16 -
+// 31), eight elements a lane.  `old`: this half's scale of the block.  Returns
+// its scale afterwards.
+template <typename T, int D>
+__device__ __forceinline__ float append_row(const Params& p, uint8_t* tiles, size_t tile, int off, float old,
+                                            const q8::Row8<T>& x) {
+  const int lane = threadIdx.x & 31, kv = lane >> 4, c = lane & 15;
+  const bool live = c < D / 8;
+  auto largest = [&](bool finite) {
+    uint32_t m = live ? x.top(finite) : 0;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+  };
+  uint32_t top = largest(false);
+  const uint32_t fine = largest(true);
+  if (top >= q8::Row8<T>::kInf) top = fine;
+  const float want = __uint_as_float(q8::pow2_bits(q8::scale_exponent(q8::Row8<T>::float_bits(top))));
+  const float scale = off > 0 ? fmaxf(old, want) : want;
+  const bool grows = off > 0 && scale > old;
+  uint8_t* to = tiles + kv * 16 * D;
+  uint8_t* cache = (kv ? p.codes[1] : p.codes[0]) + tile * kBlockSize * D + 8 * c;
+  if (live && grows) {
+    const float factor = old / scale;
+    for (int r = 0; r < off; ++r) {
+      uint2* at = reinterpret_cast<uint2*>(to + q8_offset<D>(r, c));
+      const uint2 y = q8::rescale8(*at, factor);
+      *at = y;
+      *reinterpret_cast<uint2*>(cache + r * D) = y;
+    }
+  }
+  if (live) {
+    const uint2 y = x.encode(1.f / scale);
+    *reinterpret_cast<uint2*>(to + q8_offset<D>(off, c)) = y;
+    *reinterpret_cast<uint2*>(cache + off * D) = y;
+  }
+  if (c == 0 && (off == 0 || grows)) (kv ? p.scales[1] : p.scales[0])[tile] = scale;
+  return scale;
+}
+
+template <typename T, bool Q8, int D, bool APPEND>
 __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const Params p) {
@@ -745,6 +805,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
   int get = 0, parity = 0, done = 0;  // done: blocks taken from the ring
   bool ok = true;
   float ks = 0.f, lvs = 0.f;  // lane j: K scale and log2 of V's of block 32 c + j
+  bool joined = false;        // a stage was written to (fused append)
   Piece<D>* tail = reinterpret_cast<Piece<D>*>(ring);
   if (lane == 0) head_pieces[warp].used = 0;
   bool has_tail = false;
@@ -771,6 +832,28 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
       f0 *= __uint_as_float(uint32_t(127 + __shfl_sync(0xffffffffu, qexp, 8 * t)) << 23);
       f1 *= __uint_as_float(uint32_t(127 + __shfl_sync(0xffffffffu, qexp, 8 * t + 4)) << 23);
     }
+    // the sequence's new token, K by lanes 0 - 15 and V by 16 - 31, its block
+    // (-1: not to be stored) and the block's scale, on their way while the
+    // segment runs.  A length that is not the planned one stores nothing (the
+    // plan cuts what the table cannot hold, and flags it).
+    q8::Row8<T> fresh;
+    int own = -1;
+    float old = 0.f;
+    if constexpr (APPEND) {
+      if (ends) {
+        if ((lane & 15) < D / 8)
+          fresh.load(static_cast<const T*>(lane >> 4 ? p.new_rows[1] : p.new_rows[0]) +
+                     (size_t(b) * Hkv + h) * D + 8 * (lane & 15));
+        const int length = p.context_lens[b];
+        const int phys = p.block_tables[size_t(b) * p.max_blocks + (seq.x - 1) / kBlockSize];
+        if (length != seq.x) {
+          if (length <= p.max_blocks * kBlockSize && lane == 0) dev::flag_status(p.status, kStatusPlan);
+        } else if (phys >= 0 && phys < p.num_blocks) {
+          own = phys * Hkv + h;
+          old = (lane >> 4 ? p.v_scale : p.k_scale)[own];
+        }
+      }
+    }
     float o[S::kSteps][4];
 #pragma unroll
     for (int m = 0; m < S::kSteps; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
@@ -796,6 +879,21 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return false;
+      float bks[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        lv[i] = 0.f;
+        bks[i] = 1.f;
+        if constexpr (Q8) {
+          if ((done & 31) == 0) {
+            ks = next_ks;
+            lvs = log2_scale(next_vs);
+          }
+          bks[i] = __shfl_sync(0xffffffffu, ks, done & 31);
+          lv[i] = __shfl_sync(0xffffffffu, lvs, done & 31);
+        }
+        ++done;
+      }
       // ---- S^T = K Q^T, each block's in two chains
       float s[N][4], s2[N][4];
 #pragma unroll
@@ -815,19 +913,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
       float top0 = -INFINITY, top1 = -INFINITY, high0 = -INFINITY, high1 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float c0 = f0, c1 = f1;
-        lv[i] = 0.f;
-        if constexpr (Q8) {
-          if ((done & 31) == 0) {
-            ks = next_ks;
-            lvs = log2_scale(next_vs);
-          }
-          const float k = __shfl_sync(0xffffffffu, ks, done & 31);
-          lv[i] = __shfl_sync(0xffffffffu, lvs, done & 31);
-          c0 *= k;
-          c1 *= k;
-        }
-        ++done;
+        const float c0 = Q8 ? f0 * bks[i] : f0, c1 = Q8 ? f1 * bks[i] : f1;
         x[i][0] = (s[i][0] + s2[i][0]) * c0;
         x[i][1] = (s[i][1] + s2[i][1]) * c1;
         x[i][2] = (s[i][2] + s2[i][2]) * c0;
@@ -922,15 +1008,52 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
       }
       v += N;
       // the stages are read: their next blocks
+      if constexpr (APPEND) {
+        // (writes to them come before the copies)
+        if (joined) dev::fence_proxy_async_smem();
+        joined = false;
+      }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < N; ++i)
         if (issued < count) issue();
       return true;
     };
+    // the new token into the sequence's last block, n - 1 blocks ahead of the
+    // next to be taken; its scales where take() looks for them
+    auto join = [&](int n) {
+      const int stage = get + n - 1 < ST ? get + n - 1 : get + n - 1 - ST;
+      ok = __all_sync(0xffffffffu, dev::mbar_wait_bounded(&full[stage], parity ^ int(stage < get), tmo, p.status));
+      if (!ok) return;
+      const float now = append_row<T, D>(p, ring + stage * S::kStage, size_t(own), (seq.x - 1) & 15, old, fresh);
+      const float now_k = __shfl_sync(0xffffffffu, now, 0), now_v = __shfl_sync(0xffffffffu, now, 16);
+      const int x = done + n - 1;
+      if (lane == (x & 31)) {
+        if (((done - 1) >> 5) == (x >> 5)) {
+          ks = now_k;
+          lvs = log2_scale(now_v);
+        } else {
+          next_ks = now_k;
+          next_vs = now_v;
+        }
+      }
+      joined = true;
+      __syncwarp();
+    };
     int left = run;
-    for (; left >= 2 && ok; left -= 2) take(std::integral_constant<int, 2>());
-    if (left && ok) take(std::integral_constant<int, 1>());
+    for (; left >= 2 && ok; left -= 2) {
+      if constexpr (APPEND) {
+        if (left == 2 && own >= 0) join(2);
+        if (!ok) break;
+      }
+      take(std::integral_constant<int, 2>());
+    }
+    if (left && ok) {
+      if constexpr (APPEND) {
+        if (own >= 0) join(1);
+      }
+      if (ok) take(std::integral_constant<int, 1>());
+    }
     if (!ok) break;
 
     // ---- end of the segment: sums over the 8 lanes that share a head
@@ -1175,8 +1298,14 @@ DeviceState g_dev[kMaxDevices];
 
 template <typename T, bool Q8, int D>
 cudaError_t configure() {
-  return cudaFuncSetAttribute(attend_kernel<T, Q8, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              int(Tiles<T, Q8, D>::kBytes));
+  const int bytes = int(Tiles<T, Q8, D>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if constexpr (Q8) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  }
+  return e;
 }
 
 int device_setup(int* ncta, const char* who) {
@@ -1234,6 +1363,8 @@ struct Call {
   void *out, *workspace;
   size_t workspace_bytes;
   void* stream;
+  bool append = false;
+  const void *k_new = nullptr, *v_new = nullptr;
 };
 
 int check_sizes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks,
@@ -1257,7 +1388,10 @@ cudaError_t launch_attend(cudaLaunchConfig_t cfg, const CUtensorMap& mk, const C
   cfg.gridDim = dim3(unsigned(p.ncta));
   cfg.blockDim = dim3(Tiles<T, Q8, D>::kThreads);
   cfg.dynamicSmemBytes = Tiles<T, Q8, D>::kBytes;
-  return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D>, mk, mv, p);
+  if constexpr (Q8) {
+    if (p.new_rows[0]) return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true>, mk, mv, p);
+  }
+  return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, false>, mk, mv, p);
 }
 
 template <typename T, bool Q8>
@@ -1287,7 +1421,8 @@ int entry(const Call& c) {
     if (!c.q || !c.k_cache || !c.v_cache || !c.block_tables || !c.out ||
         (c.q8 && (!c.k_scale || !c.v_scale)))
       return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
-    for (const void* ptr : {c.q, c.k_cache, c.v_cache, static_cast<const void*>(c.out)})
+    if (c.append && (!c.k_new || !c.v_new)) return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+    for (const void* ptr : {c.q, c.k_cache, c.v_cache, static_cast<const void*>(c.out), c.k_new, c.v_new})
       if (reinterpret_cast<uintptr_t>(ptr) & 15)
         return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", who);
     if (c.num_blocks <= 0 || double(c.num_blocks) * c.num_kv_heads * kBlockSize >= 2147483647.0)
@@ -1310,6 +1445,14 @@ int entry(const Call& c) {
   p.v_cache = c.v_cache;
   p.k_scale = c.k_scale;
   p.v_scale = c.v_scale;
+  if (c.append) {
+    p.new_rows[0] = c.k_new;
+    p.new_rows[1] = c.v_new;
+    p.codes[0] = static_cast<uint8_t*>(const_cast<void*>(c.k_cache));
+    p.codes[1] = static_cast<uint8_t*>(const_cast<void*>(c.v_cache));
+    p.scales[0] = const_cast<float*>(c.k_scale);
+    p.scales[1] = const_cast<float*>(c.v_scale);
+  }
   p.out = c.out;
   p.block_tables = c.block_tables;
   p.context_lens = c.context_lens;
@@ -1459,6 +1602,20 @@ PA_API int pa_paged_attention_decode_q8_run(
                         k_scale, v_scale, block_tables, context_lens, window, num_sinks, num_seqs,
                         num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_blocks, scale,
                         dtype, out, workspace, workspace_bytes, stream});
+}
+
+PA_API int pa_paged_attention_decode_q8_append_run(
+    const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+    float* k_scale, float* v_scale, const int32_t* block_tables, const int32_t* context_lens,
+    int window, int num_sinks, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  PA_TRACE("pa_paged_attention_decode_q8_append_run");
+  return window::entry({"paged_attention_decode_q8_append_run", Mode::kRunOnly, true, q, k_cache,
+                        v_cache, k_scale, v_scale, block_tables, context_lens, window, num_sinks,
+                        num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                        num_blocks, scale, dtype, out, workspace, workspace_bytes, stream, true,
+                        k_new, v_new});
 }
 
 }  // extern "C"

@@ -758,6 +758,44 @@ def prepare_decode_q8_run(q, k_cache, v_cache, k_scale, v_scale, block_tables, c
     return Prepared(capi.lib().pa_paged_attention_decode_q8_run, args, keep, dev)
 
 
+def _q8_append_run_args(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables,
+                        context_lens, window, num_sinks, scale, workspace, out, stream):
+    dev, args, out, keep = _window_args(q, k_cache, v_cache, (k_scale, v_scale), block_tables,
+                                        context_lens, window, num_sinks, scale, workspace, out,
+                                        stream)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        _cuda_contig(name, t, dev)
+    _require(k_new.dtype == v_new.dtype == q.dtype, "k_new / v_new must have q's dtype")
+    _require(k_new.shape == v_new.shape == (q.shape[0], k_cache.shape[1], k_cache.shape[3]),
+             "k_new, v_new must be [num_seqs, num_kv_heads, head_dim]")
+    args[1:1] = [C.c_void_p(k_new.data_ptr()), C.c_void_p(v_new.data_ptr())]
+    return dev, args, out, (k_new, v_new) + keep
+
+
+def paged_attention_decode_q8_append_run(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                         block_tables, context_lens, window: int, num_sinks: int,
+                                         scale: float, workspace: torch.Tensor, out=None,
+                                         stream=None) -> torch.Tensor:
+    """:func:`kv_append_q8` of one new token per sequence (row ``b`` of
+    ``k_new`` / ``v_new``, ``[B, Hkv, d]``, the token that ``context_lens[b]``
+    counts last) followed by :func:`paged_attention_decode_q8_run`, in one
+    launch, bit for bit.  The workspace must hold a plan for these lengths."""
+    dev, args, out, _ = _q8_append_run_args(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                            block_tables, context_lens, window, num_sinks, scale,
+                                            workspace, out, stream)
+    _call(dev, "pa_paged_attention_decode_q8_append_run", *args)
+    return out
+
+
+def prepare_decode_q8_append_run(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                 block_tables, context_lens, window: int, num_sinks: int,
+                                 scale: float, workspace, out, stream=None) -> Prepared:
+    dev, args, _, keep = _q8_append_run_args(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                             block_tables, context_lens, window, num_sinks, scale,
+                                             workspace, out, stream)
+    return Prepared(capi.lib().pa_paged_attention_decode_q8_append_run, args, keep, dev)
+
+
 def paged_attention_prefill_window_plan(context_lens: torch.Tensor, query_start: torch.Tensor,
                                         total_q: int, window: int, num_sinks: int,
                                         num_q_heads: int, num_kv_heads: int, head_dim: int,

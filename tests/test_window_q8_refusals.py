@@ -49,6 +49,25 @@ def test_q8_decode_refuses_what_only_it_has(lib):
 
 
 @pytest.mark.parametrize("kw,status", [
+    (dict(window=-1), 1), (dict(dtype=0), 2), (dict(dtype=7), 2), (dict(d=96), 2), (dict(hq=18), 2),
+    (dict(nb=0), 1), (dict(q=None), 1), (dict(kn=None), 1), (dict(vn=None), 1), (dict(kn=264), 1),
+    (dict(vn=264), 1), (dict(vc=264), 1), (dict(ks=None), 1), (dict(ws=None), 1), (dict(bytes=64), 1),
+])
+def test_append_run_refuses(lib, kw, status):
+    a = dict(q=256, kn=256, vn=256, kc=256, vc=256, ks=256, vs=256, bt=256, cl=256, window=8, sinks=2,
+             num_seqs=2, hq=8, hkv=2, d=128, mb=4, nb=8, scale=0.125, dtype=2, out=256, ws=256,
+             bytes=1 << 30, stream=None)
+    a.update(kw)
+    assert lib.pa_paged_attention_decode_q8_append_run(*a.values()) == status
+    assert lib.pa_last_error()
+
+
+def test_append_run_without_sequences(lib):
+    assert lib.pa_paged_attention_decode_q8_append_run(
+        *[None] * 9, 8, 2, 0, 8, 2, 128, 4, 8, 0.125, 2, None, None, 0, None) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
     (dict(window=-1), 1), (dict(sinks=-2), 1), (dict(d=80), 2), (dict(cl=None), 1),
     (dict(ws=None), 1), (dict(bytes=8), 1), (dict(hq=7), 1),
 ])
