@@ -4,10 +4,17 @@ Argument marshalling only: each function checks shapes / dtypes / devices of
 the torch tensors, passes their raw pointers and the current CUDA stream to the
 C ABI, and raises ``PagedAttnError`` on a non-zero status.  All computation
 happens in the library's kernels.
+
+``stream=`` puts a call's work on that stream (default: the current one).  What
+the call allocates for itself (an output or a workspace not passed in) is then
+that stream's memory, and the output may be used on the current stream too once
+that has been made to wait; ordering the inputs is the caller's business, as
+everywhere in torch.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 
 import torch
@@ -31,6 +38,26 @@ def _stream(device: torch.device, stream=None) -> int:
         return _raw_stream(device.index)     # the current stream without a Stream object around it
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return s.cuda_stream
+
+
+def _memory_of(stream, device: torch.device):
+    """The context to allocate in for work on ``stream``: memory let go of when
+    the call returns must come back to that stream, not to the current one,
+    whose next allocation could be written while the work still runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _out_like(q: torch.Tensor, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty_like(q)
+    with _memory_of(stream, q.device):
+        out = torch.empty_like(q)
+    out.record_stream(torch.cuda.current_stream(q.device))   # (the caller reads it there)
+    return out
 
 
 def _require(cond: bool, msg: str) -> None:
@@ -148,7 +175,7 @@ def paged_attention_decode_append_run(q, k_new, v_new, slot_mapping, k_cache, v_
     dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, context_lens)
     _append_args(q, k_new, v_new, slot_mapping, hkv, d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     _cuda_contig("workspace", workspace, dev)
@@ -163,11 +190,12 @@ def paged_attention_decode_append_run(q, k_new, v_new, slot_mapping, k_cache, v_
 def _decode(fn, q, k_cache, v_cache, block_tables, context_lens, scale, out, workspace, stream):
     dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, context_lens)
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     if workspace is None:
-        workspace = alloc_workspace(b, hq, hkv, d, mb, dev)
+        with _memory_of(stream, dev):
+            workspace = alloc_workspace(b, hq, hkv, d, mb, dev)
     _cuda_contig("workspace", workspace, dev)
     capi.check(fn(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
@@ -184,7 +212,7 @@ def paged_attention_decode_noalloc(q, k_cache, v_cache, block_tables, context_le
     (calls on one device share it, so they must not overlap on the GPU)."""
     dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, context_lens)
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     capi.check(capi.lib().pa_paged_attention_decode_noalloc(
@@ -334,12 +362,13 @@ def paged_attention_decode_shared_prefix(q, k_cache, v_cache, block_tables, cont
     parts are merged."""
     dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, context_lens)
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     if workspace is None:
         n = shared_prefix_workspace_size(b, hq, hkv, d, mb)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        with _memory_of(stream, dev):
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
     _cuda_contig("workspace", workspace, dev)
     capi.check(getattr(capi.lib(), _entry)(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
@@ -402,7 +431,7 @@ def paged_attention_decode_grouped_prefix_run(q, k_cache, v_cache, block_tables,
     dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, None)
     g = _group_args(group_start, group_prefix_blocks, b, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     _cuda_contig("workspace", workspace, dev)
@@ -424,12 +453,13 @@ def paged_attention_decode_grouped_prefix(q, k_cache, v_cache, block_tables, con
     dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, context_lens)
     g = _group_args(group_start, group_prefix_blocks, b, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     if workspace is None:
         n = grouped_prefix_workspace_size(b, hq, hkv, d, mb)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        with _memory_of(stream, dev):
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
     _cuda_contig("workspace", workspace, dev)
     capi.check(capi.lib().pa_paged_attention_decode_grouped_prefix(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
@@ -449,7 +479,7 @@ def paged_attention_decode_shared_prefix_append_run(q, k_new, v_new, slot_mappin
     dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, context_lens)
     _append_args(q, k_new, v_new, slot_mapping, hkv, d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     _cuda_contig("workspace", workspace, dev)
@@ -473,7 +503,7 @@ def paged_attention_decode_grouped_prefix_append_run(q, k_new, v_new, slot_mappi
     _append_args(q, k_new, v_new, slot_mapping, hkv, d)
     g = _group_args(group_start, group_prefix_blocks, b, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     _cuda_contig("workspace", workspace, dev)
@@ -561,11 +591,12 @@ def paged_attention_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
              "block_tables must be [num_seqs, max_blocks_per_seq]")
     _require(query_start.shape == (b + 1,), "query_start must be [num_seqs + 1]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     if workspace is None:
-        workspace = alloc_prefill_workspace(b, total_q, hq, hkv, d, dev)
+        with _memory_of(stream, dev):
+            workspace = alloc_prefill_workspace(b, total_q, hq, hkv, d, dev)
     _cuda_contig("workspace", workspace, dev)
     capi.check(getattr(capi.lib(), _entry)(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
@@ -666,11 +697,12 @@ def _window_args(q, k_cache, v_cache, scales, block_tables, context_lens, window
                  "context_lens must be int32 [num_seqs]")
         mb = block_tables.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     if workspace is None:
-        workspace = alloc_window_workspace(b, hq, hkv, d, mb, dev)
+        with _memory_of(stream, dev):
+            workspace = alloc_window_workspace(b, hq, hkv, d, mb, dev)
     _cuda_contig("workspace", workspace, dev)
     window, num_sinks = _window_ints(window, num_sinks)
     ptrs = [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()]
@@ -855,11 +887,12 @@ def paged_attention_prefill_window(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     _require(query_start.dtype == torch.int32 and query_start.shape == (b + 1,),
              "query_start must be int32 [num_seqs + 1]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _out_like(q, stream)
     _cuda_contig("out", out, dev)
     _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
     if workspace is None:
-        workspace = alloc_prefill_workspace(b, q.shape[0], hq, hkv, d, dev)
+        with _memory_of(stream, dev):
+            workspace = alloc_prefill_workspace(b, q.shape[0], hq, hkv, d, dev)
     _cuda_contig("workspace", workspace, dev)
     window, num_sinks = _window_ints(window, num_sinks)
     _call(dev, _entry, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
