@@ -677,9 +677,12 @@ def _q8_cache_args(k_cache, v_cache, k_scale, v_scale, dev):
 
 
 def _window_args(q, k_cache, v_cache, scales, block_tables, context_lens, window, num_sinks, scale,
-                 workspace, out, stream):
-    """Checks a windowed decode's operands (scales None: a cache of q's dtype);
+                 workspace, out, stream, planned):
+    """Checks a windowed decode's operands (scales None: a cache of q's dtype;
+    planned: the workspace holds the plan, so the caller has it);
     returns (device, C arguments, out, tensors to keep)."""
+    # (memory fresh from the allocator may hold an earlier step's plan)
+    _require(not planned or workspace is not None, "a run needs the workspace that holds its plan")
     dev = q.device
     if scales is None:
         dev, b, hq, hkv, d, nb, mb = _decode_args(q, k_cache, v_cache, block_tables, context_lens)
@@ -727,7 +730,7 @@ def paged_attention_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     visible token are not read, nor are their table entries, so they may have
     been freed.  Plans and runs in one call."""
     dev, args, out, _ = _window_args(q, k_cache, v_cache, None, block_tables, context_lens, window,
-                                     num_sinks, scale, workspace, out, stream)
+                                     num_sinks, scale, workspace, out, stream, False)
     _call(dev, "pa_paged_attention_decode_window", *args)
     return out
 
@@ -739,7 +742,7 @@ def paged_attention_decode_window_run(q, k_cache, v_cache, block_tables, context
     :func:`paged_attention_decode_window_plan` filled for the same lengths,
     window and first tokens."""
     dev, args, out, _ = _window_args(q, k_cache, v_cache, None, block_tables, context_lens, window,
-                                     num_sinks, scale, workspace, out, stream)
+                                     num_sinks, scale, workspace, out, stream, True)
     _call(dev, "pa_paged_attention_decode_window_run", *args)
     return out
 
@@ -748,7 +751,7 @@ def prepare_decode_window_run(q, k_cache, v_cache, block_tables, context_lens, w
                               num_sinks: int, scale: float, workspace, out,
                               stream=None) -> Prepared:
     dev, args, _, keep = _window_args(q, k_cache, v_cache, None, block_tables, context_lens,
-                                      window, num_sinks, scale, workspace, out, stream)
+                                      window, num_sinks, scale, workspace, out, stream, True)
     return Prepared(capi.lib().pa_paged_attention_decode_window_run, args, keep, dev)
 
 
@@ -764,7 +767,7 @@ def paged_attention_decode_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     is multiplied by (:func:`kv_append_q8` writes both); ``window`` 0 sees the
     whole context.  ``q`` is float16 or bfloat16."""
     dev, args, out, _ = _window_args(q, k_cache, v_cache, (k_scale, v_scale), block_tables,
-                                     context_lens, window, num_sinks, scale, workspace, out, stream)
+                                     context_lens, window, num_sinks, scale, workspace, out, stream, False)
     _call(dev, "pa_paged_attention_decode_q8", *args)
     return out
 
@@ -776,7 +779,7 @@ def paged_attention_decode_q8_run(q, k_cache, v_cache, k_scale, v_scale, block_t
     :func:`paged_attention_decode_window_plan` filled for the same lengths,
     window and first tokens."""
     dev, args, out, _ = _window_args(q, k_cache, v_cache, (k_scale, v_scale), block_tables,
-                                     context_lens, window, num_sinks, scale, workspace, out, stream)
+                                     context_lens, window, num_sinks, scale, workspace, out, stream, True)
     _call(dev, "pa_paged_attention_decode_q8_run", *args)
     return out
 
@@ -786,7 +789,7 @@ def prepare_decode_q8_run(q, k_cache, v_cache, k_scale, v_scale, block_tables, c
                           stream=None) -> Prepared:
     dev, args, _, keep = _window_args(q, k_cache, v_cache, (k_scale, v_scale), block_tables,
                                       context_lens, window, num_sinks, scale, workspace, out,
-                                      stream)
+                                      stream, True)
     return Prepared(capi.lib().pa_paged_attention_decode_q8_run, args, keep, dev)
 
 
@@ -794,7 +797,7 @@ def _q8_append_run_args(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, blo
                         context_lens, window, num_sinks, scale, workspace, out, stream):
     dev, args, out, keep = _window_args(q, k_cache, v_cache, (k_scale, v_scale), block_tables,
                                         context_lens, window, num_sinks, scale, workspace, out,
-                                        stream)
+                                        stream, True)
     for name, t in (("k_new", k_new), ("v_new", v_new)):
         _cuda_contig(name, t, dev)
     _require(k_new.dtype == v_new.dtype == q.dtype, "k_new / v_new must have q's dtype")
@@ -860,6 +863,8 @@ def paged_attention_prefill_window_run(q, k_cache, v_cache, block_tables, contex
     """:func:`paged_attention_prefill_window` over a workspace that
     :func:`paged_attention_prefill_window_plan` filled for the same chunks,
     window and first tokens: the attention kernel only."""
+    # (float32 has no plan)
+    _require(workspace is not None or q.dtype == torch.float32, "a run needs the workspace that holds its plan")
     return paged_attention_prefill_window(q, k_cache, v_cache, block_tables, context_lens,
                                           query_start, window, num_sinks, scale, out=out,
                                           workspace=workspace, stream=stream,
