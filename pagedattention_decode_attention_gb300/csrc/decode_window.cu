@@ -98,7 +98,7 @@ constexpr int kMinPlaces = 32;       // places on the line a CTA takes at least
 // 44.1)
 constexpr int kSegmentCost = 2;
 constexpr int kFillAt = 16;          // where in its 32 blocks a warp reads the next 32's entries
-constexpr float kRescale = 8.f;      // log2 by which a score may exceed the reference
+constexpr float kRescale = 8.f;      // log2 by which a score may exceed the reference (Tiles::kLift counts on it)
 constexpr int kPlanThreads = 1024;
 
 // Workspace header words: what the plan was made for; places in all, places
@@ -379,13 +379,23 @@ template <typename T, bool Q8, int D>
 struct Tiles {
   using Mm = dev::Mma<typename std::conditional<Q8, __half, T>::type>;
   static constexpr int kElem = Q8 ? 1 : 2;
-  // The softmax's weights enter V's product rounded to its 16-bit type.  f16's
-  // 2^-12 is under the rounding of any output; bf16's 2^-9 is as large as that
-  // of a bf16 output, so there what it leaves over goes through a second
-  // product: the windowed batch's output is 0.0017 (one rounding) from 64-bit
-  // arithmetic, 0.0023 without, for 89.4 us, 89.2 without (the tensor cores
-  // idle at 9 %).
+  // The softmax's weights enter V's product rounded to its 16-bit type: half a
+  // step, f16's 2^-11 and bf16's 2^-8 relative, as much as the rounding of an
+  // output of that type.  For f16 (and an 8-bit cache's f16 weights) that is
+  // accepted: outputs of the f16 window case are 1.78e-4 from 64-bit
+  // arithmetic on average, 1.60e-4 with weights in 32 bits.  For bf16 what the
+  // rounding leaves over goes through a second product: the windowed batch's
+  // output is 0.0017 (one rounding) from 64-bit arithmetic, 0.0023 without, for
+  // 89.4 us, 89.2 without (the tensor cores idle at 9 %).
   static constexpr bool kTwoParts = !Q8 && std::is_same<T, __nv_bfloat16>::value;
+  // f16 weights are 2^(x - reference + kLift).  The reference may be the
+  // sequence's largest score (a first token that takes most of the softmax),
+  // and then everything else lies under it: without the lift f16's full
+  // precision ends at 2^-14 of it and its range at 2^-25, so that thousands of
+  // small weights lose their bits or all of their share.  A score exceeds the
+  // reference by kRescale at most: 2^(7 + 8) stays under f16's 65504.  bf16 has
+  // the range of 32 bits.
+  static constexpr float kLift = Q8 || std::is_same<T, __half>::value ? 7.f : 0.f;
   static constexpr int kRowBytes = D * kElem;               // of a token's row
   // a copy box is 128 bytes wide: half a row, a row, or two tokens' rows
   static constexpr int kBoxes = kRowBytes / 128 > 1 ? kRowBytes / 128 : 1;
@@ -965,7 +975,8 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
           o[m][3] *= a1;
         }
       }
-      const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+      // (the softmax's sum is lifted like the weights, so the lift divides out)
+      const float r0 = m0 == -INFINITY ? 0.f : m0 - S::kLift, r1 = m1 == -INFINITY ? 0.f : m1 - S::kLift;
       uint32_t b0[N], b1[N], e0[N], e1[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -975,9 +986,10 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
         l1 += p1 + p3;
         if constexpr (Q8) {
           // the weights carry the block's value scale: 2^(x + log2 scale),
-          // kept near 1 by a reference of their own, so f16 holds them
+          // kept near 2^kLift by a reference of their own, so f16 holds them
           // whatever the scales are
-          const float d0 = lv[i] - (w0 == -INFINITY ? 0.f : w0), d1 = lv[i] - (w1 == -INFINITY ? 0.f : w1);
+          const float d0 = lv[i] - (w0 == -INFINITY ? 0.f : w0 - S::kLift);
+          const float d1 = lv[i] - (w1 == -INFINITY ? 0.f : w1 - S::kLift);
           p0 = dev::fast_exp2(x[i][0] + d0);
           p1 = dev::fast_exp2(x[i][1] + d1);
           p2 = dev::fast_exp2(x[i][2] + d0);
