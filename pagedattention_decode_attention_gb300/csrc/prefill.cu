@@ -414,6 +414,20 @@ struct Smem {
       1024 /* alignment slack */ + size_t(kStages) * kStageBytes + 2 * kStages * 8 + 64;
 };
 
+// Weights enter the product with V rounded to the input type (half a step,
+// 2^-11 in f16, 2^-8 in bf16, each: bf16 outputs of a windowed batch are 0.0023
+// from 64-bit arithmetic, one rounding alone is 0.0017; the second product that
+// would take up the rest costs half of this kernel's tensor work again).  With a
+// window, f16 weights are 2^(x - reference + lift): the reference may be a first
+// token that takes most of the row's softmax, and the others, up to thousands,
+// would fall among f16's subnormals (from 2^-14 of it on) or vanish (2^-25).  A
+// score exceeds the reference by 2^8 at most (kTcRescale): 2^15 stays under
+// f16's 65504.  The rows' sums are lifted alike, so the lift divides out.
+template <typename T, bool WIN>
+__host__ __device__ constexpr float weight_lift() {
+  return WIN && std::is_same<T, __half>::value ? 7.f : 0.f;
+}
+
 // One work item as every thread of the CTA holds it.
 struct Item {
   int b, qb, first, nblk, s, ns, slot, grp, ctx, g;
@@ -431,6 +445,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   constexpr int KT = D / 16;      // 16-wide steps along head_dim
   constexpr int ND = D / 8;       // 8-wide output column tiles
   constexpr int HALVES = D / 64;  // 128-byte TMA boxes per tile row
+  constexpr float kLift = weight_lift<T, WIN>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -632,8 +647,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 2));
       const float mna = fmaxf(ma, bma), mnb = fmaxf(mb, bmb);
       // a row with nothing unmasked yet keeps m = -inf: use 0 as its reference
-      const float ra0 = mna == -INFINITY ? 0.f : mna, rb0 = mnb == -INFINITY ? 0.f : mnb;
-      const float ala = dev::fast_exp2(ma - ra0), alb = dev::fast_exp2(mb - rb0);
+      const float ua = mna == -INFINITY ? 0.f : mna, ub = mnb == -INFINITY ? 0.f : mnb;
+      const float ala = dev::fast_exp2(ma - ua), alb = dev::fast_exp2(mb - ub);
+      const float ra0 = ua - kLift, rb0 = ub - kLift;  // the weights' reference
       ma = mna;
       mb = mnb;
       const uint32_t pa01 = M::pack(dev::fast_exp2(xa[0] - ra0), dev::fast_exp2(xa[1] - ra0));
@@ -744,8 +760,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         *reinterpret_cast<float2*>(pb + c) = make_float2(o[nd][2] * ib, o[nd][3] * ib);
       }
       if (tq == 0) {
-        p.part_lse[base + gq] = la > 0.f ? ma + log2f(la) : -INFINITY;
-        p.part_lse[base + gq + 8] = lb > 0.f ? mb + log2f(lb) : -INFINITY;
+        p.part_lse[base + gq] = la > 0.f ? ma + log2f(la) - kLift : -INFINITY;
+        p.part_lse[base + gq + 8] = lb > 0.f ? mb + log2f(lb) - kLift : -INFINITY;
       }
       // publish (every warp's rows), count; the CTA completing (group, g) merges
       __syncthreads();
@@ -969,6 +985,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                       const __grid_constant__ CUtensorMap tmap_o, const Params p) {
   constexpr int D = 128;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr float kLift = weight_lift<T, WIN>();
   using M = dev::Mma<T>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1459,7 +1476,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // P = 2^(s scale log2 e - ref) in the input type, over S's first 64
         // columns; masked columns (-inf) give 0.  A row with nothing visible
         // yet (ref -inf) uses 0 as its reference: every p is 0 then.
-        const float nref = mref == -INFINITY ? 0.f : -mref;
+        const float nref = mref == -INFINITY ? 0.f : kLift - mref;
         float acc[4][2] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -1539,7 +1556,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int e = 0; e < 8; ++e) f[e] = __float_as_uint(__uint_as_float(ov[c][8 * i + e]) * inv);
               dev::st_global_v8(prow + 32 * c + 8 * i, f);
             }
-          p.part_lse[pbase + it.s * pstride] = l > 0.f ? mref + log2f(l) : -INFINITY;
+          p.part_lse[pbase + it.s * pstride] = l > 0.f ? mref + log2f(l) - kLift : -INFINITY;
         }
         // every participating warp's rows are written (a lone first tile
         // arrives for the absent second one too); one thread counts the split
