@@ -440,8 +440,9 @@ PA_API int pa_paged_attention_prefill(const void* q, const void* k_cache, const 
  * and sets the status word (pa_check_status returns PA_ERR_INVALID_ARG);
  * changed lengths under the same sizes are not detected and give unspecified
  * output.  Runs may follow one plan any number of times, on any caches,
- * queries and outputs; each leaves the workspace ready for the next.  After
- * a run that timed out, plan again.  For PA_F32 the plan does nothing and
+ * queries and outputs; each leaves the workspace ready for the next.  A run
+ * that timed out voids the plan (later runs do nothing and set the status
+ * word): plan again.  For PA_F32 the plan does nothing and
  * the run is the whole call.
  * ---------------------------------------------------------------------- */
 PA_API int pa_paged_attention_prefill_plan(const int32_t* context_lens,
@@ -476,7 +477,9 @@ PA_API int pa_paged_attention_prefill_run(const void* q, const void* k_cache, co
  * _plan reads context_lens (device) and writes the work list into the
  * workspace; any number of _run calls may follow it in stream order with the
  * same sizes, window and num_sinks, over any caches (16-bit and, with
- * pa_paged_attention_decode_q8_run, 8-bit).  A run uses the lengths the plan
+ * pa_paged_attention_decode_q8_run, 8-bit).  A run that timed out voids the
+ * plan: later runs do nothing and set the status word until _plan is called
+ * again.  A run uses the lengths the plan
  * read and ignores context_lens' later contents.  A run whose workspace holds no plan
  * for its sizes does nothing and sets the status word (pa_check_status
  * returns PA_ERR_INVALID_ARG).  The workspace

@@ -713,12 +713,13 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
   const int4 hdr = *reinterpret_cast<const int4*>(p.header);
   const int4* mine = p.starts + 2 * (blockIdx.x * kWarps + warp);
   const int4 start = mine[0], start_seq = mine[1];
-  if (hdr.x != p.signature) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) dev::flag_status(p.status, kStatusPlan);
-    return;
-  }
+  // (a CTA whose wait runs out voids the plan while others may still be
+  // starting: a warp that finds none takes no blocks, and its CTA gives up
+  // where the warps meet)
+  const bool planned = __all_sync(0xffffffffu, hdr.x == p.signature);
+  if (!planned && blockIdx.x == 0 && threadIdx.x == 0) dev::flag_status(p.status, kStatusPlan);
   const int total = hdr.y, share = hdr.z;
-  if (hdr.w) {
+  if (planned && hdr.w) {
     // rows of sequences without tokens are zero
     for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x)
       if (p.seqs[b].y == 0) {
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
         for (int i = threadIdx.x; i < p.num_q_heads * D / 8; i += kThreads) row[i] = make_uint4(0, 0, 0, 0);
       }
   }
-  const int count = start.w;  // this warp's blocks
+  const int count = planned ? start.w : 0;  // this warp's blocks
   if ((long long)blockIdx.x * share >= total) return;
 
   const unsigned long long tmo = p.timeout_ns;
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
   int b = start.x, h = start.y, v = start.z;
   int4 seq = start_seq;
   int get = 0, parity = 0, done = 0;  // done: blocks taken from the ring
-  bool ok = true;
+  bool ok = planned;
   float ks = 0.f, lvs = 0.f;  // lane j: K scale and log2 of V's of block 32 c + j
   bool joined = false;        // a stage was written to (fused append)
   Piece<D>* tail = reinterpret_cast<Piece<D>*>(ring);
@@ -1136,7 +1137,12 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
   int *s_open = s_tail + kWarps, *s_merge = s_open + 2;
   if (lane == 0) s_tail[warp] = has_tail;
   if (threadIdx.x < 2) s_open[threadIdx.x] = s_merge[threadIdx.x] = -1;
-  if (!__syncthreads_and(ok)) return;
+  if (!__syncthreads_and(ok)) {
+    // a wait ran out: the pieces of this CTA are missing, and those of others
+    // stay counted (`arrivals`), so no later run may use the plan
+    if (threadIdx.x == 0 && planned) atomicExch(&p.header[kHdrSignature], 0);
+    return;
+  }
   // bit w: warp w has a last piece, a first piece, a first piece that ends its
   // sequence
   const uint32_t tails = __ballot_sync(0xffffffffu, lane < kWarps && s_tail[lane % kWarps]);

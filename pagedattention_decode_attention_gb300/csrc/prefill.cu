@@ -428,6 +428,15 @@ __host__ __device__ constexpr float weight_lift() {
   return WIN && std::is_same<T, __half>::value ? 7.f : 0.f;
 }
 
+// What the claiming thread hands out when nothing is left (or a wait ran out).
+// It alone compares with the plan's total: another CTA may void the plan while
+// this one starts, and a CTA's threads must not differ over that.
+constexpr int kNoItem = 0x7FFFFFFF;
+
+// After a wait that ran out the counters (items claimed, CTAs finished, splits
+// arrived) are not what a run expects to find: none may use the plan again.
+__device__ __forceinline__ void void_plan(const Params& p) { atomicExch(&p.header[kHdrSignature], 0); }
+
 // One work item as every thread of the CTA holds it.
 struct Item {
   int b, qb, first, nblk, s, ns, slot, grp, ctx, g;
@@ -527,14 +536,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     if (producer) {
       // the first item of every CTA is dealt statically, the rest come from
       // the counter
-      *s_claim = first_claim ? int(blockIdx.x)
-                             : int(gridDim.x) + atomicAdd(&p.header[kHdrNext], 1);
+      const int x = first_claim ? int(blockIdx.x)
+                                : int(gridDim.x) + atomicAdd(&p.header[kHdrNext], 1);
+      *s_claim = x < total ? x : kNoItem;
     }
     first_claim = false;
     __syncthreads();
     const int x = *s_claim;
     __syncthreads();
-    if (x >= total) break;
+    if (x == kNoItem) break;
     Item it;
     {
       const int4 u0 = p.units[2 * (x / Hkv)], u1 = p.units[2 * (x / Hkv) + 1];
@@ -838,9 +848,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   }
   if (!ok) {
     // a wait ran out: let this CTA's copies in flight land, then give up
-    if (producer)
+    if (producer) {
       for (int k = kc; k < ik; ++k)
         dev::mbar_wait_bounded(&full[k % kStages], (k / kStages) & 1, tmo, p.status);
+      void_plan(p);
+    }
     return;
   }
   // the last CTA to finish returns the counters to zero
@@ -1106,13 +1118,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (n >= 2)
           ok = PF_WAIT(0, dev::mbar_wait_bounded(&item_empty[slot], ((n >> 1) - 1) & 1, tmo, p.status));
         x = n == 0 ? int(blockIdx.x) : int(gridDim.x) + atomicAdd(&p.header[kHdrNext], 1);
-        if (!ok) x = total;  // stop every role
+        if (!ok || x >= total) x = kNoItem;  // stop every role
         s_item[slot] = x;
         dev::mbar_arrive(&item_full[slot]);
       }
       x = __shfl_sync(0xffffffffu, x, 0);
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (x >= total) break;
+      if (x == kNoItem) break;
       const Item it = decode(x);
       if (lane == 0) {
         if (n >= 1) ok = PF_WAIT(1, dev::mbar_wait_bounded(q_empty, (n - 1) & 1, tmo, p.status));
@@ -1214,7 +1226,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int x = *reinterpret_cast<volatile int*>(&s_item[slot]);
       __syncwarp();
       if (leader) dev::mbar_arrive(&item_empty[slot]);
-      if (x >= total) break;
+      if (x == kNoItem) break;
       const Item it = decode(x);
       const int tiles = it.two ? 2 : 1;
       ok = PF_WAIT(1, wait(q_full, n & 1));
@@ -1352,7 +1364,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int x = *reinterpret_cast<volatile int*>(&s_item[slot]);
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(&item_empty[slot]);
-      if (x >= total) break;
+      if (x == kNoItem) break;
       const Item it = decode(x);
       // a split item's rows are merged here unless the caller merges them
       const bool merge_here = it.ns > 1 && !p.defer_merge;
@@ -1704,6 +1716,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     dev::tmem_dealloc(tmem, kTcCols);
   }
   PF_STAMP(3);
+  if (threadIdx.x == 0 && planned && !all_ok) void_plan(p);
   if (threadIdx.x == 0 && planned && all_ok) {
     __threadfence();
     if (atomicAdd(&p.header[kHdrDone], 1) == int(gridDim.x) - 1) {
