@@ -428,6 +428,31 @@ __host__ __device__ constexpr float weight_lift() {
   return WIN && std::is_same<T, __half>::value ? 7.f : 0.f;
 }
 
+// dev::mbar_wait_bounded of a whole warp, which goes on or gives up as one: a
+// lane that left by itself would leave the others waiting for it at the next
+// vote, shuffle, product or tensor-memory access.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, int parity, uint64_t limit_ns, unsigned* status) {
+  return __all_sync(0xffffffffu, dev::mbar_wait_bounded(bar, uint32_t(parity), limit_ns, status));
+}
+
+// The same for a wait per tile or block: the vote is part of each poll, and the
+// clock is read after eight (37 rows over 254 tokens 13.4 us, as without any
+// vote; 14.3 with wait_warp, 14.1 with a clock read per poll).
+__device__ __forceinline__ bool wait_warp_hot(uint64_t* bar, int parity, uint64_t limit_ns, unsigned* status) {
+  if (__all_sync(0xffffffffu, dev::mbar_try_wait(bar, uint32_t(parity)))) return true;
+  for (uint64_t start = 0;;) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i)
+      if (__all_sync(0xffffffffu, dev::mbar_try_wait(bar, uint32_t(parity)))) return true;
+    const uint64_t now = dev::global_timer_ns();
+    if (start == 0) start = now;
+    if (__any_sync(0xffffffffu, now - start > limit_ns)) {
+      dev::flag_status(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
 // What the claiming thread hands out when nothing is left (or a wait ran out).
 // It alone compares with the plan's total: another CTA may void the plan while
 // this one starts, and a CTA's threads must not differ over that.
@@ -604,7 +629,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 
     for (int j = 0; j < it.nblk; ++j, ++kc) {
       const int st = kc % kStages;
-      if (!dev::mbar_wait_bounded(&full[st], (kc / kStages) & 1, tmo, p.status)) {
+      if (!wait_warp_hot(&full[st], (kc / kStages) & 1, tmo, p.status)) {
         ok = false;
         break;
       }
@@ -1211,9 +1236,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint64_t desc_k = dev::smem_desc_sw128(sbase + TcSmem::kK, 16, 1024);
     const uint64_t desc_v = dev::smem_desc_sw128(sbase + TcSmem::kV, TcSmem::kChunk, 1024);
     // every lane waits; the warp goes on only if every lane saw the phase
-    auto wait = [&](uint64_t* bar, int parity) -> bool {
-      return __all_sync(0xffffffffu, dev::mbar_wait_bounded(bar, uint32_t(parity), tmo, p.status));
-    };
+    auto wait = [&](uint64_t* bar, int parity) -> bool { return wait_warp(bar, parity, tmo, p.status); };
     int kt = 0;          // K / V tiles consumed
     int pv[2] = {0, 0};  // P V products issued per query tile
     PF_DECL;
@@ -1349,6 +1372,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lanes + 256 + w * 128;
     const float sl2 = p.scale_log2;       // > 0 on this path
+    auto wait = [&](uint64_t* bar, int parity) -> bool { return wait_warp(bar, parity, tmo, p.status); };
+    auto hot = [&](uint64_t* bar, int parity) -> bool { return wait_warp_hot(bar, parity, tmo, p.status); };
     int cnt = 0;                          // tiles of this group so far
     int sfw = 0;                          // waits on s_full[w] (two-tile items)
     int sbw[2] = {0, 0};                  // waits on sb_full[b] (one-tile items, group 0)
@@ -1357,7 +1382,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     PF_DECL;
     for (int n = 0;; ++n) {
       const int slot = n & 1;
-      if (!PF_WAIT(0, dev::mbar_wait_bounded(&item_full[slot], (n >> 1) & 1, tmo, p.status))) {
+      if (!PF_WAIT(0, wait(&item_full[slot], (n >> 1) & 1))) {
         ok = false;
         break;
       }
@@ -1372,7 +1397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // no rows here; still pass this item's merge phase with group 0, so
         // that no later wait can take an old phase for its own
         if (merge_here) {
-          if (!dev::mbar_wait_bounded(merge_go, merges & 1, tmo, p.status)) {
+          if (!wait(merge_go, merges & 1)) {
             ok = false;
             break;
           }
@@ -1401,7 +1426,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int buf = it.two ? w : (j & 1);
         uint64_t* sbar = it.two ? &s_full[w] : &sb_full[buf];
         const int spar = it.two ? (sfw++ & 1) : (sbw[buf]++ & 1);
-        if (!PF_WAIT(1, dev::mbar_wait_bounded(sbar, uint32_t(spar), tmo, p.status))) {
+        if (!PF_WAIT(1, hot(sbar, spar))) {
           ok = false;
           break;
         }
@@ -1441,7 +1466,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         auto wait_prev_pv = [&]() -> bool {
           if (pv_waited) return true;
           pv_waited = true;
-          if (!PF_WAIT(3, dev::mbar_wait_bounded(&pv_done[w], (cnt - 1) & 1, tmo, p.status)))
+          if (!PF_WAIT(3, hot(&pv_done[w], (cnt - 1) & 1)))
             return false;
           dev::tc_fence_after_sync();
           return true;
@@ -1515,7 +1540,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // rows of the last V tile past the context or past the loaded
           // blocks (and those before every row's window) are zeroed, so
           // whatever bits they hold meet only p = 0
-          if (!dev::mbar_wait_bounded(&v_full[kt & 1], (kt >> 1) & 1, tmo, p.status)) ok = false;
+          if (!wait(&v_full[kt & 1], (kt >> 1) & 1)) ok = false;
           if (ok && (t0 + r >= bound || (WIN && t0 + r < none && t0 + r >= p.num_sinks))) {
             // (each row's 16-byte chunks in an order rotated by the row, so
             // the warp's 32 rows, 128 bytes apart, do not all hit one bank)
@@ -1537,7 +1562,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (!ok) break;
       // O_w is complete once the last P V has finished: normalise and write
-      if (!PF_WAIT(3, dev::mbar_wait_bounded(&pv_done[w], (cnt - 1) & 1, tmo, p.status))) {
+      if (!PF_WAIT(3, hot(&pv_done[w], (cnt - 1) & 1))) {
         ok = false;
         break;
       }
@@ -1584,7 +1609,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           *reinterpret_cast<volatile int*>(s_merge) = decision;
           dev::mbar_arrive(merge_go);
         }
-        if (!dev::mbar_wait_bounded(merge_go, merges & 1, tmo, p.status)) ok = false;
+        if (!wait(merge_go, merges & 1)) ok = false;
         ++merges;
         const int decision = ok ? *reinterpret_cast<volatile int*>(s_merge) : -1;
         if (decision < 0) {

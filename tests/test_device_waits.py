@@ -40,3 +40,28 @@ def test_a_voided_plan_does_not_part_a_running_block():
     text = source("prefill.cu")
     compared = re.findall(r"[^\n]*\bx (?:<|>=) total\b[^\n]*", text)
     assert len(compared) == 2 and all("kNoItem" in line for line in compared)
+
+
+def statements(text, call):
+    """(the statement up to the call, the lines before it, the text behind it)
+    of every call."""
+    for m in re.finditer(re.escape(call) + r"\(", text):
+        start = max(text.rfind(c, 0, m.start()) for c in ";{}")
+        yield text[start + 1:m.start()], text[:start + 1].splitlines()[-8:], text[m.end():m.end() + 300]
+
+
+def test_warps_give_up_as_one():
+    """A lane that gives up by itself leaves its warp's others at their next
+    vote or shuffle for ever.  So a wait whose result is used either is voted
+    on or belongs to a single lane."""
+    single = re.compile(r"if \((?:lane == 0|producer|threadIdx\.x == 0)\b")
+    seen = 0
+    for name in ("prefill.cu", "decode_window.cu"):
+        for before, above, behind in statements(source(name), "mbar_wait_bounded"):
+            seen += 1
+            alone = before.strip() in ("dev::", "") or re.fullmatch(r"\s*if \([^!]*\) dev::", before)
+            voted = "__all_sync(" in before or \
+                re.match(r"[^;]*ok = false;[^;]*(?:;[^;]*){0,5}\bok = __all_sync\(0xffffffffu, ok\);", behind)
+            one = single.search(before) or any(single.search(line) for line in above)
+            assert alone or voted or one, f"{name}: {before.strip()}"
+    assert seen > 10
