@@ -34,50 +34,19 @@ struct AppendParams {
   unsigned* status;
 };
 
-// A unit is one (sequence, block the call writes to); blockIdx.x numbers them
-// with gaps: sequence b's begin at query_start[b] / 16 + 2 b, so the next one's
-// begin at least T / 16 + 2 later, and T new tokens touch at most (T + 14) / 16
-// + 1 <= T / 16 + 2 blocks: two sequences' units never meet.  A
-// warp owns one (unit, KV head, K or V): it alone reads and writes that
+// One (unit, KV head, K or V), by a warp: it alone reads and writes that
 // scale, holds the new rows in registers between finding their largest
 // magnitude and encoding them, and rescales the older rows of the block when
-// the scale grows.  Bound by bytes (2 head_dim elements read and as many
-// codes written per token and head): 13.7 K tokens of 8 heads, 84 MB, 15 us; for
-// a decode step by latency (query_start, then table entry and rows together,
-// then the scale).
+// the scale grows.
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : 4)
-    append_kernel(const AppendParams p) {
+__device__ __forceinline__ void append_block(const AppendParams& p, const int4 seq, int unit, int head, int kv,
+                                             int lane) {
   constexpr int kLanes = D / 8;             // lanes per row, eight elements each
   constexpr int kRows = 32 / kLanes;        // rows per pass
   constexpr int kPasses = kBlockSize / kRows;
-  dev::grid_launch_dependents();
-  dev::grid_dependency_wait();
-  // the unit's sequence: the last one whose first unit is not past it
-  __shared__ int4 s_seq;  // it, its first and last query row, its length
-  const int unit = blockIdx.x;
-  auto invalid = [&](int q0, int q1, int ctx) {
-    return q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > ctx ||
-           ctx > p.max_blocks * kBlockSize;
-  };
-  if (threadIdx.x == 0) s_seq = make_int4(-1, 0, 0, 0);
-  __syncthreads();
-  for (int b = threadIdx.x; b < p.num_seqs; b += kAppendWarps * 32) {
-    const int q0 = p.query_start[b], q1 = p.query_start[b + 1], ctx = p.context_lens[b];
-    if (q0 / kBlockSize + 2 * b <= unit && (b + 1 == p.num_seqs || q1 / kBlockSize + 2 * (b + 1) > unit))
-      s_seq = make_int4(b, q0, q1, ctx);
-    if (unit == 0 && blockIdx.y == 0 && invalid(q0, q1, ctx)) dev::flag_status(p.status, kStatusBounds);
-  }
-  __syncthreads();
-  const int b = s_seq.x, q0 = s_seq.y, q1 = s_seq.z, ctx = s_seq.w;
-  const int fresh_tokens = q1 - q0;
-  if (b < 0 || fresh_tokens == 0 || invalid(q0, q1, ctx)) return;
-  const int begin = ctx - fresh_tokens;     // first new token's position
+  const int b = seq.x, q0 = seq.y, q1 = seq.z, ctx = seq.w;
+  const int begin = ctx - (q1 - q0);        // first new token's position
   const int blk = begin / kBlockSize + (unit - (q0 / kBlockSize + 2 * b));
-  if (blk > (ctx - 1) / kBlockSize) return;
-  const int job = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
-  if (job >= 2 * p.num_kv_heads) return;
-  const int kv = job & 1, head = job >> 1, lane = threadIdx.x & 31;
   const int lo = max(begin - blk * kBlockSize, 0);                 // rows lo .. hi - 1 are new
   const int hi = min(ctx - blk * kBlockSize, kBlockSize);
   const int row0 = lane / kLanes, col = (lane % kLanes) * 8;
@@ -134,6 +103,106 @@ __global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : 4)
     if (r >= lo && r < hi) *reinterpret_cast<uint2*>(codes + r * D) = x[i].encode(inv);
   }
   if (lane == 0 && (lo == 0 || scale > old)) *scale_at = scale;
+}
+
+__device__ __forceinline__ bool invalid(const AppendParams& p, int q0, int q1, int ctx) {
+  return q0 < 0 || q1 < q0 || q1 > p.num_tokens || q1 - q0 > ctx || ctx > p.max_blocks * kBlockSize;
+}
+
+// Whether `unit` is one of sequence b's blocks.
+__device__ __forceinline__ bool owns(const AppendParams& p, int unit, int b, int q0, int q1, int ctx) {
+  if (q1 == q0 || invalid(p, q0, q1, ctx)) return false;
+  const int nth = unit - (q0 / kBlockSize + 2 * b);
+  return nth >= 0 && nth <= (ctx - 1) / kBlockSize - (ctx - (q1 - q0)) / kBlockSize;
+}
+
+// A unit of several sequences (see append_kernel): each one's in turn, row by
+// row from memory (the path that a call in order takes keeps its registers).
+template <typename T, int D>
+__device__ __forceinline__ void append_in_turn(const AppendParams& p, int unit, int head, int kv, int lane) {
+#pragma unroll 1
+  for (int b = 0; b < p.num_seqs; ++b) {
+    const int q0 = p.query_start[b], q1 = p.query_start[b + 1], ctx = p.context_lens[b];
+    if (!owns(p, unit, b, q0, q1, ctx)) continue;
+    const int begin = ctx - (q1 - q0);
+    const int blk = begin / kBlockSize + (unit - (q0 / kBlockSize + 2 * b));
+    const int lo = max(begin - blk * kBlockSize, 0), hi = min(ctx - blk * kBlockSize, kBlockSize);
+    const int phys = p.block_tables[size_t(b) * p.max_blocks + blk];
+    if (phys < 0 || phys >= p.num_blocks) {
+      if (lane == 0) dev::flag_status(p.status, kStatusBounds);
+      continue;
+    }
+    const size_t tile = size_t(phys) * p.num_kv_heads + head;
+    float* scale_at = (kv ? p.scale[1] : p.scale[0]) + tile;
+    const bool live = lane < D / 8;
+    const T* src = static_cast<const T*>(kv ? p.src[1] : p.src[0]) +
+                   ((int64_t(q0) + blk * kBlockSize - begin) * p.num_kv_heads + head) * D + 8 * lane;
+    uint8_t* codes = (kv ? p.cache[1] : p.cache[0]) + tile * kBlockSize * D + 8 * lane;
+    uint32_t top = 0;
+#pragma unroll 1
+    for (int r = lo; r < hi && live; ++r) {
+      Row8<T> x;
+      x.load(src + int64_t(r) * p.num_kv_heads * D);
+      top = max(top, x.top(true));
+    }
+    top = Row8<T>::float_bits(__reduce_max_sync(0xffffffffu, top));
+    const float want = __uint_as_float(pow2_bits(scale_exponent(top)));
+    const float old = lo > 0 ? *scale_at : 0.f;
+    const float scale = fmaxf(old, want);
+    __syncwarp();
+#pragma unroll 1
+    for (int r = scale > old ? 0 : lo; r < hi && live; ++r) {
+      uint2* at = reinterpret_cast<uint2*>(codes + r * D);
+      if (r < lo) {
+        *at = rescale8(*at, old / scale);
+      } else {
+        Row8<T> x;
+        x.load(src + int64_t(r) * p.num_kv_heads * D);
+        *at = x.encode(1.f / scale);
+      }
+    }
+    if (lane == 0 && (lo == 0 || scale > old)) *scale_at = scale;
+  }
+}
+
+// A unit is one (sequence, block the call writes to); blockIdx.x numbers them
+// with gaps: sequence b's begin at query_start[b] / 16 + 2 b, so the next one's
+// begin at least T / 16 + 2 later, and T new tokens touch at most (T + 14) / 16
+// + 1 <= T / 16 + 2 blocks: two sequences' units do not meet.  A warp owns one
+// (unit, KV head, K or V).  Bound by bytes (2 head_dim elements read and as many
+// codes written per token and head): 13.7 K tokens of 8 heads, 84 MB, 15 us; for
+// a decode step by latency (query_start, then table entry and rows together,
+// then the scale).
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : 4)
+    append_kernel(const AppendParams p) {
+  dev::grid_launch_dependents();
+  dev::grid_dependency_wait();
+  // the unit's sequence.  With query_start in order there is one at most; a
+  // sequence that runs backwards (skipped) may be followed by one that begins
+  // among the units of an earlier one, and then a unit is each one's in turn.
+  __shared__ int4 s_seq;  // it, its first and last query row, its length
+  __shared__ int s_hits;
+  const int unit = blockIdx.x;
+  if (threadIdx.x == 0) s_hits = 0;
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.num_seqs; b += kAppendWarps * 32) {
+    const int q0 = p.query_start[b], q1 = p.query_start[b + 1], ctx = p.context_lens[b];
+    if (owns(p, unit, b, q0, q1, ctx)) {
+      s_seq = make_int4(b, q0, q1, ctx);
+      atomicAdd(&s_hits, 1);
+    }
+    if (unit == 0 && blockIdx.y == 0 && invalid(p, q0, q1, ctx)) dev::flag_status(p.status, kStatusBounds);
+  }
+  __syncthreads();
+  const int job = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
+  if (job >= 2 * p.num_kv_heads) return;
+  const int kv = job & 1, head = job >> 1, lane = threadIdx.x & 31;
+  if (s_hits == 1) {
+    append_block<T, D>(p, s_seq, unit, head, kv, lane);
+  } else if (s_hits > 1) {
+    append_in_turn<T, D>(p, unit, head, kv, lane);
+  }
 }
 
 // Sixteen values as elements of the output's type: whole 32-byte sectors per
