@@ -360,8 +360,9 @@ __global__ void __launch_bounds__(128) f32_kernel(const Params p) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     const float s = dot * p.scale;
-    const float mn = fmaxf(m, s);
-    const float a = expf(m - mn), w = expf(s - mn);
+    // (scores of -inf before any other: nothing has weight yet)
+    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
+    const float a = expf(m - ref), w = expf(s - ref);
     l = l * a + w;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * vc[at + e];

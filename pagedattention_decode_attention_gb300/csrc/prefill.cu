@@ -1805,8 +1805,9 @@ __global__ void __launch_bounds__(128) prefill_f32_kernel(const Params p) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     const float sc = dot * p.scale;
-    const float mn = fmaxf(m, sc);
-    const float a = expf(m - mn), pw = expf(sc - mn);
+    // (scores of -inf before any other: nothing has weight yet)
+    const float mn = fmaxf(m, sc), ref = mn == -INFINITY ? 0.f : mn;
+    const float a = expf(m - ref), pw = expf(sc - ref);
     l = l * a + pw;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + pw * v_cache[r + e];
