@@ -627,124 +627,148 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
     const float sl2 = p.scale_log2;
 
-    for (int j = 0; j < it.nblk; ++j, ++kc) {
+    // Slots past the context may hold anything, and 0 * NaN is not 0: each warp
+    // clears their V rows before it reads them, when the item comes to the block
+    // that the context ends in.  The loop over the blocks stops there once (head_dim
+    // 64, 16 chunks of 512: 1564 us, 1593 without any clearing; a test in the
+    // loop 1611 - 1663, masks on V's fragments 1704).  With a window, V is masked
+    // at both ends, in the loop.
+    const int edge = !WIN && it.ctx % kBlockSize ? it.ctx / kBlockSize - it.first : -1;
+    int stop = edge > 0 && edge < it.nblk ? edge : it.nblk;
+    int j = 0;
+    auto clear = [&]() {
       const int st = kc % kStages;
-      if (!wait_warp_hot(&full[st], (kc / kStages) & 1, tmo, p.status)) {
-        ok = false;
-        break;
-      }
-      const uint32_t kt = dev::smem_u32(ring + size_t(st) * S::kStageBytes);
-      const uint32_t vt = kt + S::kTileBytes;
-      const int t0 = (it.first + j) * kBlockSize;  // first token of the block
-      // ---- S = Q K^T: 16 rows x 16 tokens (two 8-token column tiles)
-      // two accumulation chains per column tile (even / odd k-steps) halve
-      // the dependent MMA latency
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-      {
-        float e0[4] = {0.f, 0.f, 0.f, 0.f}, e1[4] = {0.f, 0.f, 0.f, 0.f};
-        const int mi = lane >> 3;
-        const int tok = ((mi >> 1) << 3) + (lane & 7);
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-          const int gc = 2 * kk + (mi & 1);
-          const uint32_t addr =
-              kt + (gc >> 3) * 2048 + tok * 128 + ((((gc & 7) ^ (tok & 7))) << 4);
-          uint32_t b0, b1, b2, b3;
-          dev::ldmatrix_x4(addr, b0, b1, b2, b3);
-          M::run(kk & 1 ? e0 : s0, qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b0, b1);
-          M::run(kk & 1 ? e1 : s1, qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b2, b3);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s0[i] += e0[i];
-          s1[i] += e1[i];
-        }
-      }
-      // ---- causal / context mask, base-2 scores
-      const int c0 = t0 + 2 * tq, c1 = c0 + 8;  // tokens of s0[0], s1[0]
-      float xa[4], xb[4];
-      // (a window: from the row's first token in it on, or a first token)
-      auto see_a = [&](int c) { return c <= end_a && (!WIN || c >= low_a || c < p.num_sinks); };
-      auto see_b = [&](int c) { return c <= end_b && (!WIN || c >= low_b || c < p.num_sinks); };
-      xa[0] = see_a(c0) ? s0[0] * sl2 : -INFINITY;
-      xa[1] = see_a(c0 + 1) ? s0[1] * sl2 : -INFINITY;
-      xa[2] = see_a(c1) ? s1[0] * sl2 : -INFINITY;
-      xa[3] = see_a(c1 + 1) ? s1[1] * sl2 : -INFINITY;
-      xb[0] = see_b(c0) ? s0[2] * sl2 : -INFINITY;
-      xb[1] = see_b(c0 + 1) ? s0[3] * sl2 : -INFINITY;
-      xb[2] = see_b(c1) ? s1[2] * sl2 : -INFINITY;
-      xb[3] = see_b(c1 + 1) ? s1[3] * sl2 : -INFINITY;
-      float bma = fmaxf(fmaxf(xa[0], xa[1]), fmaxf(xa[2], xa[3]));
-      float bmb = fmaxf(fmaxf(xb[0], xb[1]), fmaxf(xb[2], xb[3]));
-      bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 1));
-      bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 2));
-      bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 1));
-      bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 2));
-      const float mna = fmaxf(ma, bma), mnb = fmaxf(mb, bmb);
-      // a row with nothing unmasked yet keeps m = -inf: use 0 as its reference
-      const float ua = mna == -INFINITY ? 0.f : mna, ub = mnb == -INFINITY ? 0.f : mnb;
-      const float ala = dev::fast_exp2(ma - ua), alb = dev::fast_exp2(mb - ub);
-      const float ra0 = ua - kLift, rb0 = ub - kLift;  // the weights' reference
-      ma = mna;
-      mb = mnb;
-      const uint32_t pa01 = M::pack(dev::fast_exp2(xa[0] - ra0), dev::fast_exp2(xa[1] - ra0));
-      const uint32_t pb01 = M::pack(dev::fast_exp2(xb[0] - rb0), dev::fast_exp2(xb[1] - rb0));
-      const uint32_t pa23 = M::pack(dev::fast_exp2(xa[2] - ra0), dev::fast_exp2(xa[3] - ra0));
-      const uint32_t pb23 = M::pack(dev::fast_exp2(xb[2] - rb0), dev::fast_exp2(xb[3] - rb0));
-      {
-        const float2 f0 = M::unpack(pa01), f1 = M::unpack(pa23);
-        const float2 g0 = M::unpack(pb01), g1 = M::unpack(pb23);
-        la = la * ala + (f0.x + f0.y + f1.x + f1.y);
-        lb = lb * alb + (g0.x + g0.y + g1.x + g1.y);
-      }
-#pragma unroll
-      for (int nd = 0; nd < ND; ++nd) {
-        o[nd][0] *= ala;
-        o[nd][1] *= ala;
-        o[nd][2] *= alb;
-        o[nd][3] *= alb;
-      }
-      // ---- O += P V: P (16 rows x 16 tokens) is the A operand as computed
-      {
-        const int mi = lane >> 3;
-        const int tok = ((mi & 1) << 3) + (lane & 7);
-        // V of tokens that no row of the item sees (b0, b2: tokens c0, c0 + 1,
-        // b1, b3: c1, c1 + 1) reads as 0, whatever it is
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        const bool hides = WIN && (t0 + kBlockSize > it.ctx - gap ||
-                                   (t0 < it.win.low - gap && t0 + kBlockSize > p.num_sinks));
-        if (hides) {
-          auto half = [&](int c) {
-            return c < it.ctx - gap && (c >= it.win.low - gap || c < p.num_sinks) ? 0xffffu : 0u;
-          };
-          keep0 = half(c0) | half(c0 + 1) << 16;
-          keep1 = half(c1) | half(c1 + 1) << 16;
-        }
-#pragma unroll
-        for (int nd = 0; nd < ND; nd += 2) {
-          const int gc = nd + (mi >> 1);  // 16-byte chunk = 8 columns
-          const uint32_t addr =
-              vt + (gc >> 3) * 2048 + tok * 128 + ((((gc & 7) ^ (tok & 7))) << 4);
-          uint32_t b0, b1, b2, b3;
-          dev::ldmatrix_x4_trans(addr, b0, b1, b2, b3);
-          if (hides) {
-            b0 &= keep0;
-            b1 &= keep1;
-            b2 &= keep0;
-            b3 &= keep1;
-          }
-          M::run(o[nd], pa01, pb01, pa23, pb23, b0, b1);
-          M::run(o[nd + 1], pa01, pb01, pa23, pb23, b2, b3);
-        }
-      }
-      // the stage is read: order those reads before the copy that reuses it
-      dev::fence_proxy_async_smem();
+      if (!wait_warp(&full[st], (kc / kStages) & 1, tmo, p.status)) return;  // (the loop sees it again)
+      uint8_t* v_tile = ring + size_t(st) * S::kStageBytes + S::kTileBytes;
+      for (int i = lane; i < kBlockSize * 8 * HALVES; i += 32)
+        if (((i >> 3) & 15) >= it.ctx % kBlockSize)
+          *reinterpret_cast<uint4*>(v_tile + 16 * i) = make_uint4(0, 0, 0, 0);
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive(&empty[st]);
-      if (warp == 0 && j + kStages < it.nblk) {
-        if (!issue(it, j + kStages, ik)) ok = false;
-        ++ik;
+    };
+    if (edge == 0) clear();
+    for (;;) {
+      for (; j < stop; ++j, ++kc) {
+        const int st = kc % kStages;
+        if (!wait_warp_hot(&full[st], (kc / kStages) & 1, tmo, p.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t kt = dev::smem_u32(ring + size_t(st) * S::kStageBytes);
+        const uint32_t vt = kt + S::kTileBytes;
+        const int t0 = (it.first + j) * kBlockSize;  // first token of the block
+        // ---- S = Q K^T: 16 rows x 16 tokens (two 8-token column tiles)
+        // two accumulation chains per column tile (even / odd k-steps) halve
+        // the dependent MMA latency
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        {
+          float e0[4] = {0.f, 0.f, 0.f, 0.f}, e1[4] = {0.f, 0.f, 0.f, 0.f};
+          const int mi = lane >> 3;
+          const int tok = ((mi >> 1) << 3) + (lane & 7);
+#pragma unroll
+          for (int kk = 0; kk < KT; ++kk) {
+            const int gc = 2 * kk + (mi & 1);
+            const uint32_t addr =
+                kt + (gc >> 3) * 2048 + tok * 128 + ((((gc & 7) ^ (tok & 7))) << 4);
+            uint32_t b0, b1, b2, b3;
+            dev::ldmatrix_x4(addr, b0, b1, b2, b3);
+            M::run(kk & 1 ? e0 : s0, qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b0, b1);
+            M::run(kk & 1 ? e1 : s1, qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], b2, b3);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s0[i] += e0[i];
+            s1[i] += e1[i];
+          }
+        }
+        // ---- causal / context mask, base-2 scores
+        const int c0 = t0 + 2 * tq, c1 = c0 + 8;  // tokens of s0[0], s1[0]
+        float xa[4], xb[4];
+        // (a window: from the row's first token in it on, or a first token)
+        auto see_a = [&](int c) { return c <= end_a && (!WIN || c >= low_a || c < p.num_sinks); };
+        auto see_b = [&](int c) { return c <= end_b && (!WIN || c >= low_b || c < p.num_sinks); };
+        xa[0] = see_a(c0) ? s0[0] * sl2 : -INFINITY;
+        xa[1] = see_a(c0 + 1) ? s0[1] * sl2 : -INFINITY;
+        xa[2] = see_a(c1) ? s1[0] * sl2 : -INFINITY;
+        xa[3] = see_a(c1 + 1) ? s1[1] * sl2 : -INFINITY;
+        xb[0] = see_b(c0) ? s0[2] * sl2 : -INFINITY;
+        xb[1] = see_b(c0 + 1) ? s0[3] * sl2 : -INFINITY;
+        xb[2] = see_b(c1) ? s1[2] * sl2 : -INFINITY;
+        xb[3] = see_b(c1 + 1) ? s1[3] * sl2 : -INFINITY;
+        float bma = fmaxf(fmaxf(xa[0], xa[1]), fmaxf(xa[2], xa[3]));
+        float bmb = fmaxf(fmaxf(xb[0], xb[1]), fmaxf(xb[2], xb[3]));
+        bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 1));
+        bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 2));
+        bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 1));
+        bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 2));
+        const float mna = fmaxf(ma, bma), mnb = fmaxf(mb, bmb);
+        // a row with nothing unmasked yet keeps m = -inf: use 0 as its reference
+        const float ua = mna == -INFINITY ? 0.f : mna, ub = mnb == -INFINITY ? 0.f : mnb;
+        const float ala = dev::fast_exp2(ma - ua), alb = dev::fast_exp2(mb - ub);
+        const float ra0 = ua - kLift, rb0 = ub - kLift;  // the weights' reference
+        ma = mna;
+        mb = mnb;
+        const uint32_t pa01 = M::pack(dev::fast_exp2(xa[0] - ra0), dev::fast_exp2(xa[1] - ra0));
+        const uint32_t pb01 = M::pack(dev::fast_exp2(xb[0] - rb0), dev::fast_exp2(xb[1] - rb0));
+        const uint32_t pa23 = M::pack(dev::fast_exp2(xa[2] - ra0), dev::fast_exp2(xa[3] - ra0));
+        const uint32_t pb23 = M::pack(dev::fast_exp2(xb[2] - rb0), dev::fast_exp2(xb[3] - rb0));
+        {
+          const float2 f0 = M::unpack(pa01), f1 = M::unpack(pa23);
+          const float2 g0 = M::unpack(pb01), g1 = M::unpack(pb23);
+          la = la * ala + (f0.x + f0.y + f1.x + f1.y);
+          lb = lb * alb + (g0.x + g0.y + g1.x + g1.y);
+        }
+#pragma unroll
+        for (int nd = 0; nd < ND; ++nd) {
+          o[nd][0] *= ala;
+          o[nd][1] *= ala;
+          o[nd][2] *= alb;
+          o[nd][3] *= alb;
+        }
+        // ---- O += P V: P (16 rows x 16 tokens) is the A operand as computed
+        {
+          const int mi = lane >> 3;
+          const int tok = ((mi & 1) << 3) + (lane & 7);
+          // V of tokens that no row of the item sees (b0, b2: tokens c0, c0 + 1,
+          // b1, b3: c1, c1 + 1) reads as 0, whatever it is
+          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+          const bool hides = WIN && (t0 + kBlockSize > it.ctx - gap ||
+                                     (t0 < it.win.low - gap && t0 + kBlockSize > p.num_sinks));
+          if (hides) {
+            auto half = [&](int c) {
+              return c < it.ctx - gap && (c >= it.win.low - gap || c < p.num_sinks) ? 0xffffu : 0u;
+            };
+            keep0 = half(c0) | half(c0 + 1) << 16;
+            keep1 = half(c1) | half(c1 + 1) << 16;
+          }
+#pragma unroll
+          for (int nd = 0; nd < ND; nd += 2) {
+            const int gc = nd + (mi >> 1);  // 16-byte chunk = 8 columns
+            const uint32_t addr =
+                vt + (gc >> 3) * 2048 + tok * 128 + ((((gc & 7) ^ (tok & 7))) << 4);
+            uint32_t b0, b1, b2, b3;
+            dev::ldmatrix_x4_trans(addr, b0, b1, b2, b3);
+            if (hides) {
+              b0 &= keep0;
+              b1 &= keep1;
+              b2 &= keep0;
+              b3 &= keep1;
+            }
+            M::run(o[nd], pa01, pb01, pa23, pb23, b0, b1);
+            M::run(o[nd + 1], pa01, pb01, pa23, pb23, b2, b3);
+          }
+        }
+        // the stage is read: order those reads before the copy that reuses it
+        dev::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(&empty[st]);
+        if (warp == 0 && j + kStages < it.nblk) {
+          if (!issue(it, j + kStages, ik)) ok = false;
+          ++ik;
+        }
       }
+      if (WIN || !ok || stop == it.nblk) break;
+      clear();
+      stop = it.nblk;
     }
     // every thread agrees before anyone leaves the loop (no one may be left
     // waiting at a CTA barrier)
