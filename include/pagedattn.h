@@ -405,7 +405,9 @@ PA_API int pa_paged_attention_decode_grouped_prefix_append_run(
  * shape and dtype; rows of no sequence are not written.  A sequence with
  * T_b > context_lens[b], context_lens[b] > max_blocks_per_seq * 16 or rows
  * outside [0, total_q) is skipped and sets PA_ERR_DEVICE_BOUNDS, as does a
- * table entry outside [0, num_blocks) (read as block 0).
+ * table entry outside [0, num_blocks) (read as block 0).  Slots behind the
+ * last token may hold anything.  An infinity or NaN among a token's values may
+ * reach rows of its chunk that precede it as NaN (their weight of it is 0).
  *
  * Workspace: pa_paged_attention_prefill_workspace_size bytes, 256-byte
  * aligned, owned by one call at a time, no initialisation needed.  Two
@@ -566,8 +568,12 @@ PA_API int pa_paged_attention_decode_q8_append_run(
  * split and workspace (pa_paged_attention_prefill_workspace_size) otherwise
  * as for pa_paged_attention_prefill; the plan also depends on window and
  * num_sinks, which the run must repeat.  Blocks that no row of a chunk sees
- * are not read, nor are their table entries.  window == 0 is
- * pa_paged_attention_prefill itself.
+ * are not read, nor are their table entries.  With a window a row's output
+ * depends on the tokens it sees alone: infinities and NaN among the values of
+ * others do not reach it, also where other rows of its chunk see them (rows
+ * that are not finite are attended once more one by one, up to a hundred times
+ * slower where all are).
+ * window == 0 is pa_paged_attention_prefill itself.
  * ---------------------------------------------------------------------- */
 PA_API int pa_paged_attention_prefill_window(
     const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

@@ -469,6 +469,98 @@ struct Item {
   WindowRange win;
 };
 
+// Columns of a windowed row's output are not finite: they are made again from the
+// tokens that the row sees and no others.  A tile holds what all of an item's rows
+// see between them, and a weight of 0 times an infinity or NaN that only another
+// row sees is NaN (columns that are finite met none).  By a warp, row gr0 + i of the
+// item's (token, head) rows for every bit i, U tokens at a time, in 32 bits, until
+// each of these columns is NaN on the row's own account.  16 chunks of 512, window
+// 2048: 22 ms when a NaN in every fortieth block spoils every row, 0.6 when a
+// column of every token is NaN, 0.19 with finite values, as without the test.
+// (Eight or 16 tokens at a time, or a block by lanes that each take a key, need 14 -
+// 19 ms, but cost the tcgen05 kernel's loop 1 - 3 % in registers; the mma.sync
+// kernel takes eight.)
+template <typename T, int D, int U>
+__device__ __forceinline__ void attend_again(const Params& p, unsigned rows, int gr0, int b, int g, int ctx,
+                                             int q_first, int qlen) {
+  constexpr int E = D / 32, W = E / 2;  // columns and words of a row per lane
+  const int lane = threadIdx.x & 31;
+  const int32_t* table = p.block_tables + size_t(b) * p.max_blocks;
+#pragma unroll 1
+  for (; rows; rows &= rows - 1) {
+    const int gr = gr0 + __ffs(rows) - 1;
+    const size_t at = (size_t(q_first + gr / p.group) * p.num_q_heads + g * p.group + gr % p.group) * D + lane * E;
+    const int pos = ctx - qlen + gr / p.group, low = max(0, pos - p.window + 1), sinks = min(p.num_sinks, low);
+    const int n = sinks + pos - low + 1;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + at);
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + at);
+    float acc[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += U) {
+      uint32_t v[U][W];
+      float s[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = min(i0 + u, n - 1), t = i < sinks ? i : low + i - sinks;
+        int phys = table[t / kBlockSize];
+        if (phys < 0 || phys >= p.num_blocks) phys = 0;
+        const size_t from = ((size_t(phys) * p.num_kv_heads + g) * kBlockSize + t % kBlockSize) * D + lane * E;
+        s[u] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float2 x =
+              dev::Mma<T>::unpack(reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.k_cache) + from)[w]);
+          const float2 y = dev::Mma<T>::unpack(q[w]);
+          s[u] = fmaf(x.x, y.x, fmaf(x.y, y.y, s[u]));
+          v[u][w] = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v_cache) + from)[w];
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], off);
+        s[u] = i0 + u < n ? s[u] * p.scale_log2 : -INFINITY;
+        mn = fmaxf(mn, s[u]);
+      }
+      const float ref = mn == -INFINITY ? 0.f : mn, a = dev::fast_exp2(m - ref);
+      m = mn;
+      l *= a;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= a;
+      bool lost = true;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float x = dev::fast_exp2(s[u] - ref);
+        l += x;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float2 y = dev::Mma<T>::unpack(i0 + u < n ? v[u][w] : 0u);
+          acc[2 * w] = fmaf(x, y.x, acc[2 * w]);
+          acc[2 * w + 1] = fmaf(x, y.y, acc[2 * w + 1]);
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 y = dev::Mma<T>::unpack(__ldcg(out + w));
+        lost = lost && (y.x * 0.f == 0.f || acc[2 * w] != acc[2 * w]) &&
+               (y.y * 0.f == 0.f || acc[2 * w + 1] != acc[2 * w + 1]);
+      }
+      if (__all_sync(0xffffffffu, lost)) break;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const uint32_t was = __ldcg(out + w), now = dev::Mma<T>::pack(acc[2 * w] * inv, acc[2 * w + 1] * inv);
+      const float2 y = dev::Mma<T>::unpack(was);
+      const uint32_t keep = (y.x * 0.f == 0.f ? 0xffffu : 0u) | (y.y * 0.f == 0.f ? 0xffff0000u : 0u);
+      out[w] = (was & keep) | (now & ~keep);
+    }
+  }
+}
+
 // WIN: with a sliding window (p.window > 0).
 template <typename T, int D, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32, 3)
@@ -488,6 +580,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   uint64_t* empty = full + kStages;
   int* s_claim = reinterpret_cast<int*>(empty + kStages);
   int* s_last = s_claim + 1;
+  unsigned* s_bad = reinterpret_cast<unsigned*>(s_last + 1);  // [kRows / 32]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;  // fragment row group / column pair
@@ -808,6 +901,23 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         if (va) *reinterpret_cast<uint32_t*>(oa + c) = M::pack(o[nd][0] * ia, o[nd][1] * ia);
         if (vb) *reinterpret_cast<uint32_t*>(ob + c) = M::pack(o[nd][2] * ib, o[nd][3] * ib);
       }
+      if constexpr (WIN) {
+        // rows that are not finite (x * 0 is 0 of a finite x only)
+        float za = 0.f, zb = 0.f;
+#pragma unroll
+        for (int nd = 0; nd < ND; ++nd) {
+          za = fmaf(o[nd][0], 0.f, fmaf(o[nd][1], 0.f, za));
+          zb = fmaf(o[nd][2], 0.f, fmaf(o[nd][3], 0.f, zb));
+        }
+        unsigned rows = 0;
+        if (__any_sync(0xffffffffu, (va && za != 0.f) || (vb && zb != 0.f))) {
+          const unsigned bad_a = __ballot_sync(0xffffffffu, va && za != 0.f);
+          const unsigned bad_b = __ballot_sync(0xffffffffu, vb && zb != 0.f);
+          for (int r = 0; r < 8; ++r)  // row r: lanes 4 r .. 4 r + 3
+            rows |= unsigned((bad_a >> 4 * r & 15) != 0) << r | unsigned((bad_b >> 4 * r & 15) != 0) << (r + 8);
+          attend_again<T, D, 8>(p, rows, row0, it.b, it.g, it.ctx, it.q_first, it.qlen);
+        }
+      }
     } else {
       const size_t base = (size_t(it.slot + it.s) * Hkv + it.g) * kRows + warp * 16;
       float* pa = p.part_o + (base + gq) * D;
@@ -834,6 +944,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         float* wsm = reinterpret_cast<float*>(ring);  // [ns][kRows]
         const size_t sbase = (size_t(it.slot) * Hkv + it.g) * kRows;  // split s adds s*Hkv*kRows
         const size_t sstride = size_t(Hkv) * kRows;
+        if (threadIdx.x < kRows / 32) s_bad[threadIdx.x] = 0;
         if (threadIdx.x < kRows) {
           const int r = threadIdx.x;
           float mx = -INFINITY;
@@ -887,10 +998,16 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
             pk.y = M::pack(acc[k].z, acc[k].w);
             reinterpret_cast<uint2*>(static_cast<T*>(p.out) + hrow * D)[c4] = pk;
           }
+          if (WIN && fmaf(acc[k].x, 0.f, fmaf(acc[k].y, 0.f, fmaf(acc[k].z, 0.f, acc[k].w * 0.f))) != 0.f)
+            atomicOr(&s_bad[(r0 + k * RS) / 32], 1u << (r0 + k * RS) % 32);
         }
         // the ring is a copy target again after this
         dev::fence_proxy_async_smem();
         __syncthreads();
+        if constexpr (WIN) {
+          const unsigned rows = s_bad[warp / 2] >> 16 * (warp % 2) & 0xffffu;
+          if (rows) attend_again<T, D, 8>(p, rows, row0, it.b, it.g, it.ctx, it.q_first, it.qlen);
+        }
         if (producer) p.arrivals[size_t(it.grp) * Hkv + it.g] = 0;  // ready for the next run
       }
     }
@@ -1597,6 +1714,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) dev::tmem_ld32(t_o + 32 * c, ov[c]);
       dev::tmem_wait_ld();
+      // (x * 0 is 0 of a finite x only)
+      float odd = 0.f;
+      if (WIN && !merge_here) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) odd = fmaf(__uint_as_float(ov[c][i]), 0.f, odd);
+      }
       if (merge_here) {
         // ---- one of ns splits of this (query block, KV head): its rows'
         // normalised o and base-2 log-sum-exp go to the workspace; the CTA
@@ -1670,6 +1795,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 acc[4 * q4 + 2] += wgt * v.z;
                 acc[4 * q4 + 3] += wgt * v.w;
               }
+            }
+            if (WIN) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) odd = fmaf(acc[e], 0.f, odd);
             }
             {
 #pragma unroll
@@ -1748,6 +1877,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               *reinterpret_cast<uint4*>(orow + 32 * c + 8 * i) =
                   make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
           }
+        }
+      }
+      if constexpr (WIN) {
+        const unsigned rows = __ballot_sync(0xffffffffu, valid && odd != 0.f);
+        if (rows) {
+          if (p.out_tma && lane == 0) bulk_wait_all();  // (the rows' stores have landed)
+          __syncwarp();
+          attend_again<T, D, 4>(p, rows, gr - lane, it.b, it.g, it.ctx, it.q_first, it.qlen);
         }
       }
       // O_w is read: the next item's first P V may overwrite it
