@@ -611,6 +611,8 @@ PA_API int pa_paged_attention_prefill_window_run(
  *     (to nearest even) from their values;
  *   - the new codes are x / scale rounded to nearest even; infinities become
  *     +-448, NaN stays NaN.
+ * (A block may hold a positive finite scale of the program's own.  If that is
+ * no power of two, 1 / scale and old / new scale are rounded to 32 bits first.)
  * Slots behind the last token keep their bits.  Only blocks with a new token
  * are touched; a block must not be written to by two sequences of one call
  * (copy-on-write guarantees this).  T_b = 1 everywhere is a decode step.

@@ -47,12 +47,12 @@
 //    more for one on an idle GPU.
 //
 // Measured (GB300, launches in a row, of the copy rate 6.79 TB/s): 128 sequences
-// of 128 .. 8192 tokens, 32/8 heads, 8-bit: 87.6 us, 6.25 TB/s of the bytes a
-// launch cannot do without (0.92); 64 sequences, window 4096 + 64, bf16: 89.3
-// us, 6.53 TB/s (0.96); 64 sequences of 16 .. 2048 tokens, 32/32 heads, 8-bit:
-// 38.1 us, 5.46 TB/s (0.80: 2048 short segments); one sequence of 101 tokens:
-// 5.8 us; one stream with a window of 1024: 8.7 us.  With the append, two
-// launches and one: 94.2 and 90.7 us (first batch), 45.1 and 42.0 (third).  The
+// of 128 .. 8192 tokens, 32/8 heads, 8-bit: 87.9 us, 6.23 TB/s of the bytes a
+// launch cannot do without (0.92); 64 sequences, window 4096 + 64, bf16: 89.0
+// us, 6.54 TB/s (0.96); 64 sequences of 16 .. 2048 tokens, 32/32 heads, 8-bit:
+// 38.4 us, 5.42 TB/s (0.80: 2048 short segments); one sequence of 101 tokens:
+// 5.8 us; one stream with a window of 1024: 8.8 us.  With the append, two
+// launches and one: 94.3 and 90.7 us (first batch), 45.0 and 41.9 (third).  The
 // loop itself runs at the copy rate; start (plan words, table entries, first
 // copies: 2 us) and end (warps' slack, merges within and between CTAs: 3 - 5 us)
 // are what is left.
@@ -319,7 +319,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   }
 }
 
-// fp32 caches: one warp per (sequence, query head), a token at a time.
+// fp32 caches: one warp per (sequence, query head), a token at a time, so K and
+// V are read once per query head and a token waits for the one before: 64
+// sequences with a window of 4096 + 64, 32/8 heads, 4.6 ms (floor 0.2).  For
+// checking against, not for serving.
 template <int D>
 __global__ void __launch_bounds__(128) f32_kernel(const Params p) {
   constexpr int E = D / 32;
@@ -383,11 +386,11 @@ struct Tiles {
   // The softmax's weights enter V's product rounded to its 16-bit type: half a
   // step, f16's 2^-11 and bf16's 2^-8 relative, as much as the rounding of an
   // output of that type.  For f16 (and an 8-bit cache's f16 weights) that is
-  // accepted: outputs of the f16 window case are 1.78e-4 from 64-bit
-  // arithmetic on average, 1.60e-4 with weights in 32 bits.  For bf16 what the
+  // accepted: outputs of the f16 window case are 1.7e-4 from 64-bit
+  // arithmetic on average, 1.5e-4 with weights in 32 bits.  For bf16 what the
   // rounding leaves over goes through a second product: the windowed batch's
   // output is 0.0017 (one rounding) from 64-bit arithmetic, 0.0023 without, for
-  // 89.4 us, 89.2 without (the tensor cores idle at 9 %).
+  // 89.4 us, 89.2 without (the tensor cores are active 13 % of the time, 9 without).
   static constexpr bool kTwoParts = !Q8 && std::is_same<T, __nv_bfloat16>::value;
   // f16 weights are 2^(x - reference + kLift).  The reference may be the
   // sequence's largest score (a first token that takes most of the softmax),

@@ -58,7 +58,7 @@ constexpr int kRows = kWarps * 16;   // query rows per work item
 constexpr int kStages = 4;           // depth of the CTA's K/V ring
 constexpr int kMaxGroup = 8;         // query heads per KV head
 constexpr int kMinSplitBlocks = 16;  // smallest KV split
-constexpr int kMinWindowSplit = 4;    // the same with a window, 64-row units (37 rows over 254 tokens: 13.2 us; 16: 16.3)
+constexpr int kMinWindowSplit = 4;    // the same with a window, 64-row units (37 rows over 254 tokens: 13.7 us; 16: 3 us more)
 constexpr int kPartialItems = 1024;  // (split unit, KV head) partial results, at most
 constexpr int kSizeBuckets = 32;     // work-list order: floor(log2(blocks)) buckets
 constexpr int kMaxSplits = 64;       // splits of one query block (the merge's weights fit the ring)
@@ -1056,10 +1056,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 // and first tokens, numbered without the gap between them, so everything but the
 // table reads and two masks is as above: columns before a row's own window, and
 // V rows that no row of the item sees (zeroed, whatever they hold).  16 chunks of
-// 512, window 2048: 191 us, 1.11 PFLOP/s of visible work (0.58 of the measured
-// bf16 rate); two long prompts, window 4096: 236 us, 1.05 PFLOP/s.  S in half
-// tiles of 64 tokens, double-buffered so that it runs ahead of the softmax,
-// took 239 and 304 us (twice the waits, products half as wide).
+// 512, window 2048: 190 us, 1.11 PFLOP/s of visible work (0.58 of the measured
+// bf16 rate), bound by the chain of a tile; two long prompts, window 4096: 233 us,
+// 1.06 PFLOP/s, a tile 1.8 us against 2.1, but 472 items of equal length make 3.1
+// waves on 152 CTAs, the last nearly empty.  S in half tiles of 64 tokens,
+// double-buffered so that it runs ahead of the softmax, took 239 and 304 us
+// (twice the waits, products half as wide).
 // Optional per-role wait counters (SM cycles), compiled in only with
 // -DPA_PROFILE_TIMES (a separate build; the default build has none of it).
 // Per CTA 32 slots of 8: MMA thread, softmax group 0 (its thread 0), group 1,
@@ -1913,7 +1915,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // --------------------------------------------------------------- fp32 path
-// One warp per (query row, query head): a decode over the tokens the row sees.
+// One warp per (query row, query head): a decode over the tokens the row sees, a
+// token at a time (512 rows, 32 heads, window 2048: 5.0 ms).  For checking against,
+// not for serving.
 template <int D>
 __global__ void __launch_bounds__(128) prefill_f32_kernel(const Params p) {
   constexpr int E = D / 32;
