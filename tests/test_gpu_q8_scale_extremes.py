@@ -96,3 +96,39 @@ def test_decode_is_right_at_every_scale(gpu, dtype, head_dim, window, sinks, ran
     # sequence it is far under the value
     for b in range(4):
         assert np.mean(limit[b] < 0.1 * np.abs(want[b])) > 0.8
+
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("exponent", [-100, 117])
+def test_sums_and_scales_together(gpu, head_dim, exponent):
+    """The softmax's sum and the value scales lie at opposite ends of 32 bits'
+    range, or at the same one; the outputs are ordinary numbers of the scales'
+    size.  700 sequences of 3200 tokens that share their blocks: most (sequence,
+    head) runs are one warp's, whose references stay at the first block's score,
+    7.9 bits (under 8) below all others.
+
+    Every query is (1, 0, ..), the first block's keys are 0 and all others 16 * 2^-4
+    in column 0, so the scores are 0 and ``scale``.  The bound: the output's half
+    step; weights rounded to f16, half a step; 3200 / 16 terms and 64 more of merges
+    in 32 bits, twice; 2^-16 for exponents of 2^7; scores of 8 off by 2^-20."""
+    hkv, hq, n, batch = 8, 16, 3200, 700
+    nb = n // 16
+    gen = np.random.default_rng(3)
+    scale = float(np.float32(7.9 / np.log2(np.e)))
+    k = np.zeros((nb, hkv, 16, head_dim))
+    k[1:, :, :, 0] = 16
+    v = 1 + gen.integers(0, 8, k.shape) / 8.0
+    codes = [torch.from_numpy(oq.encode(x)).to(gpu).view(torch.float8_e4m3fn) for x in (k, v)]
+    scales = [torch.full((nb, hkv), s, device=gpu) for s in (2.0 ** -4, 2.0 ** exponent)]
+    tables = np.tile(np.arange(nb, dtype=np.int32), (batch, 1))
+    q = torch.zeros((batch, hq, head_dim), dtype=torch.bfloat16, device=gpu)
+    q[..., 0] = 1
+    bt, cl = to_dev(gpu, tables, [n] * batch)
+    out = pa.paged_attention_decode_q8(q, *codes, *scales, bt, cl, 0, 0, scale)
+    pa.check_status()
+    w = np.where(np.arange(nb) == 0, 2.0 ** -7.9, 1.0)[:, None, None, None]
+    want = ((w * v).sum((0, 2)) / (16 * w.sum()) * 2.0 ** exponent).repeat(2, axis=0)       # [hq, d]
+    rel = HALF_STEP["bf16"] + HALF_STEP["f16"] + 2 * (n / 16 + 64) * HALF_STEP["f32"] + 2.0 ** -16 + 2.0 ** -20
+    err = np.abs(out.double().cpu().numpy() / want - 1)
+    assert err.max() <= rel * (1 + 2.0 ** -7), f"worst {err.max():.2e} of the value, allowed {rel:.2e}"
