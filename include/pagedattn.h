@@ -676,6 +676,148 @@ PA_API int pa_paged_attention_decode_noalloc(const void* q, const void* k_cache,
                                              int dtype, void* out, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions.  (No counterpart on the pages, which start from queries
+ * and keys that already know their positions.)
+ *
+ * A head's row at position p is rotated in its first rotary_dim columns (a
+ * multiple of 16, 16 .. head_dim; the others pass through): pair i of
+ * rotary_dim / 2 turns by p * w_i and is multiplied by `magnitude`,
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin).
+ * The pairs are columns (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved = 1.
+ *
+ * pa_rotary_frequencies (host; no device work) writes w_i, rotary_dim / 2
+ * doubles, with w_i = base^(-2 i / rotary_dim), scaled for contexts longer
+ * than the model was trained on:
+ *   PA_ROTARY_PLAIN   as they are (factor, original_context, low, high unused)
+ *   PA_ROTARY_LINEAR  w_i / factor
+ *   PA_ROTARY_BASE    base * factor^(rotary_dim / (rotary_dim - 2)) for base
+ *   PA_ROTARY_BANDS   by the turns n = original_context * w_i / 2 pi that a pair
+ *                     makes over the trained context: w_i / factor up to `low`
+ *                     turns, w_i from `high` on, between them
+ *                     w_i * (g + (1 - g) / factor), g = (n - low) / (high - low)
+ *                     ("YaRN: Efficient Context Window Extension of Large
+ *                     Language Models", section 3.2; its temperature is a
+ *                     magnitude of 0.1 ln(factor) + 1)
+ * pa_rotary_turns (host) turns any frequencies, in radians per position, into
+ * what the device calls take: w / 2 pi, less whole turns, times 2^64, as a
+ * 64-bit integer.  Its product with a position wraps at a whole turn by
+ * itself, so angles are exact to 2^-33 of a turn at any 32-bit position.  The
+ * caller copies them to the device once (`turns`, 8-byte aligned).
+ *
+ * Positions are any int32, negative ones too.  The transposed rotation, which
+ * takes the gradients of rotated rows to those of the rows, is the same call
+ * with negated turns.  Cosines and sines are computed in the kernel; products
+ * are fp32 and a result is rounded once to its type.
+ *
+ * Rows lie `*_stride` elements apart (a multiple of 16 bytes; 0 repeats one
+ * row), a row's heads side by side: the q, k and v parts of a fused
+ * projection's output are passed as they lie.  Tensors are 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+typedef enum pa_rotary_scaling {
+  PA_ROTARY_PLAIN = 0,
+  PA_ROTARY_LINEAR = 1,
+  PA_ROTARY_BASE = 2,
+  PA_ROTARY_BANDS = 3
+} pa_rotary_scaling;
+
+PA_API int pa_rotary_frequencies(int rotary_dim, double base, int scaling, double factor,
+                                 int original_context, double low, double high,
+                                 double* frequencies);
+PA_API int pa_rotary_turns(const double* frequencies, int num_frequencies, int64_t* turns);
+
+/* ------------------------------------------------------------------------
+ * pa_rotary -- num_tokens query and key rows rotated: row t of q
+ * ([num_q_heads][head_dim]) to row t of q_out at positions[t], likewise k.
+ * In place with q_out == q and the same stride (k alike); otherwise outputs
+ * overlap no input.  num_q_heads 0 leaves out q and q_out, num_kv_heads 0 k
+ * and k_out (NULL).
+ * ---------------------------------------------------------------------- */
+PA_API int pa_rotary(const void* q, const void* k, const int32_t* positions, const int64_t* turns,
+                     int rotary_dim, int interleaved, float magnitude, int num_tokens,
+                     int num_q_heads, int num_kv_heads, int head_dim, int64_t q_stride,
+                     int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride, int dtype,
+                     void* q_out, void* k_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_rotary_kv_append -- pa_rotary of q and k, the rotated keys going to their
+ * slots of a paged cache with v beside them, in one launch: the codes of
+ * pa_rotary followed by pa_kv_append, bit for bit.
+ *
+ * A token with a negative slot has its query rotated and stores nothing; a
+ * slot >= num_blocks * 16 stores nothing and sets PA_ERR_DEVICE_BOUNDS.  q_out
+ * may be q (same stride); the caches overlap no input.  num_q_heads 0 leaves
+ * out q and q_out.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_rotary_kv_append(const void* q, const void* k, const void* v,
+                               const int32_t* positions, const int64_t* turns, int rotary_dim,
+                               int interleaved, float magnitude, void* k_cache, void* v_cache,
+                               const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                               int num_kv_heads, int head_dim, int num_blocks, int64_t q_stride,
+                               int64_t k_stride, int64_t v_stride, int64_t q_out_stride, int dtype,
+                               void* q_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_rotary_kv_append_q8 -- pa_kv_append_q8 with keys rotated on the way, and
+ * the queries of the same rows rotated to q_out, in one launch.
+ *
+ * positions may be NULL: a token's place in its sequence, as its length and
+ * query_start say.  A rotated key is quantised from 32 bits (scale and code),
+ * not from the input's type.  Rows of no sequence, and those of a sequence
+ * whose lengths are out of range (PA_ERR_DEVICE_BOUNDS), keep their q_out; a
+ * bad block loses the block's keys and values only.  Everything else as for
+ * pa_kv_append_q8 and pa_rotary_kv_append.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_rotary_kv_append_q8(const void* q, const void* k, const void* v,
+                                  const int32_t* positions, const int64_t* turns, int rotary_dim,
+                                  int interleaved, float magnitude, void* k_cache, void* v_cache,
+                                  float* k_scale, float* v_scale, const int32_t* block_tables,
+                                  const int32_t* context_lens, const int32_t* query_start,
+                                  int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                                  int head_dim, int max_blocks_per_seq, int num_blocks,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  int64_t q_out_stride, int dtype, void* q_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_paged_attention_decode_rotary_append_run -- a decode step's layer in one
+ * launch: pa_paged_attention_decode_append_run whose q and k_new are rotated
+ * on the way, over the same plan.
+ *
+ * positions may be NULL: context_lens[b] - 1.  The caches end up as
+ * pa_rotary_kv_append leaves them, bit for bit.  The rotated query is not
+ * rounded to q's type before its product (f16 and bf16: its first 16 and 22
+ * bits are used), so the output is nearer to exact arithmetic than that call
+ * followed by pa_paged_attention_decode_run; a query whose rotated values pass
+ * its type's range gives infinities.  PA_F32 runs as two launches, which keep
+ * the rotated queries in out.  out overlaps no input.  Everything else as for
+ * pa_paged_attention_decode_append_run.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_paged_attention_decode_rotary_append_run(
+    const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+    const int64_t* turns, int rotary_dim, int interleaved, float magnitude,
+    const int64_t* slot_mapping, void* k_cache, void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+    float scale, int dtype, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_paged_attention_decode_q8_rotary_append_run --
+ * pa_paged_attention_decode_q8_append_run whose q and k_new are rotated on the
+ * way, in one launch over the same plan.  positions may be NULL: the newest
+ * token's place, context_lens[b] - 1.  Codes and scales end up as
+ * pa_rotary_kv_append_q8 leaves them, bit for bit; the rotated query enters
+ * its product unrounded to q's type.  out overlaps no input.
+ * ---------------------------------------------------------------------- */
+PA_API int pa_paged_attention_decode_q8_rotary_append_run(
+    const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+    const int64_t* turns, int rotary_dim, int interleaved, float magnitude, void* k_cache,
+    void* v_cache, float* k_scale, float* v_scale, const int32_t* block_tables,
+    const int32_t* context_lens, int window, int num_sinks, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, int64_t q_stride,
+    int64_t k_stride, int64_t v_stride, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * pa_block_copy -- copy-on-write block copies, all layers in one launch.
  *
  * OS-lab appendix, sections 4.3-4.4 (when the target block's refcount is

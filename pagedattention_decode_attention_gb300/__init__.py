@@ -21,6 +21,13 @@ Device entry points (hand-written sm_103a kernels behind the C ABI in
   :func:`block_dequantize` -- a cache held in 8 bits (e4m3 codes, a
   power-of-two scale per block and head): quantising append, decode (windowed
   or not), whole blocks read back as 16- or 32-bit values;
+* :class:`Rotary`, :func:`rotary` -- rotary positions: query and key rows
+  rotated (halves or interleaved pairs, part of the head, scaled for long
+  contexts; the transposed rotation for gradients); :func:`rotary_kv_append`,
+  :func:`rotary_kv_append_q8` on the way into the cache, and
+  :func:`paged_attention_decode_rotary_append_run`,
+  :func:`paged_attention_decode_q8_rotary_append_run` within a decode step's
+  one launch;
 * :func:`block_copy` -- copy-on-write block copies across all layers;
 * :func:`block_swap` -- whole blocks between the device caches and
   page-locked host caches (preemption / offload), all layers in one launch;
@@ -54,7 +61,13 @@ from .ops import (LayerCaches, Prepared, alloc_prefill_workspace, alloc_workspac
                   paged_attention_decode_q8_append_run, prepare_decode_q8_append_run,
                   paged_attention_prefill_window, paged_attention_prefill_window_plan,
                   paged_attention_prefill_window_run, kv_append_q8, prepare_kv_append_q8,
-                  block_dequantize, prepare_block_dequantize)
+                  block_dequantize, prepare_block_dequantize,
+                  Rotary, rotary, prepare_rotary, rotary_frequencies, rotary_turns,
+                  rotary_kv_append, prepare_rotary_kv_append,
+                  rotary_kv_append_q8, prepare_rotary_kv_append_q8,
+                  paged_attention_decode_rotary_append_run, prepare_decode_rotary_append_run,
+                  paged_attention_decode_q8_rotary_append_run,
+                  prepare_decode_q8_rotary_append_run)
 from .pool import BlockPool  # noqa: F401
 
 # the C entry points' own names for the calls above whose Python name is shorter

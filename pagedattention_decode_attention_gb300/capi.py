@@ -34,6 +34,7 @@ BLOCK_SIZE = 16
 
 
 PA_SWAP_OUT, PA_SWAP_IN = 0, 1
+PA_ROTARY_PLAIN, PA_ROTARY_LINEAR, PA_ROTARY_BASE, PA_ROTARY_BANDS = range(4)
 
 
 class PoolStats(C.Structure):
@@ -50,6 +51,7 @@ class PagedAttnError(RuntimeError):
         self.status = status
 
 
+_i64 = C.c_int64
 _vp, _i, _i64p, _i32p, _sz = C.c_void_p, C.c_int, C.POINTER(C.c_int64), C.POINTER(C.c_int32), C.c_size_t
 
 SIGNATURES = {
@@ -121,6 +123,20 @@ SIGNATURES = {
                                                                           _vp, _sz, _vp]),
     "pa_kv_append_q8": (_i, [_vp] * 9 + [_i] * 7 + [_vp]),
     "pa_block_dequantize": (_i, [_vp] * 5 + [_i] * 6 + [_vp, _vp, _vp]),
+    "pa_rotary_frequencies": (_i, [_i, C.c_double, _i, C.c_double, _i, C.c_double, C.c_double,
+                                   C.POINTER(C.c_double)]),
+    "pa_rotary_turns": (_i, [C.POINTER(C.c_double), _i, _i64p]),
+    "pa_rotary": (_i, [_vp] * 4 + [_i] * 2 + [C.c_float] + [_i] * 4 + [_i64] * 4 + [_i] + [_vp] * 3),
+    "pa_rotary_kv_append": (_i, [_vp] * 5 + [_i] * 2 + [C.c_float] + [_vp] * 3 + [_i] * 5
+                            + [_i64] * 4 + [_i] + [_vp] * 2),
+    "pa_rotary_kv_append_q8": (_i, [_vp] * 5 + [_i] * 2 + [C.c_float] + [_vp] * 7 + [_i] * 7
+                               + [_i64] * 4 + [_i] + [_vp] * 2),
+    "pa_paged_attention_decode_rotary_append_run": (
+        _i, [_vp] * 5 + [_i] * 2 + [C.c_float] + [_vp] * 5 + [_i] * 6 + [_i64] * 3
+        + [C.c_float, _i, _vp, _vp, _sz, _vp]),
+    "pa_paged_attention_decode_q8_rotary_append_run": (
+        _i, [_vp] * 5 + [_i] * 2 + [C.c_float] + [_vp] * 6 + [_i] * 8 + [_i64] * 3
+        + [C.c_float, _i, _vp, _vp, _sz, _vp]),
     "pa_block_copy": (_i, [C.POINTER(_vp), C.POINTER(_vp), _i, _vp, _i, _i, _i, _i, _i, _vp]),
     "pa_block_swap": (_i, [C.POINTER(_vp), C.POINTER(_vp), C.POINTER(_vp), C.POINTER(_vp), _i,
                            _vp, _i, _i, _i, _i, _i, _i, _i, _vp]),

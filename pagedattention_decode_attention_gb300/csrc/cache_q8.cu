@@ -1,5 +1,6 @@
-// The 8-bit paged cache: kv_append_q8 (new tokens quantised into their blocks)
-// and block_dequantize (whole blocks read back as 16- or 32-bit values).
+// The 8-bit paged cache: kv_append_q8 (new tokens quantised into their blocks),
+// rotary_kv_append_q8 (the same with queries and keys rotated on the way) and
+// block_dequantize (whole blocks read back as 16- or 32-bit values).
 //
 // Format (q8.cuh): k_cache, v_cache hold e4m3 codes [num_blocks][num_kv_heads]
 // [16][head_dim]; k_scale, v_scale one fp32 power of two per (block, KV head).
@@ -13,6 +14,7 @@
 #include "device_common.cuh"
 #include "pagedattn.h"
 #include "q8.cuh"
+#include "rotary.cuh"
 #include "status.h"
 #include "trace.h"
 
@@ -205,6 +207,169 @@ __global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : 4)
   }
 }
 
+// ------------------------------------------------- rotated on the way
+struct RotaryAppendParams {
+  AppendParams a;       // src: k, v
+  const void* q;
+  void* q_out;
+  int64_t stride[3], q_out_stride;  // elements between rows of k, v, q; of q_out
+  int num_q_heads;
+  const int32_t* positions;         // null: a token's place in its sequence
+  rot::Args rot;
+};
+
+// One (unit, head of Q, K or V), by a warp, as append_block; a lane takes item
+// lane % NJ of rows lane / NJ, + 32 / NJ, ....  K and V are quantised from 32
+// bits: a rotated key is rounded once, to its code.  `angles`: the cosines and
+// sines of the unit's rows.
+template <typename T, int D>
+__device__ __forceinline__ void rotary_block(const RotaryAppendParams& p, const int4 seq, int unit, int job,
+                                             const float2 (&angles)[kBlockSize][D / 2], int lane) {
+  constexpr int NJ = D / 16, kRows = 32 / NJ, kPasses = kBlockSize / kRows;
+  const int b = seq.x, q0 = seq.y, q1 = seq.z, ctx = seq.w;
+  const int begin = ctx - (q1 - q0);
+  const int blk = begin / kBlockSize + (unit - (q0 / kBlockSize + 2 * b));
+  const int lo = max(begin - blk * kBlockSize, 0);
+  const int hi = min(ctx - blk * kBlockSize, kBlockSize);
+  const int kv = job < 2 * p.a.num_kv_heads ? job & 1 : 2;  // K, V, Q
+  const int head = kv < 2 ? job >> 1 : job - 2 * p.a.num_kv_heads;
+  const int j = lane % NJ, row0 = lane / NJ;
+  const bool turns = kv != 1 && 16 * j < p.rot.dim;
+  const int2 at = kv != 1 ? rot::item_columns(p.rot, j) : make_int2(16 * j, 16 * j + 8);
+  // (row 0 of the block, which lies before the tokens when lo > 0)
+  const int64_t first = int64_t(q0) + blk * kBlockSize - begin;
+  const T* src = static_cast<const T*>(kv == 2 ? p.q : kv ? p.a.src[1] : p.a.src[0]) +
+                 first * p.stride[kv] + head * D;
+  float x[kPasses][16];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = i * kRows + row0;
+    if (r < lo || r >= hi) continue;
+    rot::Chunk<T> u, w;
+    u.load(src + r * p.stride[kv] + at.x);
+    w.load(src + r * p.stride[kv] + at.y);
+    u.to_float(x[i]);
+    w.to_float(x[i] + 8);
+    if (turns) {
+      float c[8], s[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c[e] = angles[r][8 * j + e].x;
+        s[e] = angles[r][8 * j + e].y;
+      }
+      rot::turn_item(p.rot.interleaved, x[i], c, s);
+    }
+  }
+  if (kv == 2) {
+    T* to = static_cast<T*>(p.q_out) + first * p.q_out_stride + head * D;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = i * kRows + row0;
+      if (r < lo || r >= hi) continue;
+      rot::Chunk<T> u, w;
+      u.from_float(x[i]);
+      w.from_float(x[i] + 8);
+      u.store(to + r * p.q_out_stride + at.x);
+      w.store(to + r * p.q_out_stride + at.y);
+    }
+    return;
+  }
+  const int phys = p.a.block_tables[size_t(b) * p.a.max_blocks + blk];
+  if (phys < 0 || phys >= p.a.num_blocks) {
+    if (lane == 0) dev::flag_status(p.a.status, kStatusBounds);
+    return;
+  }
+  const size_t tile = size_t(phys) * p.a.num_kv_heads + head;
+  float* scale_at = (kv ? p.a.scale[1] : p.a.scale[0]) + tile;
+  const float old = lo > 0 ? *scale_at : 0.f;
+  // the largest finite magnitude
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = i * kRows + row0;
+    if (r < lo || r >= hi) continue;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t m = __float_as_uint(x[i][e]) & 0x7FFFFFFFu;
+      if (m < 0x7F800000u) top = max(top, m);
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  const float want = __uint_as_float(pow2_bits(scale_exponent(top)));
+  const float scale = lo > 0 ? fmaxf(old, want) : want;
+  const float inv = 1.f / scale;
+  uint8_t* codes = (kv ? p.a.cache[1] : p.a.cache[0]) + tile * kBlockSize * D;
+  const bool grows = lo > 0 && scale > old;
+  const float factor = grows ? old / scale : 1.f;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = i * kRows + row0;
+    if (r >= hi || (r < lo && !grows)) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint2* to = reinterpret_cast<uint2*>(codes + r * D + (h ? at.y : at.x));
+      if (r < lo) {
+        *to = rescale8(*to, factor);
+      } else {
+        uint32_t c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = encode2(x[i][8 * h + 2 * e] * inv, x[i][8 * h + 2 * e + 1] * inv);
+        *to = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      }
+    }
+  }
+  if (lane == 0 && (lo == 0 || grows)) *scale_at = scale;
+}
+
+// Units as append_kernel's; a warp owns one (unit, head of Q, K or V).
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendWarps * 32) rotary_append_kernel(const RotaryAppendParams p) {
+  dev::grid_launch_dependents();
+  dev::grid_dependency_wait();
+  __shared__ __align__(16) float2 angles[kBlockSize][D / 2];
+  __shared__ int4 s_seq;
+  __shared__ int s_hits;
+  const int unit = blockIdx.x;
+  if (threadIdx.x == 0) s_hits = 0;
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.a.num_seqs; b += kAppendWarps * 32) {
+    const int q0 = p.a.query_start[b], q1 = p.a.query_start[b + 1], ctx = p.a.context_lens[b];
+    if (owns(p.a, unit, b, q0, q1, ctx)) {
+      s_seq = make_int4(b, q0, q1, ctx);
+      atomicAdd(&s_hits, 1);
+    }
+    if (unit == 0 && blockIdx.y == 0 && invalid(p.a, q0, q1, ctx)) dev::flag_status(p.a.status, kStatusBounds);
+  }
+  __syncthreads();
+  const int hits = s_hits;
+  const int job = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
+  auto take = [&](const int4 seq) {
+    const int begin = seq.w - (seq.z - seq.y);
+    const int blk = begin / kBlockSize + (unit - (seq.y / kBlockSize + 2 * seq.x));
+    const int lo = max(begin - blk * kBlockSize, 0), hi = min(seq.w - blk * kBlockSize, kBlockSize);
+    const int pairs = p.rot.dim / 2;
+    for (int i = threadIdx.x; i < (hi - lo) * pairs; i += kAppendWarps * 32) {
+      const int r = lo + i / pairs, e = i % pairs;
+      const int place = blk * kBlockSize + r;
+      const int position = p.positions ? p.positions[int64_t(seq.y) + place - begin] : place;
+      angles[r][e] = rot::cos_sin(position, p.rot.freqs[e], p.rot.magnitude);
+    }
+    __syncthreads();
+    if (job < 2 * p.a.num_kv_heads + p.num_q_heads) rotary_block<T, D>(p, seq, unit, job, angles, threadIdx.x & 31);
+  };
+  if (hits == 1) {
+    take(s_seq);
+  } else if (hits > 1) {
+    // a unit of several sequences: each one's in turn
+    for (int b = 0; b < p.a.num_seqs; ++b) {
+      const int q0 = p.a.query_start[b], q1 = p.a.query_start[b + 1], ctx = p.a.context_lens[b];
+      if (!owns(p.a, unit, b, q0, q1, ctx)) continue;
+      take(make_int4(b, q0, q1, ctx));
+      __syncthreads();
+    }
+  }
+}
+
 // Sixteen values as elements of the output's type: whole 32-byte sectors per
 // store where the output is 32-byte aligned.
 template <typename T>
@@ -381,6 +546,90 @@ PA_API int pa_kv_append_q8(const void* k, const void* v, void* k_cache, void* v_
   else
     e = wide ? cudaLaunchKernelEx(&cfg, append_kernel<__nv_bfloat16, 128>, p)
              : cudaLaunchKernelEx(&cfg, append_kernel<__nv_bfloat16, 64>, p);
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+  return PA_OK;
+}
+
+PA_API int pa_rotary_kv_append_q8(const void* q, const void* k, const void* v,
+                                  const int32_t* positions, const int64_t* turns, int rotary_dim,
+                                  int interleaved, float magnitude, void* k_cache, void* v_cache,
+                                  float* k_scale, float* v_scale, const int32_t* block_tables,
+                                  const int32_t* context_lens, const int32_t* query_start,
+                                  int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                                  int head_dim, int max_blocks_per_seq, int num_blocks,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  int64_t q_out_stride, int dtype, void* q_out, void* stream) {
+  PA_TRACE("pa_rotary_kv_append_q8");
+  const char* who = "rotary_kv_append_q8";
+  int rc = check_shape(dtype, head_dim, num_kv_heads, num_blocks, who);
+  if (rc != PA_OK) return rc;
+  if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq <= 0 || num_q_heads < 0 || num_q_heads > 1 << 16)
+    return fail(PA_ERR_INVALID_ARG, "%s: sizes must be positive", who);
+  if (double(max_blocks_per_seq) * kBlockSize >= 2147483647.0 ||
+      double(num_tokens) / kBlockSize + 2.0 * num_seqs >= 2147483647.0)
+    return fail(PA_ERR_INVALID_ARG, "%s: sizes too large", who);
+  const int elem = dtype == PA_F32 ? 4 : 2;
+  if (rc == PA_OK) rc = rot::check_stride(q_stride, elem, 0, "q_stride", who);
+  if (rc == PA_OK) rc = rot::check_stride(k_stride, elem, 0, "k_stride", who);
+  if (rc == PA_OK) rc = rot::check_stride(v_stride, elem, 0, "v_stride", who);
+  if (rc == PA_OK)
+    rc = rot::check_stride(q_out_stride, elem, num_tokens > 1 ? int64_t(num_q_heads) * head_dim : 0,
+                           "q_out_stride", who);
+  if (rc != PA_OK) return rc;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  RotaryAppendParams p = {};
+  rc = rot::check_args(turns, rotary_dim, interleaved, magnitude, head_dim, who, &p.rot);
+  if (rc != PA_OK) return rc;
+  if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables ||
+      !context_lens || !query_start || (num_q_heads && (!q || !q_out)))
+    return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (misaligned(k) || misaligned(v) || misaligned(k_cache) || misaligned(v_cache) ||
+      (num_q_heads && (misaligned(q) || misaligned(q_out))))
+    return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", who);
+  unsigned* status = device_status_word();
+  if (!status) return PA_ERR_CUDA;
+  p.a.src[0] = k;
+  p.a.src[1] = v;
+  p.a.cache[0] = static_cast<uint8_t*>(k_cache);
+  p.a.cache[1] = static_cast<uint8_t*>(v_cache);
+  p.a.scale[0] = k_scale;
+  p.a.scale[1] = v_scale;
+  p.a.block_tables = block_tables;
+  p.a.context_lens = context_lens;
+  p.a.query_start = query_start;
+  p.a.num_seqs = num_seqs;
+  p.a.num_tokens = num_tokens;
+  p.a.num_kv_heads = num_kv_heads;
+  p.a.max_blocks = max_blocks_per_seq;
+  p.a.num_blocks = num_blocks;
+  p.a.status = status;
+  p.q = q;
+  p.q_out = q_out;
+  p.stride[0] = k_stride;
+  p.stride[1] = v_stride;
+  p.stride[2] = q_stride;
+  p.q_out_stride = q_out_stride;
+  p.num_q_heads = num_q_heads;
+  p.positions = positions;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(num_tokens / kBlockSize + 2 * num_seqs),
+                     unsigned((2 * num_kv_heads + num_q_heads + kAppendWarps - 1) / kAppendWarps));
+  cfg.blockDim = dim3(kAppendWarps * 32);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  const bool wide = head_dim == 128;
+  if (dtype == PA_F32)
+    e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<float, 128>, p)
+             : cudaLaunchKernelEx(&cfg, rotary_append_kernel<float, 64>, p);
+  else if (dtype == PA_F16)
+    e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<__half, 128>, p)
+             : cudaLaunchKernelEx(&cfg, rotary_append_kernel<__half, 64>, p);
+  else
+    e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<__nv_bfloat16, 128>, p)
+             : cudaLaunchKernelEx(&cfg, rotary_append_kernel<__nv_bfloat16, 64>, p);
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
   return PA_OK;
 }

@@ -939,14 +939,63 @@ struct Item {
   int bmem, bvalid, bpatch;
   long long mslot;
   unsigned okmask;  // members whose new token is stored and attended
+  int pos;   // rotation: the new token's position
   int slot;  // fused append: the new token's slot, or -1 (none / not this item)
   bool patch;  // the new token is this item's last attended token
 };
 
+// The new token of a sequence that attends nothing, rotated into its slot, by
+// one lane.
+template <typename T, int D>
+__device__ __noinline__ void store_rotated(const Params& p, int b, long long slot) {
+  const int position = p.positions ? p.positions[b] : p.context_lens[b] - 1;
+  const T* k = static_cast<const T*>(p.k_new) + b * p.k_stride;
+  const T* v = static_cast<const T*>(p.v_new) + b * p.v_stride;
+  const size_t first = size_t(slot / kBlockSize) * p.num_kv_heads * kBlockSize + size_t(slot % kBlockSize);
+  for (int j = 0; j < D / 16; ++j) {
+    const int2 at = rot::item_columns(p.rot, j);
+    float c[8], s[8];
+    if (16 * j < p.rot.dim) {
+      for (int i = 0; i < 8; ++i) {
+        const float2 cs = rot::cos_sin(position, p.rot.freqs[8 * j + i], p.rot.magnitude);
+        c[i] = cs.x;
+        s[i] = cs.y;
+      }
+    }
+    for (int h = 0; h < p.num_kv_heads; ++h) {
+      const size_t to = (first + size_t(h) * kBlockSize) * D;
+      T* kc = static_cast<T*>(const_cast<void*>(p.k_cache)) + to;
+      T* vc = static_cast<T*>(const_cast<void*>(p.v_cache)) + to;
+      rot::Chunk<T> a, e;
+      a.load(k + h * D + at.x);
+      e.load(k + h * D + at.y);
+      if (16 * j < p.rot.dim) {
+        float x[16];
+        a.to_float(x);
+        e.to_float(x + 8);
+        rot::turn_item(p.rot.interleaved, x, c, s);
+        a.from_float(x);
+        e.from_float(x + 8);
+      }
+      a.store(kc + at.x);
+      e.store(kc + at.y);
+      a.load(v + h * D + 16 * j);
+      e.load(v + h * D + 16 * j + 8);
+      a.store(vc + 16 * j);
+      e.store(vc + 16 * j + 8);
+    }
+  }
+}
+
 // NT: query-row tiles of 8 per item (1: up to 8 rows, one sequence's query
 // group; 2: up to 16, the rows of the members of a group sharing the item's
 // blocks).
-template <typename T, int D, int W, int NT>
+// ROT: the query rows and the new K rows are rotated (rotary.cuh) in the
+// warp's staging buffer, between their copy and the fragments.  Each lane
+// computes two cosines an item and holds the frequencies; the rotated query is
+// not rounded to T: what the rounding leaves over goes through a second
+// product (bf16 outputs 0.0022 from 64-bit arithmetic, 0.0031 without).
+template <typename T, int D, int W, int NT, bool ROT>
 __global__ void __launch_bounds__(W * 32)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const Params p) {
@@ -958,6 +1007,11 @@ __global__ void __launch_bounds__(W * 32)
                             (16 * kTeamRow + 16) * 4 <= 2 * S::kStageBytes),
                 "a team warp's results fit the first two stages of its ring");
   constexpr int HALVES = D / 64;  // 128-byte TMA boxes per tile row
+  constexpr int NJ = D / 16;      // 16-column items of a row's rotation
+  static_assert(!ROT || NT == 1, "rotation is built for one sequence's rows");
+  // f16 weights of the rotating kernel are 2^(x - max + 7): without the lift a
+  // dominant token leaves the small ones under f16's precision
+  constexpr float kLift = ROT && std::is_same<T, __half>::value ? 7.f : 0.f;
   // The next item is claimed when this many blocks of the current one are
   // still to be issued: its claim takes one pipeline step per block (counter,
   // unit, table entries, query copy), so it is ready when the ring wants it.
@@ -1010,6 +1064,7 @@ __global__ void __launch_bounds__(W * 32)
   // The next kernel of the stream may start launching; it waits for this
   // one's completion before it touches memory.
   dev::grid_launch_dependents();
+  int64_t freqs[ROT ? D / 64 : 1];
   // This warp's first item, dealt statically.  W consecutive items (the
   // heads of one unit, reading neighbouring tiles) per CTA measured best
   // when every warp gets one (MHA 7B decode 0.868 of the measured copy
@@ -1085,6 +1140,7 @@ __global__ void __launch_bounds__(W * 32)
     }
   }
   dev::grid_dependency_wait();  // the kernel before this one has completed
+  if constexpr (ROT) rot::WarpAngles<D>::load_freqs(p.rot, lane, freqs);
   TIME_MARK(0, dev::global_timer_ns());
 
   const unsigned long long tmo = p.timeout_ns;
@@ -1139,7 +1195,9 @@ __global__ void __launch_bounds__(W * 32)
         for (int i = 0; i < Hq * D * 2 / 16; ++i) row[i] = make_uint4(0, 0, 0, 0);
         const long long slot = fused ? p.slot_mapping[b] : -1;
         if (slot >= num_slots) dev::flag_status(p.status, kStatusBounds);
-        if (slot >= 0 && slot < num_slots) {
+        if (ROT && slot >= 0 && slot < num_slots) {
+          store_rotated<T, D>(p, b, slot);
+        } else if (slot >= 0 && slot < num_slots) {
           for (int h = 0; h < Hkv; ++h) {
             const size_t src = (size_t(b) * Hkv + h) * D / 8;
             const size_t dst = ((size_t(slot / kBlockSize) * Hkv + h) * kBlockSize +
@@ -1241,6 +1299,7 @@ __global__ void __launch_bounds__(W * 32)
       }
       nxt.rows = nxt.m * G;
       nxt.nsplit = __ldg(&p.ws.nsplits[nxt.b]);
+      if constexpr (ROT) nxt.pos = p.positions ? __ldg(&p.positions[nxt.b]) : nxt.ctx - 1;
       // only an item of one sequence carries its new token
       cslot = fused && (cu.z & 0xff00) == 0 ? __ldg(&p.slot_mapping[nxt.b]) : -1;
       nxt.phys = lane < nxt.nblk
@@ -1343,18 +1402,31 @@ __global__ void __launch_bounds__(W * 32)
       __syncwarp();
       // lane r copies query row r (member r / G, head r % G of the group)
       // into row r of the buffer
-      if (lane < nxt.rows)
-        dev::bulk_load(qbuf + lane * S::kQRow,
-                       static_cast<const uint8_t*>(p.q) +
-                           ((size_t(nxt.b) + lane / G) * Hq + size_t(nxt.g) * G + lane % G) *
-                               D * 2,
-                       D * 2, my_q);
-      if (rbytes && lane == 0) {
-        const size_t row = (size_t(nxt.b) * Hkv + nxt.g) * D * 2;
-        dev::bulk_load(qbuf + 8 * S::kQRow, static_cast<const uint8_t*>(p.k_new) + row, D * 2,
-                       my_q);
-        dev::bulk_load(qbuf + 8 * S::kQRow + D, static_cast<const uint8_t*>(p.v_new) + row, D * 2,
-                       my_q);
+      if constexpr (ROT) {
+        if (lane < G)
+          dev::bulk_load(qbuf + lane * S::kQRow,
+                         static_cast<const T*>(p.q) + nxt.b * p.q_stride + (nxt.g * G + lane) * D,
+                         D * 2, my_q);
+        if (rbytes && lane == 0) {
+          dev::bulk_load(qbuf + 8 * S::kQRow,
+                         static_cast<const T*>(p.k_new) + nxt.b * p.k_stride + nxt.g * D, D * 2, my_q);
+          dev::bulk_load(qbuf + 8 * S::kQRow + D,
+                         static_cast<const T*>(p.v_new) + nxt.b * p.v_stride + nxt.g * D, D * 2, my_q);
+        }
+      } else {
+        if (lane < nxt.rows)
+          dev::bulk_load(qbuf + lane * S::kQRow,
+                         static_cast<const uint8_t*>(p.q) +
+                             ((size_t(nxt.b) + lane / G) * Hq + size_t(nxt.g) * G + lane % G) *
+                                 D * 2,
+                         D * 2, my_q);
+        if (rbytes && lane == 0) {
+          const size_t row = (size_t(nxt.b) * Hkv + nxt.g) * D * 2;
+          dev::bulk_load(qbuf + 8 * S::kQRow, static_cast<const uint8_t*>(p.k_new) + row, D * 2,
+                         my_q);
+          dev::bulk_load(qbuf + 8 * S::kQRow + D, static_cast<const uint8_t*>(p.v_new) + row, D * 2,
+                         my_q);
+        }
       }
       ++q_issued;
       cstage = 4;
@@ -1432,7 +1504,10 @@ __global__ void __launch_bounds__(W * 32)
     // the second row tile holds rows (warp-uniform)
     const bool two = NT == 2 && rows > 8;
     // B fragments of Q^T (k = head_dim, n = query head of the group)
-    if (!mbar_wait_bounded(my_q, q_taken & 1, tmo, p.status)) {
+    bool arrived = mbar_wait_bounded(my_q, q_taken & 1, tmo, p.status);
+    // (the rotation's shuffles need every lane: a warp that gives up does as one)
+    if constexpr (ROT) arrived = __all_sync(0xffffffffu, arrived);
+    if (!arrived) {
       drain();
       return;
     }
@@ -1442,16 +1517,85 @@ __global__ void __launch_bounds__(W * 32)
     unsigned long long merge_ns = 0;
 #endif
     uint32_t qb0[NT][KT], qb1[NT][KT];
+    auto fragments = [&](uint32_t (&f0)[NT][KT], uint32_t (&f1)[NT][KT]) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int hq = 8 * t + (lane >> 2);
-      const int n0 = 2 * (lane & 3);
-      const uint16_t* qrow = qbuf + hq * S::kQRow + n0;
+      for (int t = 0; t < NT; ++t) {
+        const int hq = 8 * t + (lane >> 2);
+        const int n0 = 2 * (lane & 3);
+        const uint16_t* qrow = qbuf + hq * S::kQRow + n0;
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+          f0[t][kk] = hq < rows ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk) : 0u;
+          f1[t][kk] = hq < rows ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 8) : 0u;
+        }
+      }
+    };
+    uint32_t ql0[ROT ? KT : 1], ql1[ROT ? KT : 1];  // what q's rounding leaves over
+    if constexpr (ROT) {
+      // a lane rotates item lane % NJ of rows lane / NJ, + 32 / NJ, ..., and
+      // the first lanes the new K row's; the rows are replaced by their
+      // rounded values, then, once those are fragments, by what is left over
+      constexpr int kRows = 32 / NJ, kTurns = (8 + kRows - 1) / kRows;
+      const int j = lane % NJ;
+      rot::WarpAngles<D> angles;
+      angles.set(freqs, cur.pos, p.rot.magnitude);
+      float c[8], sn[8];
+      angles.gather(j, c, sn);
+      const int2 at = rot::item_columns(p.rot, j);
+      const bool turns = 16 * j < p.rot.dim;
+      rot::Chunk<T> left[kTurns][2];
+      auto turn_row = [&](uint16_t* row, rot::Chunk<T>* rest) {
+        T* a = reinterpret_cast<T*>(row + at.x);
+        T* b2 = reinterpret_cast<T*>(row + at.y);
+        rot::Chunk<T> u, w;
+        u.load(a);
+        w.load(b2);
+        float x[16], y[16];
+        u.to_float(x);
+        w.to_float(x + 8);
+        rot::turn_item(p.rot.interleaved, x, c, sn);
+        u.from_float(x);
+        w.from_float(x + 8);
+        u.store(a);
+        w.store(b2);
+        if (rest) {
+          u.to_float(y);
+          w.to_float(y + 8);
+          // (nothing is left over of an infinity)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = fabsf(y[i]) < INFINITY ? x[i] - y[i] : 0.f;
+          rest[0].from_float(y);
+          rest[1].from_float(y + 8);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        left[i][0].v[0] = left[i][1].v[0] = make_uint4(0, 0, 0, 0);
+        const int r = i * kRows + lane / NJ;
+        if (r < rows && turns) turn_row(qbuf + r * S::kQRow, left[i]);
+      }
+      if (cur.slot >= 0 && lane < NJ && turns) turn_row(qbuf + 8 * S::kQRow, nullptr);
+      __syncwarp();
+      fragments(qb0, qb1);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const int r = i * kRows + lane / NJ;
+        if (r < rows) {
+          left[i][0].store(reinterpret_cast<T*>(qbuf + r * S::kQRow + at.x));
+          left[i][1].store(reinterpret_cast<T*>(qbuf + r * S::kQRow + at.y));
+        }
+      }
+      __syncwarp();
+      uint32_t f0[NT][KT], f1[NT][KT];
+      fragments(f0, f1);
 #pragma unroll
       for (int kk = 0; kk < KT; ++kk) {
-        qb0[t][kk] = hq < rows ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk) : 0u;
-        qb1[t][kk] = hq < rows ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 8) : 0u;
+        ql0[kk] = f0[0][kk];
+        ql1[kk] = f1[0][kk];
       }
+    } else {
+      fragments(qb0, qb1);
     }
     // fused append: lane l < D/4 holds 16 bytes of the new K row (l < D/8)
     // or V row; they go to the cache slot now and into the tile at the last block
@@ -1505,7 +1649,9 @@ __global__ void __launch_bounds__(W * 32)
       const int st = cst;
       if (NT == 1 && j == nblk - 1 && nsplit > 1 && lane == 0)
         seen = dev::ld_relaxed_gpu(&p.ws.arrivals[size_t(b) * Hkv + g]);
-      if (!mbar_wait_bounded(&my_full[st], cph, tmo, p.status)) {
+      bool landed = mbar_wait_bounded(&my_full[st], cph, tmo, p.status);
+      if constexpr (ROT) landed = __all_sync(0xffffffffu, landed);
+      if (!landed) {
         drain();
         return;
       }
@@ -1556,6 +1702,7 @@ __global__ void __launch_bounds__(W * 32)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         sa[t][0] = sa[t][1] = sa[t][2] = sa[t][3] = sb[t][0] = sb[t][1] = sb[t][2] = sb[t][3] = 0.f;
+      float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};  // ROT: the rest's product
       {
         const int row = lane & 15;
 #pragma unroll
@@ -1573,6 +1720,12 @@ __global__ void __launch_bounds__(W * 32)
             else
               M::run(sa[t], a0, a1, a2, a3, qb0[t][kk], qb1[t][kk]);
           }
+          if constexpr (ROT) {
+            if (kk & 1)
+              M::run(sd, a0, a1, a2, a3, ql0[kk], ql1[kk]);
+            else
+              M::run(sc, a0, a1, a2, a3, ql0[kk], ql1[kk]);
+          }
         }
       }
       // ---- mask, scale to base 2, online softmax per query column
@@ -1585,6 +1738,11 @@ __global__ void __launch_bounds__(W * 32)
         if (t == 1 && !two) {
           pb0[t] = pb1[t] = 0u;
           continue;
+        }
+        if constexpr (ROT) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)  // (an infinite score has no rest: 0 or a sign's opposite times infinity)
+            if (fabsf(sa[0][e] + sb[0][e]) < INFINITY) sb[0][e] += sc[e] + sd[e];
         }
         // a member's own block counts for that member's rows only
         const bool c0 = bmem < 0 || mc0[t] == bmem, c1 = bmem < 0 || mc1[t] == bmem;
@@ -1599,11 +1757,14 @@ __global__ void __launch_bounds__(W * 32)
           bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, o_));
         }
         const float mn0 = fmaxf(m0[t], bm0), mn1 = fmaxf(m1[t], bm1);
-        const float al0 = dev::fast_exp2(m0[t] - mn0), al1 = dev::fast_exp2(m1[t] - mn1);
+        // (ROT: as long as every score was -inf, nothing has a weight)
+        const float rf0 = ROT && mn0 == -INFINITY ? 0.f : mn0, rf1 = ROT && mn1 == -INFINITY ? 0.f : mn1;
+        const float al0 = dev::fast_exp2(m0[t] - rf0), al1 = dev::fast_exp2(m1[t] - rf1);
         m0[t] = mn0;
         m1[t] = mn1;
-        const uint32_t p01 = M::pack(dev::fast_exp2(x0 - mn0), dev::fast_exp2(x1 - mn1));
-        const uint32_t p23 = M::pack(dev::fast_exp2(x2 - mn0), dev::fast_exp2(x3 - mn1));
+        const float lf0 = rf0 - kLift, lf1 = rf1 - kLift;
+        const uint32_t p01 = M::pack(dev::fast_exp2(x0 - lf0), dev::fast_exp2(x1 - lf1));
+        const uint32_t p23 = M::pack(dev::fast_exp2(x2 - lf0), dev::fast_exp2(x3 - lf1));
         {
           const float2 f01 = M::unpack(p01), f23 = M::unpack(p23);
           l0[t] = l0[t] * al0 + f01.x + f23.x;
@@ -2200,17 +2361,18 @@ struct DeviceState {
   int sms = 0;
   Tuning tuning;
   KernelConfig cfg[2][2];   // [bf16?][head_dim 128?]
+  KernelConfig cfg_rot[2][2];  // the same for the rotating decode (8 warps)
   KernelConfig cfg2[2][2];  // the same for two query-row tiles (grouped decode, 8 warps)
 };
 DeviceState g_dev[kMaxDevices];
 
 
-template <typename T, int D, int W, int NT = 1>
+template <typename T, int D, int W, int NT = 1, bool ROT = false>
 cudaError_t configure_kernel(KernelConfig* cfg, const Tuning& t, size_t optin, size_t per_sm) {
   // shared memory per CTA when `ctas_per_sm` CTAs share an SM (1 KiB reserved each)
   size_t budget = per_sm / t.ctas_per_sm - 1024;
   if (budget > optin) budget = optin;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, W, NT>,
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D, W, NT, ROT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(budget));
   if (e != cudaSuccess) return e;
   int stages = Smem<D, W, NT>::stages_for(budget);  // per math warp
@@ -2218,7 +2380,7 @@ cudaError_t configure_kernel(KernelConfig* cfg, const Tuning& t, size_t optin, s
   cfg->stages = stages;
   cfg->smem = Smem<D, W, NT>::bytes(stages);
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&cfg->ctas_per_sm,
-                                                    decode_kernel<T, D, W, NT>, W * 32, cfg->smem);
+                                                    decode_kernel<T, D, W, NT, ROT>, W * 32, cfg->smem);
   if (cfg->ctas_per_sm > t.ctas_per_sm) cfg->ctas_per_sm = t.ctas_per_sm;
   return e;
 }
@@ -2229,7 +2391,15 @@ cudaError_t configure_all(DeviceState& st, size_t optin, size_t per_sm) {
   if (e == cudaSuccess) e = configure_kernel<__nv_bfloat16, 64, W>(&st.cfg[1][0], st.tuning, optin, per_sm);
   if (e == cudaSuccess) e = configure_kernel<__half, 128, W>(&st.cfg[0][1], st.tuning, optin, per_sm);
   if (e == cudaSuccess) e = configure_kernel<__half, 64, W>(&st.cfg[0][0], st.tuning, optin, per_sm);
-  // the grouped decode always runs 8 math warps per CTA
+  // the rotating decode and the grouped decode always run 8 math warps per CTA
+  if (e == cudaSuccess)
+    e = configure_kernel<__nv_bfloat16, 128, 8, 1, true>(&st.cfg_rot[1][1], st.tuning, optin, per_sm);
+  if (e == cudaSuccess)
+    e = configure_kernel<__nv_bfloat16, 64, 8, 1, true>(&st.cfg_rot[1][0], st.tuning, optin, per_sm);
+  if (e == cudaSuccess)
+    e = configure_kernel<__half, 128, 8, 1, true>(&st.cfg_rot[0][1], st.tuning, optin, per_sm);
+  if (e == cudaSuccess)
+    e = configure_kernel<__half, 64, 8, 1, true>(&st.cfg_rot[0][0], st.tuning, optin, per_sm);
   if (e == cudaSuccess)
     e = configure_kernel<__nv_bfloat16, 128, 8, 2>(&st.cfg2[1][1], st.tuning, optin, per_sm);
   if (e == cudaSuccess)
@@ -2258,6 +2428,7 @@ int device_setup(int device) {
     for (int a = 0; a < 2 && st.error == PA_OK; ++a)
       for (int d = 0; d < 2; ++d)
         if (st.cfg[a][d].stages < 1 || st.cfg[a][d].ctas_per_sm < 1 ||
+            st.cfg_rot[a][d].stages < 1 || st.cfg_rot[a][d].ctas_per_sm < 1 ||
             st.cfg2[a][d].stages < 1 || st.cfg2[a][d].ctas_per_sm < 1)
           st.error = PA_ERR_UNSUPPORTED;
   });
@@ -2265,7 +2436,7 @@ int device_setup(int device) {
   return PA_OK;
 }
 
-template <typename T, int D, int W, int NT = 1>
+template <typename T, int D, int W, int NT = 1, bool ROT = false>
 int launch_tc(Params prm, const KernelConfig& kc, int sms, cudaStream_t stream) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   alignas(64) CUtensorMap mk, mv;
@@ -2283,7 +2454,7 @@ int launch_tc(Params prm, const KernelConfig& kc, int sms, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, W, NT>, mk, mv, prm);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<T, D, W, NT, ROT>, mk, mv, prm);
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode: launch failed: %s", cudaGetErrorString(e));
   return PA_OK;
 }
@@ -2428,6 +2599,10 @@ struct AppendArgs {
   const void* k_new = nullptr;
   const void* v_new = nullptr;
   const int64_t* slot_mapping = nullptr;
+  // rotation of q and k_new (freqs null: none), see Params
+  rot::Args rot = {};
+  const int32_t* positions = nullptr;
+  int64_t q_stride = 0, k_stride = 0, v_stride = 0;
 };
 
 // Checks the new tokens' rows and slots of a fused append call.
@@ -2477,8 +2652,16 @@ int run_impl(const void* q, const void* k_cache, const void* v_cache, const int3
   apply_suffix(prm, sfx);
 
   if (app.slot_mapping && dtype == PA_F32) {
-    // the fp32 path is not fused: append first, then attend
-    rc = pa_kv_append(app.k_new, app.v_new, const_cast<void*>(k_cache), const_cast<void*>(v_cache),
+    // the fp32 path is not fused: append first, then attend (the rotated
+    // queries wait in `out`: a warp reads its row before it writes there)
+    if (app.rot.freqs) prm.q = out;
+    rc = app.rot.freqs
+             ? rot::append_rows(q, app.k_new, app.v_new, app.positions, context_lens, app.rot,
+                                const_cast<void*>(k_cache), const_cast<void*>(v_cache),
+                                app.slot_mapping, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                num_blocks, app.q_stride, app.k_stride, app.v_stride,
+                                int64_t(num_q_heads) * head_dim, dtype, out, stream, who)
+             : pa_kv_append(app.k_new, app.v_new, const_cast<void*>(k_cache), const_cast<void*>(v_cache),
                       app.slot_mapping, num_seqs, num_kv_heads, head_dim, num_blocks, dtype,
                       stream);
     if (rc != PA_OK) return rc;
@@ -2486,6 +2669,11 @@ int run_impl(const void* q, const void* k_cache, const void* v_cache, const int3
     prm.k_new = app.k_new;
     prm.v_new = app.v_new;
     prm.slot_mapping = app.slot_mapping;
+    prm.rot = app.rot;
+    prm.positions = app.positions;
+    prm.q_stride = app.q_stride;
+    prm.k_stride = app.k_stride;
+    prm.v_stride = app.v_stride;
   }
   if (dtype == PA_F32) {
     const int blocks = (num_seqs * num_q_heads + 3) / 4;
@@ -2500,6 +2688,14 @@ int run_impl(const void* q, const void* k_cache, const void* v_cache, const int3
   }
   const DeviceState& st = g_dev[device];
   const KernelConfig& kc = st.cfg[dtype == PA_BF16][head_dim == 128];
+  if (app.rot.freqs) {
+    const KernelConfig& kr = st.cfg_rot[dtype == PA_BF16][head_dim == 128];
+    if (dtype == PA_BF16)
+      return head_dim == 128 ? launch_tc<__nv_bfloat16, 128, 8, 1, true>(prm, kr, st.sms, stream)
+                             : launch_tc<__nv_bfloat16, 64, 8, 1, true>(prm, kr, st.sms, stream);
+    return head_dim == 128 ? launch_tc<__half, 128, 8, 1, true>(prm, kr, st.sms, stream)
+                           : launch_tc<__half, 64, 8, 1, true>(prm, kr, st.sms, stream);
+  }
   if (st.tuning.warps == 4) {
     if (dtype == PA_BF16)
       return head_dim == 128 ? launch_tc<__nv_bfloat16, 128, 4>(prm, kc, st.sms, stream)
@@ -2594,6 +2790,36 @@ PA_API int pa_paged_attention_decode_append_run(
   AppendArgs app;
   rc = append_args(k_new, v_new, slot_mapping, app, who);
   if (rc != PA_OK) return rc;
+  return run_impl(q, k_cache, v_cache, block_tables, context_lens, num_seqs, num_q_heads,
+                  num_kv_heads, head_dim, max_blocks_per_seq, num_blocks, scale, dtype, out,
+                  workspace, workspace_bytes, static_cast<cudaStream_t>(stream), who, app);
+}
+
+PA_API int pa_paged_attention_decode_rotary_append_run(
+    const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+    const int64_t* turns, int rotary_dim, int interleaved, float magnitude,
+    const int64_t* slot_mapping, void* k_cache, void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+    float scale, int dtype, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  PA_TRACE("pa_paged_attention_decode_rotary_append_run");
+  const char* who = "paged_attention_decode_rotary_append_run";
+  int rc = check_decode_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                               dtype, who);
+  const int elem = dtype == PA_F32 ? 4 : 2;
+  if (rc == PA_OK) rc = rot::check_stride(q_stride, elem, 0, "q_stride", who);
+  if (rc == PA_OK) rc = rot::check_stride(k_stride, elem, 0, "k_stride", who);
+  if (rc == PA_OK) rc = rot::check_stride(v_stride, elem, 0, "v_stride", who);
+  if (rc != PA_OK || num_seqs == 0) return rc;
+  AppendArgs app;
+  rc = append_args(k_new, v_new, slot_mapping, app, who);
+  if (rc == PA_OK)
+    rc = rot::check_args(turns, rotary_dim, interleaved, magnitude, head_dim, who, &app.rot);
+  if (rc != PA_OK) return rc;
+  app.positions = positions;
+  app.q_stride = q_stride;
+  app.k_stride = k_stride;
+  app.v_stride = v_stride;
   return run_impl(q, k_cache, v_cache, block_tables, context_lens, num_seqs, num_q_heads,
                   num_kv_heads, head_dim, max_blocks_per_seq, num_blocks, scale, dtype, out,
                   workspace, workspace_bytes, static_cast<cudaStream_t>(stream), who, app);

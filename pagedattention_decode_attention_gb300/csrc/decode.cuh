@@ -4,6 +4,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "rotary.cuh"
+
 namespace pa {
 namespace decode {
 
@@ -123,6 +125,12 @@ struct Params {
   const void* k_new;
   const void* v_new;
   const int64_t* slot_mapping;
+  // Rotation (decode_kernel<..., true>): q's rows and k_new's are rotated for
+  // positions[b] (null: context_lens[b] - 1), and rows of q, k_new and v_new
+  // are these many elements apart.
+  rot::Args rot;
+  const int32_t* positions;
+  int64_t q_stride, k_stride, v_stride;
   // Suffix mode (cas_o non-null): each sequence attends only its tokens from
   // ctx_offset on (table entries from table_offset on), and the results go
   // to cas_o / cas_lse (fp32 o and base-2 log-sum-exp per (sequence, head))

@@ -70,6 +70,7 @@
 #include "device_common.cuh"
 #include "pagedattn.h"
 #include "q8.cuh"
+#include "rotary.cuh"
 #include "status.h"
 #include "tensor_map.h"
 #include "trace.h"
@@ -146,6 +147,11 @@ struct Params {
   const void* new_rows[2];
   uint8_t* codes[2];
   float* scales[2];
+  // rotation of q's rows and the new K rows (rotary.cuh): positions (null: the
+  // newest token's place), elements between rows of q, K and V
+  rot::Args rot;
+  const int32_t* positions;
+  int64_t q_stride, new_stride[2];
   void* out;
   const int32_t* block_tables;
   const int32_t* context_lens;
@@ -379,7 +385,8 @@ __global__ void __launch_bounds__(128) f32_kernel(const Params p) {
 
 // ------------------------------------------------------- tensor-core path
 // Tiles of the cache: C = the cache's element (uint8_t: e4m3 codes).
-template <typename T, bool Q8, int D>
+// ROT: with room for a warp's query rows, which it rotates there.
+template <typename T, bool Q8, int D, bool ROT = false>
 struct Tiles {
   using Mm = dev::Mma<typename std::conditional<Q8, __half, T>::type>;
   static constexpr int kElem = Q8 ? 1 : 2;
@@ -409,13 +416,17 @@ struct Tiles {
   static constexpr int kStage = 2 * kTile;                  // K tile, V tile
   static constexpr int kWarps = warps_of(Q8, D);
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = (kWarps == 8 ? 24576 : !Q8 ? 16384 : 12288) / kStage;
+  static constexpr int kStages = (kWarps == 8 ? 24576 : !Q8 ? 16384 : 12288) / kStage - (ROT && D == 64 ? 1 : 0);
   static constexpr int kSteps = D / 16;                     // 16-wide steps of either product
   static constexpr size_t kRing = size_t(kWarps) * kStages * kStage;
   static constexpr size_t kPieces = kRing;                  // Piece[kWarps]
   static constexpr size_t kBars = kPieces + kWarps * sizeof(Piece<D>);
   static constexpr size_t kFlags = kBars + size_t(kWarps) * kStages * 8;  // int[kWarps + 4]
-  static constexpr size_t kBytes = kFlags + (kWarps + 4) * 4;
+  // rows 16 bytes apart, so that lanes reading one column of several do not meet in a bank
+  static constexpr int kQRow = D + 8;
+  static constexpr int kQBytes = ROT ? kMaxGroup * kQRow * 2 : 0;
+  static constexpr size_t kRows = (kFlags + (kWarps + 4) * 4 + 15) & ~size_t(15);
+  static constexpr size_t kBytes = ROT ? kRows + size_t(kWarps) * kQBytes : kFlags + (kWarps + 4) * 4;
   // merge of a sequence's pieces over CTAs, in the ring's place
   static_assert(kRing >= size_t(kMaxCtas) * kMaxGroup * 12, "merge weights");
   static_assert(size_t(kStages) * kStage >= sizeof(Piece<D>), "a warp's last piece");
@@ -687,12 +698,86 @@ __device__ __forceinline__ float append_row(const Params& p, uint8_t* tiles, siz
   return scale;
 }
 
-template <typename T, bool Q8, int D, bool APPEND>
-__global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
+// A query row's 16 rotated values (an item of row lane / NJ; the NJ lanes of a
+// row call together) as f16 in the warp's rows, `to` + at.x and at.y, brought to
+// f16's range by a power of two of the row's largest (its exponent is
+// returned): a row of any size keeps every bit down to 2^-38 of its largest
+// element.  f16 queries: x is left with what the rounding left over.
+template <int NJ, bool REST>
+__device__ __forceinline__ int place_q(float (&x)[16], uint16_t* to, const int2 at) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = NJ / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int e0 = int(top >> 23);  // biased exponent; 0: nothing, 255: not finite
+  const int e = e0 == 0 || e0 == 255 ? 0 : max(e0 - 127 - 13, -120);
+  const float down = __uint_as_float(uint32_t(127 - e) << 23);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] *= down;
+    x[2 * i + 1] *= down;
+    w[i] = dev::Mma<__half>::pack(x[2 * i], x[2 * i + 1]);
+    if constexpr (REST) {
+      // (of an infinity nothing is left over)
+      const float2 f = dev::Mma<__half>::unpack(w[i]);
+      x[2 * i] = fabsf(f.x) < INFINITY ? x[2 * i] - f.x : 0.f;
+      x[2 * i + 1] = fabsf(f.y) < INFINITY ? x[2 * i + 1] - f.y : 0.f;
+    }
+  }
+  *reinterpret_cast<uint4*>(to + at.x) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(to + at.y) = make_uint4(w[4], w[5], w[6], w[7]);
+  return e;
+}
+
+// The new K row rotated, 8 columns a lane (lanes 0 - 15; the others hold V's and
+// keep it), in 32 bits.
+template <typename T, int D>
+__device__ __forceinline__ q8::Row8<float> rotate_row(const Params& p, const q8::Row8<T>& x,
+                                                      const rot::WarpAngles<D>& angles) {
+  const int lane = threadIdx.x & 31, chunk = lane & 15, half = p.rot.dim / 16;
+  rot::Chunk<T> raw;
+  raw.v[0] = x.v;
+  float y[8], c[8], s[8];
+  raw.to_float(y);
+  const bool second = !p.rot.interleaved && chunk >= half;
+  const int j = p.rot.interleaved ? chunk / 2 : second ? chunk - half : chunk;
+  angles.gather(j & (rot::WarpAngles<D>::NJ - 1), c, s);
+  const int from = lane + (chunk < half ? half : -half);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float other = __shfl_sync(0xffffffffu, y[i], from & 31);
+    if (lane >= 16 || p.rot.interleaved || chunk >= 2 * half) continue;
+    float a = second ? other : y[i], b = second ? y[i] : other;
+    rot::turn_pair(a, b, c[i], s[i]);
+    y[i] = second ? b : a;
+  }
+  if (lane < 16 && p.rot.interleaved && 8 * chunk < p.rot.dim) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      rot::turn_pair(y[2 * i], y[2 * i + 1], chunk & 1 ? c[4 + i] : c[i], chunk & 1 ? s[4 + i] : s[i]);
+  }
+  q8::Row8<float> out;
+  out.v[0] = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+  out.v[1] = make_uint4(__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7]));
+  return out;
+}
+
+// ROT (with APPEND): the query rows and the new K row are rotated on the way.  A
+// segment's rows are loaded as items (rotary.cuh), rotated in registers, and
+// turned into fragments through the warp's shared memory.  They are rounded to
+// f16, not to T; where T is f16, what that leaves over goes through a second
+// product (outputs 2.8e-4 from 64-bit arithmetic, 3.8e-4 without).
+template <typename T, bool Q8, int D, bool APPEND, bool ROT>
+__global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const Params p) {
-  using S = Tiles<T, Q8, D>;
+  using S = Tiles<T, Q8, D, ROT>;
   using Mm = typename S::Mm;
+  static_assert(!ROT || (Q8 && APPEND), "rotation is built for the 8-bit append");
+  constexpr bool kRest = ROT && std::is_same<T, __half>::value;
+  constexpr int NJ = D / 16;  // 16-column items of a row's rotation
   constexpr int ST = S::kStages, kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr bool kTwoParts = S::kTwoParts;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -805,11 +890,30 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
   // a segment's query rows are loaded a segment ahead; the first one's before
   // the table entries that the copies wait for
   uint4 raw[D / 32];
-  auto fetch_q = [&](int qb, int qh) {
-    load_q<T, Q8, D>(static_cast<const T*>(p.q) + (size_t(qb) * p.num_q_heads + qh * G + g) * D, g < G, t, raw);
+  int position = 0;           // of the segment's new token
+  int64_t freqs[ROT ? D / 64 : 1];
+  uint16_t* rows = reinterpret_cast<uint16_t*>(smem + S::kRows + size_t(warp) * S::kQBytes);
+  auto fetch_q = [&](int qb, int qh, int length) {
+    if constexpr (ROT) {
+      const int2 at = rot::item_columns(p.rot, lane % NJ);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const int r = i * (32 / NJ) + lane / NJ;
+        const T* row = static_cast<const T*>(p.q) + qb * p.q_stride + (qh * G + r) * D;
+        raw[2 * i] = raw[2 * i + 1] = make_uint4(0, 0, 0, 0);
+        if (r < G) {
+          raw[2 * i] = *reinterpret_cast<const uint4*>(row + at.x);
+          raw[2 * i + 1] = *reinterpret_cast<const uint4*>(row + at.y);
+        }
+      }
+      position = p.positions ? p.positions[qb] : length - 1;
+    } else {
+      load_q<T, Q8, D>(static_cast<const T*>(p.q) + (size_t(qb) * p.num_q_heads + qh * G + g) * D, g < G, t, raw);
+    }
   };
   if (count > 0) {
-    fetch_q(start.x, start.y);
+    fetch_q(start.x, start.y, start_seq.x);
+    if constexpr (ROT) rot::WarpAngles<D>::load_freqs(p.rot, lane, freqs);
     fill();
   }
   for (int i = 0; i < ST && issued < count; ++i) issue();
@@ -829,7 +933,60 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
     const int run = min(seq.y - v, count - done);
     const bool starts = v == 0, ends = v + run == seq.y;
     uint32_t qf[S::kSteps][2];
-    const int qexp = convert_q<T, Q8, D>(raw, qf);
+    int qexp;
+    rot::WarpAngles<D> angles;
+    if constexpr (ROT) {
+      angles.set(freqs, position, p.rot.magnitude);
+      float c[8], sn[8];
+      angles.gather(lane % NJ, c, sn);
+      const int2 at = rot::item_columns(p.rot, lane % NJ);
+      float x[D / 64][16];
+      int e[D / 64];
+      __syncwarp();  // (the last segment's rows are read)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        rot::Chunk<T> u, w;
+        u.v[0] = raw[2 * i];
+        w.v[0] = raw[2 * i + 1];
+        u.to_float(x[i]);
+        w.to_float(x[i] + 8);
+        if (16 * (lane % NJ) < p.rot.dim) rot::turn_item(p.rot.interleaved, x[i], c, sn);
+        e[i] = place_q<NJ, kRest>(x[i], rows + (i * (32 / NJ) + lane / NJ) * S::kQRow, at);
+      }
+      __syncwarp();
+      // (rows past the group were loaded as zeros)
+      auto fragments = [&](uint4 (&w)[D / 32]) {
+        load_q<__half, Q8, D>(reinterpret_cast<const __half*>(rows + g * S::kQRow), true, t, w);
+      };
+      fragments(raw);
+      convert_q<__half, Q8, D>(raw, qf);
+      // row g's exponent: item 0 of the row has it
+      qexp = __shfl_sync(0xffffffffu, e[0], (g % (32 / NJ)) * NJ);
+      if constexpr (D == 128) {
+        const int high = __shfl_sync(0xffffffffu, e[D / 64 - 1], (g % (32 / NJ)) * NJ);
+        if (g >= 32 / NJ) qexp = high;
+      }
+      if constexpr (kRest) {
+        // what the rounding left over, as fragments, each lane's together
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          uint16_t* to = rows + (i * (32 / NJ) + lane / NJ) * S::kQRow;
+          rot::Chunk<__half> u, w;
+          u.from_float(x[i]);
+          w.from_float(x[i] + 8);
+          u.store(reinterpret_cast<__half*>(to + at.x));
+          w.store(reinterpret_cast<__half*>(to + at.y));
+        }
+        __syncwarp();
+        fragments(raw);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) reinterpret_cast<uint4*>(rows)[i * 32 + lane] = raw[i];
+      }
+    } else {
+      qexp = convert_q<T, Q8, D>(raw, qf);
+    }
     // the next segment: the sequence's next head, or the next sequence that
     // has tokens
     int nb = b, nh = h + 1;
@@ -840,7 +997,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
         do nseq = p.seqs[++nb];
         while (nseq.y == 0);
       }
-      fetch_q(nb, nh);
+      fetch_q(nb, nh, nseq.x);
     }
     float f0 = p.scale_log2, f1 = p.scale_log2;
     if constexpr (Q8) {
@@ -858,7 +1015,9 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
       if (ends) {
         if ((lane & 15) < D / 8)
           fresh.load(static_cast<const T*>(lane >> 4 ? p.new_rows[1] : p.new_rows[0]) +
-                     (size_t(b) * Hkv + h) * D + 8 * (lane & 15));
+                     (ROT ? b * (lane >> 4 ? p.new_stride[1] : p.new_stride[0]) + h * D
+                          : int64_t((size_t(b) * Hkv + h) * D)) +
+                     8 * (lane & 15));
         const int length = p.context_lens[b];
         const int phys = p.block_tables[size_t(b) * p.max_blocks + (seq.x - 1) / kBlockSize];
         if (length != seq.x) {
@@ -921,6 +1080,12 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
         for (int k = 0; k < S::kSteps; k += 2) {
           Mm::run(s[i], f[k][0], f[k][1], f[k][2], f[k][3], qf[k][0], qf[k][1]);
           Mm::run(s2[i], f[k + 1][0], f[k + 1][1], f[k + 1][2], f[k + 1][3], qf[k + 1][0], qf[k + 1][1]);
+          if constexpr (kRest) {
+            // (convert_q's order: two steps to 16 bytes)
+            const uint4 w = reinterpret_cast<const uint4*>(rows)[k / 2 * 32 + lane];
+            Mm::run(s[i], f[k][0], f[k][1], f[k][2], f[k][3], w.x, w.y);
+            Mm::run(s2[i], f[k + 1][0], f[k + 1][1], f[k + 1][2], f[k + 1][3], w.z, w.w);
+          }
         }
       }
       // ---- base-2 scores of tokens t0 + g (x[0], x[1]) and t0 + g + 8
@@ -1042,7 +1207,12 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D>::kThreads, 1)
       const int stage = get + n - 1 < ST ? get + n - 1 : get + n - 1 - ST;
       ok = __all_sync(0xffffffffu, dev::mbar_wait_bounded(&full[stage], parity ^ int(stage < get), tmo, p.status));
       if (!ok) return;
-      const float now = append_row<T, D>(p, ring + stage * S::kStage, size_t(own), (seq.x - 1) & 15, old, fresh);
+      float now;
+      if constexpr (ROT)
+        now = append_row<float, D>(p, ring + stage * S::kStage, size_t(own), (seq.x - 1) & 15, old,
+                                   rotate_row<T, D>(p, fresh, angles));
+      else
+        now = append_row<T, D>(p, ring + stage * S::kStage, size_t(own), (seq.x - 1) & 15, old, fresh);
       const float now_k = __shfl_sync(0xffffffffu, now, 0), now_v = __shfl_sync(0xffffffffu, now, 16);
       const int x = done + n - 1;
       if (lane == (x & 31)) {
@@ -1321,11 +1491,15 @@ DeviceState g_dev[kMaxDevices];
 template <typename T, bool Q8, int D>
 cudaError_t configure() {
   const int bytes = int(Tiles<T, Q8, D>::kBytes);
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, false>,
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, false, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if constexpr (Q8) {
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               bytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(Tiles<T, Q8, D, true>::kBytes));
   }
   return e;
 }
@@ -1387,6 +1561,9 @@ struct Call {
   void* stream;
   bool append = false;
   const void *k_new = nullptr, *v_new = nullptr;
+  rot::Args rot = {};  // freqs null: none
+  const int32_t* positions = nullptr;
+  int64_t q_stride = 0, k_stride = 0, v_stride = 0;
 };
 
 int check_sizes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks,
@@ -1411,9 +1588,13 @@ cudaError_t launch_attend(cudaLaunchConfig_t cfg, const CUtensorMap& mk, const C
   cfg.blockDim = dim3(Tiles<T, Q8, D>::kThreads);
   cfg.dynamicSmemBytes = Tiles<T, Q8, D>::kBytes;
   if constexpr (Q8) {
-    if (p.new_rows[0]) return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true>, mk, mv, p);
+    if (p.rot.freqs) {
+      cfg.dynamicSmemBytes = Tiles<T, Q8, D, true>::kBytes;
+      return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true, true>, mk, mv, p);
+    }
+    if (p.new_rows[0]) return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true, false>, mk, mv, p);
   }
-  return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, false>, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, false, false>, mk, mv, p);
 }
 
 template <typename T, bool Q8>
@@ -1475,6 +1656,11 @@ int entry(const Call& c) {
     p.scales[0] = const_cast<float*>(c.k_scale);
     p.scales[1] = const_cast<float*>(c.v_scale);
   }
+  p.rot = c.rot;
+  p.positions = c.positions;
+  p.q_stride = c.q_stride;
+  p.new_stride[0] = c.k_stride;
+  p.new_stride[1] = c.v_stride;
   p.out = c.out;
   p.block_tables = c.block_tables;
   p.context_lens = c.context_lens;
@@ -1638,6 +1824,33 @@ PA_API int pa_paged_attention_decode_q8_append_run(
                         num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
                         num_blocks, scale, dtype, out, workspace, workspace_bytes, stream, true,
                         k_new, v_new});
+}
+
+PA_API int pa_paged_attention_decode_q8_rotary_append_run(
+    const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+    const int64_t* turns, int rotary_dim, int interleaved, float magnitude, void* k_cache,
+    void* v_cache, float* k_scale, float* v_scale, const int32_t* block_tables,
+    const int32_t* context_lens, int window, int num_sinks, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, int64_t q_stride,
+    int64_t k_stride, int64_t v_stride, float scale, int dtype, void* out, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  PA_TRACE("pa_paged_attention_decode_q8_rotary_append_run");
+  const char* who = "paged_attention_decode_q8_rotary_append_run";
+  window::Call c = {who, Mode::kRunOnly, true, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                    context_lens, window, num_sinks, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                    max_blocks_per_seq, num_blocks, scale, dtype, out, workspace, workspace_bytes,
+                    stream, true, k_new, v_new};
+  int rc = rot::check_stride(q_stride, 2, 0, "q_stride", who);
+  if (rc == PA_OK) rc = rot::check_stride(k_stride, 2, 0, "k_stride", who);
+  if (rc == PA_OK) rc = rot::check_stride(v_stride, 2, 0, "v_stride", who);
+  if (rc == PA_OK && num_seqs > 0)
+    rc = rot::check_args(turns, rotary_dim, interleaved, magnitude, head_dim, who, &c.rot);
+  if (rc != PA_OK) return rc;
+  c.positions = positions;
+  c.q_stride = q_stride;
+  c.k_stride = k_stride;
+  c.v_stride = v_stride;
+  return window::entry(c);
 }
 
 }  // extern "C"

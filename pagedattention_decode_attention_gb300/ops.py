@@ -990,6 +990,395 @@ def prepare_block_dequantize(k_cache, v_cache, k_scale, v_scale, src_dst_pairs, 
     return Prepared(capi.lib().pa_block_dequantize, args, keep, dev)
 
 
+_SCALINGS = {None: capi.PA_ROTARY_PLAIN, "linear": capi.PA_ROTARY_LINEAR,
+             "base": capi.PA_ROTARY_BASE, "bands": capi.PA_ROTARY_BANDS}
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | None = None,
+                       factor: float = 1.0, original_context: int = 0, low: float = 1.0,
+                       high: float = 32.0) -> torch.Tensor:
+    """Angles per position (radians, float64 ``[rotary_dim / 2]`` on the host) of
+    rotary positions: ``base ** (-2 i / rotary_dim)``, scaled for long contexts
+    by ``"linear"``, ``"base"`` or ``"bands"`` (``low`` and ``high`` count a
+    pair's turns over ``original_context`` tokens; see ``pagedattn.h``)."""
+    _require(scaling in _SCALINGS, "scaling must be None, 'linear', 'base' or 'bands'")
+    out = torch.empty(max(int(rotary_dim) // 2, 0), dtype=torch.float64)
+    capi.check(capi.lib().pa_rotary_frequencies(
+        int(rotary_dim), float(base), _SCALINGS[scaling], float(factor), int(original_context),
+        float(low), float(high), C.cast(out.data_ptr(), C.POINTER(C.c_double))))
+    return out
+
+
+def rotary_turns(frequencies: torch.Tensor) -> torch.Tensor:
+    """Frequencies (radians per position) as the kernels take them: int64
+    fractions of a turn times 2^64, on the host."""
+    f = torch.as_tensor(frequencies, dtype=torch.float64).cpu().contiguous()
+    _require(f.dim() == 1, "frequencies must be one-dimensional")
+    out = torch.empty(f.shape, dtype=torch.int64)
+    capi.check(capi.lib().pa_rotary_turns(
+        C.cast(f.data_ptr(), C.POINTER(C.c_double)), f.numel(),
+        C.cast(out.data_ptr(), C.POINTER(C.c_int64))))
+    return out
+
+
+class Rotary:
+    """How a model's queries and keys are rotated: the frequencies, on the
+    device, with the layout of the pairs and the magnitude.  Made once and kept.
+
+    The first ``rotary_dim`` columns (default: all) of each head turn; pairs are
+    ``(i, i + rotary_dim / 2)``, or ``(2 i, 2 i + 1)`` with ``interleaved``.
+    ``base``, ``scaling``, ``factor``, ``original_context``, ``low`` and ``high``
+    are :func:`rotary_frequencies`'; ``frequencies`` (radians per position,
+    ``rotary_dim / 2`` of them) takes their place.  Rotated pairs are multiplied
+    by ``magnitude``."""
+
+    def __init__(self, head_dim: int, device, rotary_dim: int | None = None, base: float = 10000.0,
+                 interleaved: bool = False, scaling: str | None = None, factor: float = 1.0,
+                 original_context: int = 0, low: float = 1.0, high: float = 32.0,
+                 magnitude: float = 1.0, frequencies=None):
+        self.head_dim = int(head_dim)
+        self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
+        _require(self.head_dim in (64, 128), "head_dim must be 64 or 128")
+        _require(16 <= self.rotary_dim <= self.head_dim and self.rotary_dim % 16 == 0,
+                 "rotary_dim must be a multiple of 16, 16 .. head_dim")
+        _require(abs(float(magnitude)) < 3e38, "magnitude must be finite")
+        if frequencies is None:
+            frequencies = rotary_frequencies(self.rotary_dim, base, scaling, factor,
+                                             original_context, low, high)
+        turns = rotary_turns(frequencies)
+        _require(turns.numel() == self.rotary_dim // 2, "frequencies must be rotary_dim / 2 numbers")
+        self.interleaved, self.magnitude = bool(interleaved), float(magnitude)
+        self._keep(turns, device)
+
+    def _keep(self, turns, device):
+        # (a blocking copy: any stream may read it from here on)
+        self._host, self.turns = turns, turns.to(device)
+        self.device = self.turns.device
+
+    def transposed(self) -> "Rotary":
+        """The transposed rotation: what takes the gradients of rotated rows to
+        those of the rows (and undoes a rotation of magnitude 1)."""
+        other = object.__new__(Rotary)
+        other.__dict__.update(self.__dict__)
+        other._keep(-self._host, self.device)
+        return other
+
+    def _args(self, dev, head_dim):
+        """The C arguments, checked against the tensors they are used with."""
+        if self.device != dev:
+            raise ValueError(f"the rotation's frequencies must be on {dev}")
+        _require(self.head_dim == head_dim, "the rotation is for another head_dim")
+        return [C.c_void_p(self.turns.data_ptr()), self.rotary_dim, int(self.interleaved),
+                C.c_float(self.magnitude)]
+
+
+def _rows(name: str, t: torch.Tensor, device: torch.device, written: bool = False) -> int:
+    """Checks rows ``[T, H, d]`` whose heads lie side by side; their stride."""
+    if t.get_device() != device.index:
+        raise ValueError(f"{name} must be on {device}")
+    _require(t.dim() == 3, f"{name} must be [num_tokens, num_heads, head_dim]")
+    n, h, d = t.shape
+    if d > 1 and t.stride(2) != 1 or h > 1 and t.stride(1) != d:
+        raise ValueError(f"{name}'s heads must lie side by side")
+    if n <= 1:
+        return h * d
+    _require(not written or t.stride(0) >= h * d, f"{name}'s rows must not overlap")
+    return t.stride(0)
+
+
+def _positions_arg(positions, n, device):
+    if positions is None:
+        return C.c_void_p(None)
+    _cuda_contig("positions", positions, device)
+    _require(positions.dtype == torch.int32 and positions.shape == (n,),
+             "positions must be int32, one per row")
+    return C.c_void_p(positions.data_ptr())
+
+
+def _ptr(t):
+    return C.c_void_p(None if t is None else t.data_ptr())
+
+
+def _rotary_args(q, k, positions, rot, q_out, k_out, stream):
+    _require(q is not None or k is not None, "need q or k")
+    ref = q if q is not None else k
+    dev = ref.device
+    strides, heads = [], []
+    for name, t in (("q", q), ("k", k)):
+        strides.append(0 if t is None else _rows(name, t, dev))
+        heads.append(0 if t is None else t.shape[1])
+        _require(t is None or (t.dtype == ref.dtype and t.shape[0] == ref.shape[0]
+                               and t.shape[2] == ref.shape[2]),
+                 "q and k must be [num_tokens, num_heads, head_dim] of one dtype")
+    n, _, d = ref.shape
+    _require(positions is not None, "positions must be given")
+    where = _positions_arg(positions, n, dev)
+    code = _dtype_code(ref)
+    outs = []
+    for name, t, out in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if t is None:
+            _require(out is None, f"{name} without its input")
+            strides.append(0)
+        else:
+            if out is None:
+                out = _rows_out(t, stream)
+            strides.append(_rows(name, out, dev, True))
+            _require(out.shape == t.shape and out.dtype == t.dtype, f"{name} must match its input")
+        outs.append(out)
+    args = ([_ptr(q), _ptr(k), where] + rot._args(dev, d) + [n] + heads + [d]
+            + [C.c_int64(x) for x in strides] + [code, _ptr(outs[0]), _ptr(outs[1]),
+                                                 C.c_void_p(_stream(dev, stream))])
+    return dev, args, outs, (q, k, positions, rot, *outs)
+
+
+def _rows_out(t: torch.Tensor, stream) -> torch.Tensor:
+    """Contiguous rows like ``t``'s."""
+    if stream is None:
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    with _memory_of(stream, t.device):
+        out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    out.record_stream(torch.cuda.current_stream(t.device))   # (the caller reads it there)
+    return out
+
+
+def rotary(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor, rot: Rotary,
+           q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Query and key rows (``[T, Hq, d]``, ``[T, Hkv, d]``, heads side by side:
+    parts of a fused projection's output as they lie) rotated to ``positions``
+    (int32 ``[T]``); either may be None.  Returns ``(q_out, k_out)``; ``q_out=q``
+    (``k_out=k``) rotates in place.  Gradients: the same call on them with
+    ``rot.transposed()``."""
+    dev, args, outs, _ = _rotary_args(q, k, positions, rot, q_out, k_out, stream)
+    _call(dev, "pa_rotary", *args)
+    return outs[0], outs[1]
+
+
+def prepare_rotary(q, k, positions, rot: Rotary, q_out, k_out, stream=None) -> Prepared:
+    dev, args, _, keep = _rotary_args(q, k, positions, rot, q_out, k_out, stream)
+    return Prepared(capi.lib().pa_rotary, args, keep, dev)
+
+
+def _rotary_rows(q, k, v, dev, hkv, d):
+    """Checks the rows that go into a cache, and the queries beside them
+    (None: none); their strides."""
+    strides = [0 if q is None else _rows("q", q, dev), _rows("k", k, dev), _rows("v", v, dev)]
+    _require(k.dtype == v.dtype and k.shape == v.shape and tuple(k.shape[1:]) == (hkv, d),
+             "k, v must be [num_tokens, num_kv_heads, head_dim] of one dtype")
+    _require(q is None or (q.dtype == k.dtype and q.shape[0] == k.shape[0] and q.shape[2] == d),
+             "q must be [num_tokens, num_q_heads, head_dim] of k's dtype")
+    return strides
+
+
+def _rotary_q_out(q, q_out, dev, stream):
+    if q is None:
+        _require(q_out is None, "q_out without q")
+        return None, 0
+    if q_out is None:
+        q_out = _rows_out(q, stream)
+    stride = _rows("q_out", q_out, dev, True)
+    _require(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must match q")
+    return q_out, stride
+
+
+def _rotary_append_args(q, k, v, positions, rot, k_cache, v_cache, slot_mapping, q_out, stream):
+    dev = k_cache.device
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("slot_mapping", slot_mapping)):
+        _cuda_contig(name, t, dev)
+    _require(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[2] == 16,
+             "caches must be [num_blocks, num_kv_heads, 16, head_dim]")
+    nb, hkv, _, d = k_cache.shape
+    strides = _rotary_rows(q, k, v, dev, hkv, d)
+    n = k.shape[0]
+    _require(k.dtype == k_cache.dtype == v_cache.dtype, "dtypes must match")
+    _require(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (n,),
+             "slot_mapping must be int64 [num_tokens]")
+    _require(positions is not None, "positions must be given")
+    where, code = _positions_arg(positions, n, dev), _dtype_code(k)
+    q_out, q_out_stride = _rotary_q_out(q, q_out, dev, stream)
+    args = ([_ptr(q), _ptr(k), _ptr(v), where] + rot._args(dev, d)
+            + [_ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n,
+               0 if q is None else q.shape[1], hkv, d, nb]
+            + [C.c_int64(x) for x in strides + [q_out_stride]]
+            + [code, _ptr(q_out), C.c_void_p(_stream(dev, stream))])
+    return dev, args, q_out, (q, k, v, positions, rot, k_cache, v_cache, slot_mapping, q_out)
+
+
+def rotary_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                     positions: torch.Tensor, rot: Rotary, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                     q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """:func:`rotary` of ``q`` and ``k`` and :func:`kv_append` of the rotated
+    keys and ``v`` in one launch, bit for bit; returns the rotated queries.
+    Rows as in :func:`rotary`; ``q`` may be None.  A token with a negative slot
+    has its query rotated and stores nothing."""
+    dev, args, q_out, _ = _rotary_append_args(q, k, v, positions, rot, k_cache, v_cache,
+                                              slot_mapping, q_out, stream)
+    _call(dev, "pa_rotary_kv_append", *args)
+    return q_out
+
+
+def prepare_rotary_kv_append(q, k, v, positions, rot: Rotary, k_cache, v_cache, slot_mapping,
+                             q_out, stream=None) -> Prepared:
+    dev, args, _, keep = _rotary_append_args(q, k, v, positions, rot, k_cache, v_cache,
+                                             slot_mapping, q_out, stream)
+    return Prepared(capi.lib().pa_rotary_kv_append, args, keep, dev)
+
+
+def _rotary_append_q8_args(q, k, v, positions, rot, k_cache, v_cache, k_scale, v_scale,
+                           block_tables, context_lens, query_start, q_out, stream):
+    dev = k_cache.device
+    for name, t in (("block_tables", block_tables), ("context_lens", context_lens),
+                    ("query_start", query_start)):
+        _cuda_contig(name, t, dev)
+    nb, hkv, d = _q8_cache_args(k_cache, v_cache, k_scale, v_scale, dev)
+    strides = _rotary_rows(q, k, v, dev, hkv, d)
+    n = k.shape[0]
+    _require(block_tables.dtype == torch.int32 and block_tables.dim() == 2,
+             "block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    b, mb = block_tables.shape
+    _require(context_lens.dtype == torch.int32 and context_lens.shape == (b,),
+             "context_lens must be int32 [num_seqs]")
+    _require(query_start.dtype == torch.int32 and query_start.shape == (b + 1,),
+             "query_start must be int32 [num_seqs + 1]")
+    where, code = _positions_arg(positions, n, dev), _dtype_code(k)
+    q_out, q_out_stride = _rotary_q_out(q, q_out, dev, stream)
+    args = ([_ptr(q), _ptr(k), _ptr(v), where] + rot._args(dev, d)
+            + [_ptr(t) for t in (k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                                 query_start)]
+            + [b, n, 0 if q is None else q.shape[1], hkv, d, mb, nb]
+            + [C.c_int64(x) for x in strides + [q_out_stride]]
+            + [code, _ptr(q_out), C.c_void_p(_stream(dev, stream))])
+    return dev, args, q_out, (q, k, v, positions, rot, k_cache, v_cache, k_scale, v_scale,
+                              block_tables, context_lens, query_start, q_out)
+
+
+def rotary_kv_append_q8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor | None, rot: Rotary, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                        block_tables: torch.Tensor, context_lens: torch.Tensor,
+                        query_start: torch.Tensor, q_out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor | None:
+    """:func:`kv_append_q8` with keys rotated on the way (quantised from 32
+    bits), and ``q``'s rows rotated to ``q_out``, in one launch; returns the
+    rotated queries.  ``positions`` None: each token's place in its sequence.
+    Rows of no sequence keep their ``q_out``."""
+    dev, args, q_out, _ = _rotary_append_q8_args(q, k, v, positions, rot, k_cache, v_cache,
+                                                 k_scale, v_scale, block_tables, context_lens,
+                                                 query_start, q_out, stream)
+    _call(dev, "pa_rotary_kv_append_q8", *args)
+    return q_out
+
+
+def prepare_rotary_kv_append_q8(q, k, v, positions, rot: Rotary, k_cache, v_cache, k_scale,
+                                v_scale, block_tables, context_lens, query_start, q_out,
+                                stream=None) -> Prepared:
+    dev, args, _, keep = _rotary_append_q8_args(q, k, v, positions, rot, k_cache, v_cache, k_scale,
+                                                v_scale, block_tables, context_lens, query_start,
+                                                q_out, stream)
+    return Prepared(capi.lib().pa_rotary_kv_append_q8, args, keep, dev)
+
+
+def _decode_rotary_args(q, k_new, v_new, positions, rot, slot_mapping, scales, k_cache, v_cache,
+                        block_tables, context_lens, window, num_sinks, scale, workspace, out,
+                        stream):
+    """What both rotating decodes check (scales None: a cache of q's dtype)."""
+    _require(workspace is not None, "a run needs the workspace that holds its plan")
+    dev = q.device
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
+                    ("context_lens", context_lens), ("workspace", workspace)):
+        _cuda_contig(name, t, dev)
+    if scales is None:
+        _require(k_cache.dtype == v_cache.dtype == q.dtype, "q and caches must share a dtype")
+        _require(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[2] == 16,
+                 "caches must be [num_blocks, num_kv_heads, 16, head_dim]")
+        nb, hkv, _, d = k_cache.shape
+    else:
+        nb, hkv, d = _q8_cache_args(k_cache, v_cache, *scales, dev)
+        _require(q.dtype in (torch.float16, torch.bfloat16), "q must be float16 or bfloat16")
+    strides = _rotary_rows(q, k_new, v_new, dev, hkv, d)
+    b, hq, _ = q.shape
+    _require(block_tables.dtype == torch.int32 and block_tables.dim() == 2
+             and block_tables.shape[0] == b,
+             "block_tables must be int32 [num_seqs, max_blocks_per_seq]")
+    _require(context_lens.dtype == torch.int32 and context_lens.shape == (b,),
+             "context_lens must be int32 [num_seqs]")
+    if scales is None:
+        _cuda_contig("slot_mapping", slot_mapping, dev)
+        _require(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (b,),
+                 "slot_mapping must be int64 [num_seqs]")
+    where, code = _positions_arg(positions, b, dev), _dtype_code(q)
+    if out is None:
+        out = _rows_out(q, stream)
+    _cuda_contig("out", out, dev)
+    _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    args = [_ptr(q), _ptr(k_new), _ptr(v_new), where] + rot._args(dev, d)
+    if scales is None:
+        args += [_ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                 _ptr(context_lens)]
+    else:
+        args += [_ptr(t) for t in (k_cache, v_cache, *scales, block_tables, context_lens)]
+        args += list(_window_ints(window, num_sinks))
+    args += ([b, hq, hkv, d, block_tables.shape[1], nb] + [C.c_int64(x) for x in strides]
+             + [C.c_float(scale), code, _ptr(out), _ptr(workspace),
+                C.c_size_t(workspace.numel() * workspace.element_size()),
+                C.c_void_p(_stream(dev, stream))])
+    return dev, args, out, (q, k_new, v_new, positions, rot, slot_mapping, scales, k_cache,
+                            v_cache, block_tables, context_lens, workspace, out)
+
+
+def paged_attention_decode_rotary_append_run(q, k_new, v_new, positions, rot: Rotary, slot_mapping,
+                                             k_cache, v_cache, block_tables, context_lens, scale,
+                                             workspace: torch.Tensor, out=None,
+                                             stream=None) -> torch.Tensor:
+    """:func:`paged_attention_decode_append_run` whose ``q`` and ``k_new`` are
+    rotated on the way, in one launch on the same plan.  ``positions`` (int32
+    ``[B]``) None: ``context_lens - 1``.  Rows of ``q``, ``k_new`` and ``v_new``
+    as in :func:`rotary`.  The caches end up as :func:`rotary_kv_append` leaves
+    them; the rotated query is not rounded to 16 bits before its product."""
+    dev, args, out, _ = _decode_rotary_args(q, k_new, v_new, positions, rot, slot_mapping, None,
+                                            k_cache, v_cache, block_tables, context_lens, 0, 0,
+                                            scale, workspace, out, stream)
+    _call(dev, "pa_paged_attention_decode_rotary_append_run", *args)
+    return out
+
+
+def prepare_decode_rotary_append_run(q, k_new, v_new, positions, rot: Rotary, slot_mapping,
+                                     k_cache, v_cache, block_tables, context_lens, scale,
+                                     workspace, out, stream=None) -> Prepared:
+    dev, args, _, keep = _decode_rotary_args(q, k_new, v_new, positions, rot, slot_mapping, None,
+                                             k_cache, v_cache, block_tables, context_lens, 0, 0,
+                                             scale, workspace, out, stream)
+    return Prepared(capi.lib().pa_paged_attention_decode_rotary_append_run, args, keep, dev)
+
+
+def paged_attention_decode_q8_rotary_append_run(q, k_new, v_new, positions, rot: Rotary, k_cache,
+                                                v_cache, k_scale, v_scale, block_tables,
+                                                context_lens, window: int, num_sinks: int,
+                                                scale: float, workspace: torch.Tensor, out=None,
+                                                stream=None) -> torch.Tensor:
+    """:func:`paged_attention_decode_q8_append_run` whose ``q`` and ``k_new`` are
+    rotated on the way, in one launch on the same plan.  ``positions`` (int32
+    ``[B]``) None: ``context_lens - 1``.  Codes and scales end up as
+    :func:`rotary_kv_append_q8` leaves them."""
+    dev, args, out, _ = _decode_rotary_args(q, k_new, v_new, positions, rot, None,
+                                            (k_scale, v_scale), k_cache, v_cache, block_tables,
+                                            context_lens, window, num_sinks, scale, workspace, out,
+                                            stream)
+    _call(dev, "pa_paged_attention_decode_q8_rotary_append_run", *args)
+    return out
+
+
+def prepare_decode_q8_rotary_append_run(q, k_new, v_new, positions, rot: Rotary, k_cache, v_cache,
+                                        k_scale, v_scale, block_tables, context_lens, window: int,
+                                        num_sinks: int, scale: float, workspace, out,
+                                        stream=None) -> Prepared:
+    dev, args, _, keep = _decode_rotary_args(q, k_new, v_new, positions, rot, None,
+                                             (k_scale, v_scale), k_cache, v_cache, block_tables,
+                                             context_lens, window, num_sinks, scale, workspace,
+                                             out, stream)
+    return Prepared(capi.lib().pa_paged_attention_decode_q8_rotary_append_run, args, keep, dev)
+
+
 class LayerCaches:
     """Every layer's K and V cache (``[num_blocks, Hkv, 16, d]`` each), checked
     once, with the per-layer pointer arrays the multi-layer copies pass
