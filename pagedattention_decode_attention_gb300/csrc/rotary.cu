@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "pagedattn.h"
@@ -18,7 +19,7 @@ namespace rot {
 namespace {
 
 constexpr int kBlockSize = 16;
-constexpr int kMaxWarps = 16;
+constexpr int kThreads = 128;
 
 struct Params {
   const void* src[3];  // q, k, v
@@ -26,6 +27,10 @@ struct Params {
   int64_t src_stride[3], dst_stride[3];
   int heads[3];
   int groups[3];       // warps a token's rows take (see rows_kernel)
+  int num_tokens;
+  int parts;           // warps that share a token's groups: `share` each, the
+  int share, extra;    // first `extra` one more
+  bool wide;           // every row begins on a 32-byte boundary
   const int32_t* positions;
   const int32_t* lengths;  // without positions: a token is at lengths[token] - 1
   const int64_t* slots;
@@ -34,61 +39,105 @@ struct Params {
   unsigned* status;
 };
 
-// A warp takes 32 / NJ heads of one token, one item a lane.
-template <typename T, int D, bool APPEND>
-__global__ void rows_kernel(const Params p) {
-  constexpr int NJ = D / 16, kHeads = 32 / NJ;
-  dev::grid_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int group = blockIdx.y * (blockDim.x >> 5) + warp;
-  int kind = 0;
-  while (kind < 3 && group >= p.groups[kind]) group -= p.groups[kind++];
-  dev::grid_dependency_wait();
-  if (kind == 3) return;
-  const int64_t token = blockIdx.x;
-  const int j = lane % NJ, head = group * kHeads + lane / NJ;
-  const bool live = head < p.heads[kind];
-  const bool turns = kind < 2;
-  const int2 at = turns ? item_columns(p.rot, j) : make_int2(16 * j, 16 * j + 8);
-  Chunk<T> a, b;
-  if (live) {
-    const T* row = static_cast<const T*>(p.src[kind]) + token * p.src_stride[kind] + int64_t(head) * D;
-    a.load(row + at.x);
-    b.load(row + at.y);
-  }
-  int64_t slot = 0;
-  if (APPEND && kind > 0) {
-    slot = p.slots[token];
-    if (slot >= p.num_slots) {
-      if (lane == 0) dev::flag_status(p.status, kStatusBounds);
+// An item's two chunks, in whole 32-byte sectors where they lie so (`wide`; for
+// 16-bit types the chunks must be neighbours, `joined`).
+template <typename T>
+__device__ __forceinline__ void load_item(const T* row, int2 at, bool wide, bool joined, Chunk<T>& a, Chunk<T>& b) {
+  if constexpr (sizeof(T) == 4) {
+    if (wide) {
+      load32(row + at.x, a.v[0], a.v[1]);
+      load32(row + at.y, b.v[0], b.v[1]);
       return;
     }
-    if (slot < 0) return;
+  } else if (wide && joined) {
+    load32(row + at.x, a.v[0], b.v[0]);
+    return;
   }
-  if (turns) {
-    WarpAngles<D> angles;
-    int64_t f[WarpAngles<D>::kPer];
-    angles.load_freqs(p.rot, lane, f);
-    angles.set(f, p.positions ? p.positions[token] : p.lengths[token] - 1, p.rot.magnitude);
-    float c[8], s[8];
-    angles.gather(j, c, s);
-    if (16 * j < p.rot.dim) {
-      float x[16];
-      a.to_float(x);
-      b.to_float(x + 8);
-      turn_item(p.rot.interleaved, x, c, s);
-      a.from_float(x);
-      b.from_float(x + 8);
+  a.load(row + at.x);
+  b.load(row + at.y);
+}
+template <typename T>
+__device__ __forceinline__ void store_item(T* row, int2 at, bool wide, bool joined, const Chunk<T>& a,
+                                           const Chunk<T>& b) {
+  if constexpr (sizeof(T) == 4) {
+    if (wide) {
+      store32(row + at.x, a.v[0], a.v[1]);
+      store32(row + at.y, b.v[0], b.v[1]);
+      return;
     }
+  } else if (wide && joined) {
+    store32(row + at.x, a.v[0], b.v[0]);
+    return;
   }
-  if (!live) return;
-  T* row = static_cast<T*>(p.dst[kind]);
-  if (APPEND && kind > 0)
-    row += ((slot / kBlockSize * p.heads[kind] + head) * kBlockSize + slot % kBlockSize) * D;
-  else
-    row += token * p.dst_stride[kind] + int64_t(head) * D;
   a.store(row + at.x);
   b.store(row + at.y);
+}
+
+// A group is 32 / NJ heads of one of a token's q, k and v, one item a lane; a warp
+// takes N groups of one token, all its loads before anything else.
+template <typename T, int D, bool APPEND, int N>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const Params p) {
+  constexpr int NJ = D / 16, kHeads = 32 / NJ;
+  dev::grid_launch_dependents();
+  const int lane = threadIdx.x, j = lane % NJ;
+  const int64_t token = int64_t(blockIdx.x) * blockDim.z + threadIdx.z;
+  const int part = blockIdx.y * blockDim.y + threadIdx.y;
+  if (token >= p.num_tokens || part >= p.parts) return;
+  const int group0 = N == 1 ? part : part * p.share + min(part, p.extra);
+  const int count = N == 1 ? 1 : p.share + (part < p.extra ? 1 : 0);
+  int64_t f[WarpAngles<D>::kPer];
+  const int2 turned = item_columns(p.rot, j);
+  // (what a group is follows from its number, for the whole warp)
+  auto locate = [&](int i, int& head) {
+    int group = group0 + i, kind = 0;
+    while (kind < 2 && group >= p.groups[kind]) group -= p.groups[kind++];
+    head = group * kHeads + lane / NJ;
+    return kind;
+  };
+  dev::grid_dependency_wait();
+  const int position = p.positions ? p.positions[token] : p.lengths[token] - 1;
+  int64_t slot = 0;
+  if (APPEND) slot = p.slots[token];
+  WarpAngles<D>::load_freqs(p.rot, lane, f);
+  Chunk<T> a[N], b[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    int head;
+    const int kind = locate(i, head);
+    if (i >= count || head >= p.heads[kind]) continue;
+    const T* row = static_cast<const T*>(p.src[kind]) + token * p.src_stride[kind] + int64_t(head) * D;
+    load_item(row, kind < 2 ? turned : make_int2(16 * j, 16 * j + 8), p.wide, kind == 2 || p.rot.interleaved, a[i],
+              b[i]);
+  }
+  WarpAngles<D> angles;
+  angles.set(f, position, p.rot.magnitude);
+  float c[8], s[8];
+  angles.gather(j, c, s);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    int head;
+    const int kind = locate(i, head);
+    if (i >= count) break;
+    if (kind < 2 && 16 * j < p.rot.dim) {
+      float x[16];
+      a[i].to_float(x);
+      b[i].to_float(x + 8);
+      turn_item(p.rot.interleaved, x, c, s);
+      a[i].from_float(x);
+      b[i].from_float(x + 8);
+    }
+    T* row = static_cast<T*>(p.dst[kind]);
+    if (APPEND && kind > 0) {
+      if (slot >= p.num_slots && lane == 0) dev::flag_status(p.status, kStatusBounds);
+      if (slot < 0 || slot >= p.num_slots) continue;
+      row += ((slot / kBlockSize * p.heads[kind] + head) * kBlockSize + slot % kBlockSize) * D;
+    } else {
+      row += token * p.dst_stride[kind] + int64_t(head) * D;
+    }
+    if (head >= p.heads[kind]) continue;
+    store_item(row, kind < 2 ? turned : make_int2(16 * j, 16 * j + 8), p.wide, kind == 2 || p.rot.interleaved, a[i],
+               b[i]);
+  }
 }
 
 int elem_bytes(int dtype) { return dtype == PA_F32 ? 4 : 2; }
@@ -108,34 +157,67 @@ int check_rows(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, 
   return PA_OK;
 }
 
+template <typename T, int D, bool APPEND>
+cudaError_t launch_rows(Params p, int groups, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto go = [&](auto number) {
+    constexpr int N = decltype(number)::value;
+    p.parts = (groups + N - 1) / N;
+    p.share = groups / p.parts;
+    p.extra = groups % p.parts;
+    const int wide = p.parts < kThreads / 32 ? p.parts : kThreads / 32;
+    const int tokens = kThreads / 32 / wide;
+    cfg.gridDim = dim3(unsigned((int64_t(p.num_tokens) + tokens - 1) / tokens),
+                       unsigned((p.parts + wide - 1) / wide));
+    cfg.blockDim = dim3(32, unsigned(wide), unsigned(tokens));
+    return cudaLaunchKernelEx(&cfg, rows_kernel<T, D, APPEND, N>, p);
+  };
+  // A warp's angles cost as much as two groups' rotation, and what a warp has
+  // in flight hides its latency: the more groups it takes the better, as long
+  // as the warps fill the GPU.  (16-bit rows, one group, three, four: 2.4, 2.6,
+  // 2.8 us for 128 tokens of 12 groups; 5.8, 4.1, 4.5 for 1024; 31.2, 25.2,
+  // 25.6 for 6401; 48.1, 38.0, 36.0 for 7200 of 16.)  A group of 32-bit rows is
+  // twice the bytes, and one a warp is enough (17.0 us for 3268 tokens of 8
+  // groups, 17.0 with three, 17.1 with four).
+  const int64_t units = int64_t(p.num_tokens) * groups;
+  if constexpr (sizeof(T) == 2) {
+    if (units > 100000 && (groups + 3) / 4 < (groups + 2) / 3) return go(std::integral_constant<int, 4>());
+    if (units > 7000) return go(std::integral_constant<int, 3>());
+  }
+  return go(std::integral_constant<int, 1>());
+}
+
 template <bool APPEND>
 int launch(Params& p, int num_tokens, int head_dim, int dtype, void* stream, const char* who) {
   p.status = device_status_word();
   if (!p.status) return PA_ERR_CUDA;
+  p.num_tokens = num_tokens;
+  uintptr_t ends = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!p.heads[i]) continue;
+    ends |= reinterpret_cast<uintptr_t>(p.src[i]) | reinterpret_cast<uintptr_t>(p.dst[i]);
+    ends |= uintptr_t(p.src_stride[i] * elem_bytes(dtype)) | uintptr_t(p.dst_stride[i] * elem_bytes(dtype));
+  }
+  p.wide = (ends & 31) == 0;
   const int per = 32 / (head_dim / 16);
   int groups = 0;
   for (int i = 0; i < 3; ++i) groups += p.groups[i] = (p.heads[i] + per - 1) / per;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  const int gy = (groups + kMaxWarps - 1) / kMaxWarps;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(num_tokens), unsigned(gy));
-  cfg.blockDim = dim3(unsigned((groups + gy - 1) / gy * 32));
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const bool wide = head_dim == 128;
   if (dtype == PA_F32)
-    e = wide ? cudaLaunchKernelEx(&cfg, rows_kernel<float, 128, APPEND>, p)
-             : cudaLaunchKernelEx(&cfg, rows_kernel<float, 64, APPEND>, p);
+    e = wide ? launch_rows<float, 128, APPEND>(p, groups, s) : launch_rows<float, 64, APPEND>(p, groups, s);
   else if (dtype == PA_F16)
-    e = wide ? cudaLaunchKernelEx(&cfg, rows_kernel<__half, 128, APPEND>, p)
-             : cudaLaunchKernelEx(&cfg, rows_kernel<__half, 64, APPEND>, p);
+    e = wide ? launch_rows<__half, 128, APPEND>(p, groups, s) : launch_rows<__half, 64, APPEND>(p, groups, s);
   else
-    e = wide ? cudaLaunchKernelEx(&cfg, rows_kernel<__nv_bfloat16, 128, APPEND>, p)
-             : cudaLaunchKernelEx(&cfg, rows_kernel<__nv_bfloat16, 64, APPEND>, p);
+    e = wide ? launch_rows<__nv_bfloat16, 128, APPEND>(p, groups, s)
+             : launch_rows<__nv_bfloat16, 64, APPEND>(p, groups, s);
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
   return PA_OK;
 }
