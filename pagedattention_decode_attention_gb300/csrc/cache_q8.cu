@@ -11,6 +11,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "pagedattn.h"
 #include "q8.cuh"
@@ -218,121 +220,189 @@ struct RotaryAppendParams {
   rot::Args rot;
 };
 
-// One (unit, head of Q, K or V), by a warp, as append_block; a lane takes item
-// lane % NJ of rows lane / NJ, + 32 / NJ, ....  K and V are quantised from 32
-// bits: a rotated key is rounded once, to its code.  `angles`: the cosines and
-// sines of the unit's rows.
-template <typename T, int D>
-__device__ __forceinline__ void rotary_block(const RotaryAppendParams& p, const int4 seq, int unit, int job,
-                                             const float2 (&angles)[kBlockSize][D / 2], int lane) {
-  constexpr int NJ = D / 16, kRows = 32 / NJ, kPasses = kBlockSize / kRows;
-  const int b = seq.x, q0 = seq.y, q1 = seq.z, ctx = seq.w;
-  const int begin = ctx - (q1 - q0);
-  const int blk = begin / kBlockSize + (unit - (q0 / kBlockSize + 2 * b));
-  const int lo = max(begin - blk * kBlockSize, 0);
-  const int hi = min(ctx - blk * kBlockSize, kBlockSize);
-  const int kv = job < 2 * p.a.num_kv_heads ? job & 1 : 2;  // K, V, Q
-  const int head = kv < 2 ? job >> 1 : job - 2 * p.a.num_kv_heads;
-  const int j = lane % NJ, row0 = lane / NJ;
-  const bool turns = kv != 1 && 16 * j < p.rot.dim;
-  const int2 at = kv != 1 ? rot::item_columns(p.rot, j) : make_int2(16 * j, 16 * j + 8);
-  // (row 0 of the block, which lies before the tokens when lo > 0)
-  const int64_t first = int64_t(q0) + blk * kBlockSize - begin;
-  const T* src = static_cast<const T*>(kv == 2 ? p.q : kv ? p.a.src[1] : p.a.src[0]) +
-                 first * p.stride[kv] + head * D;
-  float x[kPasses][16];
+// The cosines and sines of a unit's rows, an item's 8 pairs as 4 pieces of 16
+// bytes (two cosines, two sines), items side by side: the lanes of a row read
+// without bank conflicts.
+template <int D>
+struct UnitAngles {
+  float4 cs[kBlockSize][4][D / 16];
+  __device__ __forceinline__ void put(int row, int pair, float2 x) {
+    float* to = reinterpret_cast<float*>(&cs[row][(pair & 7) >> 1][pair >> 3]) + (pair & 1);
+    to[0] = x.x;
+    to[2] = x.y;
+  }
+  __device__ __forceinline__ void get(int row, int j, float (&c)[8], float (&s)[8]) const {
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = i * kRows + row0;
-    if (r < lo || r >= hi) continue;
-    rot::Chunk<T> u, w;
-    u.load(src + r * p.stride[kv] + at.x);
-    w.load(src + r * p.stride[kv] + at.y);
-    u.to_float(x[i]);
-    w.to_float(x[i] + 8);
-    if (turns) {
-      float c[8], s[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = angles[r][8 * j + e].x;
-        s[e] = angles[r][8 * j + e].y;
-      }
-      rot::turn_item(p.rot.interleaved, x[i], c, s);
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = cs[row][i][j];
+      c[2 * i] = x.x;
+      c[2 * i + 1] = x.y;
+      s[2 * i] = x.z;
+      s[2 * i + 1] = x.w;
     }
   }
-  if (kv == 2) {
-    T* to = static_cast<T*>(p.q_out) + first * p.q_out_stride + head * D;
+};
+
+// What a warp knows of its unit.
+struct Unit {
+  int lo, hi;      // rows of the block that are new
+  int64_t first;   // the query row that row 0 of the block would be
+  int phys;        // -1: not a block
+};
+
+// The new rows of one (unit, head of Q, K or V) as they lie in memory: a lane has item lane % NJ of rows lane / NJ, + 32 / NJ, ....
+template <typename T, int D>
+struct UnitRows {
+  static constexpr int NJ = D / 16, kRows = 32 / NJ, kPasses = kBlockSize / kRows;
+  rot::Chunk<T> u[kPasses], w[kPasses];
+  float old;  // K, V: the block's scale
+  int kv, head;
+  int2 at;
+
+  __device__ __forceinline__ void load(const RotaryAppendParams& p, const Unit& n, int job, int lane) {
+    kv = job < 2 * p.a.num_kv_heads ? job & 1 : 2;  // K, V, Q
+    head = kv < 2 ? job >> 1 : job - 2 * p.a.num_kv_heads;
+    const int j = lane % NJ, row0 = lane / NJ;
+    at = kv != 1 ? rot::item_columns(p.rot, j) : make_int2(16 * j, 16 * j + 8);
+    const T* from = static_cast<const T*>(kv == 2 ? p.q : kv ? p.a.src[1] : p.a.src[0]) +
+                    (n.first + row0) * p.stride[kv] + head * D;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int r = i * kRows + row0;
-      if (r < lo || r >= hi) continue;
-      rot::Chunk<T> u, w;
-      u.from_float(x[i]);
-      w.from_float(x[i] + 8);
-      u.store(to + r * p.q_out_stride + at.x);
-      w.store(to + r * p.q_out_stride + at.y);
-    }
-    return;
-  }
-  const int phys = p.a.block_tables[size_t(b) * p.a.max_blocks + blk];
-  if (phys < 0 || phys >= p.a.num_blocks) {
-    if (lane == 0) dev::flag_status(p.a.status, kStatusBounds);
-    return;
-  }
-  const size_t tile = size_t(phys) * p.a.num_kv_heads + head;
-  float* scale_at = (kv ? p.a.scale[1] : p.a.scale[0]) + tile;
-  const float old = lo > 0 ? *scale_at : 0.f;
-  // the largest finite magnitude
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = i * kRows + row0;
-    if (r < lo || r >= hi) continue;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint32_t m = __float_as_uint(x[i][e]) & 0x7FFFFFFFu;
-      if (m < 0x7F800000u) top = max(top, m);
-    }
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  const float want = __uint_as_float(pow2_bits(scale_exponent(top)));
-  const float scale = lo > 0 ? fmaxf(old, want) : want;
-  const float inv = 1.f / scale;
-  uint8_t* codes = (kv ? p.a.cache[1] : p.a.cache[0]) + tile * kBlockSize * D;
-  const bool grows = lo > 0 && scale > old;
-  const float factor = grows ? old / scale : 1.f;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = i * kRows + row0;
-    if (r >= hi || (r < lo && !grows)) continue;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint2* to = reinterpret_cast<uint2*>(codes + r * D + (h ? at.y : at.x));
-      if (r < lo) {
-        *to = rescale8(*to, factor);
-      } else {
-        uint32_t c[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = encode2(x[i][8 * h + 2 * e] * inv, x[i][8 * h + 2 * e + 1] * inv);
-        *to = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      if (r >= n.lo && r < n.hi) {
+        u[i].load(from + at.x);
+        w[i].load(from + at.y);
       }
+      from += kRows * p.stride[kv];
+    }
+    old = 0.f;
+    if (kv < 2 && n.lo > 0 && n.phys >= 0)
+      old = (kv ? p.a.scale[1] : p.a.scale[0])[size_t(n.phys) * p.a.num_kv_heads + head];
+  }
+
+  // Pass i's values, rotated (V: as they are).
+  template <bool INTER>
+  __device__ __forceinline__ void values(const RotaryAppendParams& p, const UnitAngles<D>& angles, int lane, int i,
+                                         float (&x)[16]) const {
+    u[i].to_float(x);
+    w[i].to_float(x + 8);
+    if (kv != 1 && 16 * (lane % NJ) < p.rot.dim) {
+      float c[8], s[8];
+      angles.get(i * kRows + lane / NJ, lane % NJ, c, s);
+      rot::turn_item(INTER, x, c, s);
     }
   }
-  if (lane == 0 && (lo == 0 || grows)) *scale_at = scale;
+};
+
+// The largest finite magnitude.
+__device__ __forceinline__ float largest_of(const float (&x)[16]) {
+  float m = 0.f;  // (NaN is passed over)
+#pragma unroll
+  for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]));
+  if (m == INFINITY) {
+    m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = fabsf(x[e]) < INFINITY ? fmaxf(m, fabsf(x[e])) : m;
+  }
+  return m;
 }
 
-// Units as append_kernel's; a warp owns one (unit, head of Q, K or V).
-template <typename T, int D>
-__global__ void __launch_bounds__(kAppendWarps * 32) rotary_append_kernel(const RotaryAppendParams p) {
+// Rotates and stores what was loaded.  K and V are quantised from 32 bits: a
+// rotated key is rounded once, to its code.  (Keys are rotated twice, for the
+// block's largest magnitude and for the codes: keeping the 32 or 64 values takes
+// a third of the warps, 46.1 us and 42.9 for 9900 tokens of 32 heads of 64.)
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void store_unit(const RotaryAppendParams& p, const Unit& n, int lane,
+                                           const UnitRows<T, D>& rows, const UnitAngles<D>& angles) {
+  using U = UnitRows<T, D>;
+  const int kv = rows.kv, row0 = lane / U::NJ;
+  const int2 at = rows.at;
+  if (kv == 2) {
+    T* to = static_cast<T*>(p.q_out) + (n.first + row0) * p.q_out_stride + rows.head * D;
+#pragma unroll
+    for (int i = 0; i < U::kPasses; ++i) {
+      const int r = i * U::kRows + row0;
+      if (r >= n.lo && r < n.hi) {
+        float x[16];
+        rows.template values<INTER>(p, angles, lane, i, x);
+        rot::Chunk<T> u, w;
+        u.from_float(x);
+        w.from_float(x + 8);
+        u.store(to + at.x);
+        w.store(to + at.y);
+      }
+      to += U::kRows * p.q_out_stride;
+    }
+    return;
+  }
+  if (n.phys < 0) return;
+  // the largest finite magnitude
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < U::kPasses; ++i) {
+    const int r = i * U::kRows + row0;
+    if (r < n.lo || r >= n.hi) continue;
+    float x[16];
+    rows.template values<INTER>(p, angles, lane, i, x);
+    m = fmaxf(m, largest_of(x));
+  }
+  const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+  const float want = __uint_as_float(pow2_bits(scale_exponent(top)));
+  const float scale = n.lo > 0 ? fmaxf(rows.old, want) : want;
+  const float inv = 1.f / scale;
+  const size_t tile = size_t(n.phys) * p.a.num_kv_heads + rows.head;
+  uint8_t* codes = (kv ? p.a.cache[1] : p.a.cache[0]) + (tile * kBlockSize + row0) * D;
+  if (n.lo > 0 && scale > rows.old) {
+    // older rows of the block: the same values under the larger scale
+    const float factor = rows.old / scale;
+#pragma unroll 1
+    for (int r = row0; r < n.lo; r += U::kRows) {
+      uint2* a = reinterpret_cast<uint2*>(codes + (r - row0) * D + at.x);
+      uint2* b = reinterpret_cast<uint2*>(codes + (r - row0) * D + at.y);
+      *a = rescale8(*a, factor);
+      *b = rescale8(*b, factor);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U::kPasses; ++i) {
+    const int r = i * U::kRows + row0;
+    if (r < n.lo || r >= n.hi) continue;
+    float x[16];
+    rows.template values<INTER>(p, angles, lane, i, x);
+    uint32_t c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 y = rot::mul2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(inv, inv));
+      c[e] = encode2(y.x, y.y);
+    }
+    *reinterpret_cast<uint2*>(codes + i * U::kRows * D + at.x) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    *reinterpret_cast<uint2*>(codes + i * U::kRows * D + at.y) = make_uint2(c[4] | c[5] << 16, c[6] | c[7] << 16);
+  }
+  if (lane == 0 && (n.lo == 0 || scale > rows.old)) (kv ? p.a.scale[1] : p.a.scale[0])[tile] = scale;
+}
+
+// Units as append_kernel's; a warp takes every (8 gridDim.y)-th head of Q, K and V
+// of its unit.  Bound by bytes and, nearly, by instructions (2.2 a cycle and SM;
+// the angles are shared by a CTA, products go two to an instruction): 10.6 K
+// tokens of 32/8 heads, 238 MB, 39.3 us, 0.90 of the copy rate; 9.9 K of 32/32
+// heads of 64, 203 MB, 41.2 us, 0.73 (half of its rows are quantised).  Three
+// CTAs an SM: two 48.5 us, four 53.6 (they spill).
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : D == 64 ? 4 : 3)
+    rotary_append_kernel(const RotaryAppendParams p) {
+  constexpr int kThreads = kAppendWarps * 32, kPairs = D / 2;
   dev::grid_launch_dependents();
   dev::grid_dependency_wait();
-  __shared__ __align__(16) float2 angles[kBlockSize][D / 2];
+  __shared__ UnitAngles<D> angles;
   __shared__ int4 s_seq;
   __shared__ int s_hits;
-  const int unit = blockIdx.x;
+  const int unit = blockIdx.x, lane = threadIdx.x & 31;
+  // this thread's pair of every row it computes the angle of
+  const int pair = threadIdx.x % kPairs;
+  const int64_t freq = pair < p.rot.dim / 2 ? p.rot.freqs[pair] : 0;
   if (threadIdx.x == 0) s_hits = 0;
   __syncthreads();
-  for (int b = threadIdx.x; b < p.a.num_seqs; b += kAppendWarps * 32) {
+  for (int b = threadIdx.x; b < p.a.num_seqs; b += kThreads) {
     const int q0 = p.a.query_start[b], q1 = p.a.query_start[b + 1], ctx = p.a.context_lens[b];
     if (owns(p.a, unit, b, q0, q1, ctx)) {
       s_seq = make_int4(b, q0, q1, ctx);
@@ -342,20 +412,32 @@ __global__ void __launch_bounds__(kAppendWarps * 32) rotary_append_kernel(const 
   }
   __syncthreads();
   const int hits = s_hits;
-  const int job = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
+  const int jobs = 2 * p.a.num_kv_heads + p.num_q_heads, step = gridDim.y * kAppendWarps;
   auto take = [&](const int4 seq) {
     const int begin = seq.w - (seq.z - seq.y);
     const int blk = begin / kBlockSize + (unit - (seq.y / kBlockSize + 2 * seq.x));
-    const int lo = max(begin - blk * kBlockSize, 0), hi = min(seq.w - blk * kBlockSize, kBlockSize);
-    const int pairs = p.rot.dim / 2;
-    for (int i = threadIdx.x; i < (hi - lo) * pairs; i += kAppendWarps * 32) {
-      const int r = lo + i / pairs, e = i % pairs;
-      const int place = blk * kBlockSize + r;
-      const int position = p.positions ? p.positions[int64_t(seq.y) + place - begin] : place;
-      angles[r][e] = rot::cos_sin(position, p.rot.freqs[e], p.rot.magnitude);
+    Unit n;
+    n.lo = max(begin - blk * kBlockSize, 0);
+    n.hi = min(seq.w - blk * kBlockSize, kBlockSize);
+    n.first = int64_t(seq.y) + blk * kBlockSize - begin;
+    n.phys = p.a.block_tables[size_t(seq.x) * p.a.max_blocks + blk];
+    if (n.phys < 0 || n.phys >= p.a.num_blocks) {
+      if (threadIdx.x == 0 && blockIdx.y == 0) dev::flag_status(p.a.status, kStatusBounds);
+      n.phys = -1;
+    }
+    int job = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
+    UnitRows<T, D> rows;
+    if (job < jobs) rows.load(p, n, job, lane);
+    for (int r = n.lo + threadIdx.x / kPairs; r < n.hi; r += kThreads / kPairs) {
+      const int position = p.positions ? p.positions[n.first + r] : blk * kBlockSize + r;
+      angles.put(r, pair, rot::cos_sin(position, freq, p.rot.magnitude));
     }
     __syncthreads();
-    if (job < 2 * p.a.num_kv_heads + p.num_q_heads) rotary_block<T, D>(p, seq, unit, job, angles, threadIdx.x & 31);
+    while (job < jobs) {
+      store_unit<T, D, INTER>(p, n, lane, rows, angles);
+      job += step;
+      if (job < jobs) rows.load(p, n, job, lane);
+    }
   };
   if (hits == 1) {
     take(s_seq);
@@ -366,6 +448,152 @@ __global__ void __launch_bounds__(kAppendWarps * 32) rotary_append_kernel(const 
       if (!owns(p.a, unit, b, q0, q1, ctx)) continue;
       take(make_int4(b, q0, q1, ctx));
       __syncthreads();
+    }
+  }
+}
+
+// The same where sequences have a token or two (a decode step): a unit is (token,
+// block the call writes to), unit query_start[b] + i the i-th block of sequence
+// b; a CTA takes a unit, a warp 32 / NJ heads of Q, K or V and its rows in turn,
+// an item a lane.  A chain of latencies: the sequence, its row, table entry and
+// position, the block's scale.  128 tokens of 48 heads: 2.6 us, 4.7 by blocks of
+// 16 rows.  (With the registers of two CTAs an SM 3.3, though 512 tokens then
+// take 6.6 and not 8.8.)
+constexpr int kFewWarps = 16;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kFewWarps * 32) rotary_append_few_kernel(const RotaryAppendParams p) {
+  constexpr int NJ = D / 16, kHeads = 32 / NJ;
+  dev::grid_launch_dependents();
+  __shared__ int4 s_seq;
+  __shared__ int s_hits;
+  const int unit = blockIdx.x, lane = threadIdx.x & 31, j = lane % NJ;
+  if (threadIdx.x == 0) s_hits = 0;
+  __syncthreads();
+  dev::grid_dependency_wait();
+  int64_t freqs[rot::WarpAngles<D>::kPer];
+  rot::WarpAngles<D>::load_freqs(p.rot, lane, freqs);
+  auto mine = [&](int b, int4& seq) {
+    const int q0 = p.a.query_start[b], q1 = p.a.query_start[b + 1], ctx = p.a.context_lens[b];
+    seq = make_int4(b, q0, q1, ctx);
+    const bool bad = invalid(p.a, q0, q1, ctx);
+    if (bad && unit == 0 && blockIdx.y == 0) dev::flag_status(p.a.status, kStatusBounds);
+    if (bad || q1 == q0 || unit < q0) return false;
+    return unit - q0 <= (ctx - 1) / kBlockSize - (ctx - (q1 - q0)) / kBlockSize;
+  };
+  for (int b = threadIdx.x; b < p.a.num_seqs; b += blockDim.x) {
+    int4 seq;
+    if (mine(b, seq)) {
+      s_seq = seq;
+      atomicAdd(&s_hits, 1);
+    }
+  }
+  __syncthreads();
+  // Q, K, V by groups of heads
+  const int groups_q = (p.num_q_heads + kHeads - 1) / kHeads, groups_k = (p.a.num_kv_heads + kHeads - 1) / kHeads;
+  int group = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (group >= groups_q + 2 * groups_k) return;
+  const int kv = group < groups_q ? 2 : group < groups_q + groups_k ? 0 : 1;
+  group -= kv == 2 ? 0 : kv == 0 ? groups_q : groups_q + groups_k;
+  const int head = group * kHeads + lane / NJ;
+  const bool live = head < (kv == 2 ? p.num_q_heads : p.a.num_kv_heads);
+  const int2 at = kv != 1 ? rot::item_columns(p.rot, j) : make_int2(16 * j, 16 * j + 8);
+  const T* src = static_cast<const T*>(kv == 2 ? p.q : kv ? p.a.src[1] : p.a.src[0]) + int64_t(head) * D;
+  auto take = [&](const int4 seq) {
+    const int begin = seq.w - (seq.z - seq.y);
+    const int blk = begin / kBlockSize + unit - seq.y;
+    const int lo = max(begin - blk * kBlockSize, 0), hi = min(seq.w - blk * kBlockSize, kBlockSize);
+    const int64_t first = int64_t(seq.y) + blk * kBlockSize - begin;
+    rot::Chunk<T> u, w;
+    float x[16];
+    auto load = [&](int r) {
+      if (live) {
+        u.load(src + (first + r) * p.stride[kv] + at.x);
+        w.load(src + (first + r) * p.stride[kv] + at.y);
+      }
+    };
+    auto values = [&](int r) {
+      if (kv != 1) {
+        const int position = p.positions ? p.positions[first + r] : blk * kBlockSize + r;
+        rot::WarpAngles<D> angles;
+        float c[8], s[8];
+        angles.set(freqs, position, p.rot.magnitude);
+        angles.gather(j, c, s);
+        u.to_float(x);
+        w.to_float(x + 8);
+        if (16 * j < p.rot.dim) rot::turn_item(p.rot.interleaved, x, c, s);
+      } else {
+        u.to_float(x);
+        w.to_float(x + 8);
+      }
+    };
+    load(lo);
+    int phys = 0;
+    float old = 0.f;
+    size_t tile = 0;
+    if (kv != 2) {
+      phys = p.a.block_tables[size_t(seq.x) * p.a.max_blocks + blk];
+      if (phys < 0 || phys >= p.a.num_blocks) {
+        if (lane == 0) dev::flag_status(p.a.status, kStatusBounds);
+        return;
+      }
+      tile = size_t(phys) * p.a.num_kv_heads + head;
+      if (lo > 0 && live) old = (kv ? p.a.scale[1] : p.a.scale[0])[tile];
+    }
+    float m = 0.f;
+    for (int r = lo; r < hi; ++r) {
+      if (r > lo) load(r);
+      values(r);
+      if (kv != 2) {
+        m = fmaxf(m, largest_of(x));
+      } else if (live) {
+        T* to = static_cast<T*>(p.q_out) + (first + r) * p.q_out_stride + int64_t(head) * D;
+        u.from_float(x);
+        w.from_float(x + 8);
+        u.store(to + at.x);
+        w.store(to + at.y);
+      }
+    }
+    if (kv == 2) return;
+#pragma unroll
+    for (int o = NJ / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float want = __uint_as_float(pow2_bits(scale_exponent(__float_as_uint(m))));
+    const float scale = lo > 0 ? fmaxf(old, want) : want;
+    const float inv = 1.f / scale;
+    uint8_t* codes = (kv ? p.a.cache[1] : p.a.cache[0]) + tile * kBlockSize * D;
+    const bool grows = live && lo > 0 && scale > old;
+    if (grows) {
+      const float factor = old / scale;
+#pragma unroll 4
+      for (int r = 0; r < lo; ++r) {
+        uint2* a = reinterpret_cast<uint2*>(codes + r * D + at.x);
+        uint2* b = reinterpret_cast<uint2*>(codes + r * D + at.y);
+        *a = rescale8(*a, factor);
+        *b = rescale8(*b, factor);
+      }
+    }
+    for (int r = lo; r < hi; ++r) {
+      if (hi - lo > 1) {
+        load(r);
+        values(r);
+      }
+      uint32_t c[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = encode2(x[2 * e] * inv, x[2 * e + 1] * inv);
+      if (!live) continue;
+      *reinterpret_cast<uint2*>(codes + r * D + at.x) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      *reinterpret_cast<uint2*>(codes + r * D + at.y) = make_uint2(c[4] | c[5] << 16, c[6] | c[7] << 16);
+    }
+    if (live && j == 0 && (lo == 0 || grows)) (kv ? p.a.scale[1] : p.a.scale[0])[tile] = scale;
+  };
+  if (s_hits == 1) {
+    take(s_seq);
+  } else if (s_hits > 1) {
+    // a unit of several sequences: each one's in turn
+    for (int b = 0; b < p.a.num_seqs; ++b) {
+      int4 seq;
+      if (mine(b, seq)) take(seq);
+      __syncwarp();
     }
   }
 }
@@ -613,23 +841,50 @@ PA_API int pa_rotary_kv_append_q8(const void* q, const void* k, const void* v,
   p.positions = positions;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(num_tokens / kBlockSize + 2 * num_seqs),
-                     unsigned((2 * num_kv_heads + num_q_heads + kAppendWarps - 1) / kAppendWarps));
-  cfg.blockDim = dim3(kAppendWarps * 32);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e;
   const bool wide = head_dim == 128;
-  if (dtype == PA_F32)
-    e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<float, 128>, p)
-             : cudaLaunchKernelEx(&cfg, rotary_append_kernel<float, 64>, p);
-  else if (dtype == PA_F16)
-    e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<__half, 128>, p)
-             : cudaLaunchKernelEx(&cfg, rotary_append_kernel<__half, 64>, p);
-  else
-    e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<__nv_bfloat16, 128>, p)
-             : cudaLaunchKernelEx(&cfg, rotary_append_kernel<__nv_bfloat16, 64>, p);
+  if (num_tokens <= 2 * num_seqs) {
+    const int per = 32 / (head_dim / 16);
+    const int groups = (num_q_heads + per - 1) / per + 2 * ((num_kv_heads + per - 1) / per);
+    const int gy = (groups + kFewWarps - 1) / kFewWarps;
+    cfg.gridDim = dim3(unsigned(num_tokens), unsigned(gy));
+    cfg.blockDim = dim3(unsigned((groups + gy - 1) / gy * 32));
+    if (dtype == PA_F32)
+      e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_few_kernel<float, 128>, p)
+               : cudaLaunchKernelEx(&cfg, rotary_append_few_kernel<float, 64>, p);
+    else if (dtype == PA_F16)
+      e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_few_kernel<__half, 128>, p)
+               : cudaLaunchKernelEx(&cfg, rotary_append_few_kernel<__half, 64>, p);
+    else
+      e = wide ? cudaLaunchKernelEx(&cfg, rotary_append_few_kernel<__nv_bfloat16, 128>, p)
+               : cudaLaunchKernelEx(&cfg, rotary_append_few_kernel<__nv_bfloat16, 64>, p);
+  } else {
+    // Three heads a warp pay for the CTA's angles and its sequence's search
+    // (10.6 K tokens of 48 heads: 43.7 us with six, 39.3 with three, 42.5 with
+    // one), as long as there are CTAs for the GPU (1 K: 13.9, 9.8, 6.2).
+    const int64_t units = int64_t(num_tokens) / kBlockSize + 2 * num_seqs;
+    const int rounds = (2 * num_kv_heads + num_q_heads + kAppendWarps - 1) / kAppendWarps;
+    const int64_t fill = (1024 + units - 1) / units;
+    int gy = (rounds + 2) / 3;
+    if (gy < fill) gy = int(fill < rounds ? fill : rounds);
+    cfg.gridDim = dim3(unsigned(units), unsigned(gy));
+    cfg.blockDim = dim3(kAppendWarps * 32);
+    auto go = [&](auto inter) {
+      constexpr bool I = decltype(inter)::value;
+      if (dtype == PA_F32)
+        return wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<float, 128, I>, p)
+                    : cudaLaunchKernelEx(&cfg, rotary_append_kernel<float, 64, I>, p);
+      if (dtype == PA_F16)
+        return wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<__half, 128, I>, p)
+                    : cudaLaunchKernelEx(&cfg, rotary_append_kernel<__half, 64, I>, p);
+      return wide ? cudaLaunchKernelEx(&cfg, rotary_append_kernel<__nv_bfloat16, 128, I>, p)
+                  : cudaLaunchKernelEx(&cfg, rotary_append_kernel<__nv_bfloat16, 64, I>, p);
+    };
+    e = interleaved ? go(std::true_type()) : go(std::false_type());
+  }
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
   return PA_OK;
 }

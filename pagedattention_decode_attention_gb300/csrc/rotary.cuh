@@ -67,6 +67,36 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) 
   a = x;
 }
 
+// Two products, or two products added to, in one instruction each (sm_100 on).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// Two neighbouring pairs of a half layout: turn_pair of each, bit for bit.
+__device__ __forceinline__ void turn_two(float* a, float* b, const float* c, const float* s) {
+  const float2 x = make_float2(a[0], a[1]), y = make_float2(b[0], b[1]);
+  const float2 cc = make_float2(c[0], c[1]), ss = make_float2(s[0], s[1]);
+  const float2 u = fma2(x, cc, mul2(y, make_float2(-s[0], -s[1])));
+  const float2 v = fma2(y, cc, mul2(x, ss));
+  a[0] = u.x;
+  a[1] = u.y;
+  b[0] = v.x;
+  b[1] = v.y;
+}
+
 // A warp's angles.  With NJ = D / 16 items a row, lane l keeps the 2 or 1 pairs
 // 8 j + q * kPer .. of item j = l % NJ, q = l / NJ (two cosines a lane at
 // head_dim 128, each computed once in the warp); gather(j) collects an item's 8.
@@ -117,7 +147,7 @@ __device__ __forceinline__ void turn_item(bool interleaved, float (&x)[16], cons
     for (int i = 0; i < 8; ++i) turn_pair(x[2 * i], x[2 * i + 1], c[i], s[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn_pair(x[i], x[8 + i], c[i], s[i]);
+    for (int i = 0; i < 8; i += 2) turn_two(x + i, x + 8 + i, c + i, s + i);
   }
 }
 

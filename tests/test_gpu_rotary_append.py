@@ -131,6 +131,69 @@ def test_append_q8_is_rotary_then_append(gpu, dtype, head_dim, heads, given):
             assert same_bits(codes[i], want_codes[i]) and same_bits(scales[i], want_scales[i])
 
 
+# a decode step; a chunk or two among sequences that have nothing new
+FEW = {"step": ([1, 16, 17, 100, 33, 5000, 48, 31, 2, 15], [1] * 10),
+       "chunks": ([40, 16, 17, 7, 33, 18, 48, 31, 2, 15, 12, 11, 99, 20, 10], [24, 0, 0, 1, 0, 2, 0, 0, 0, 0, 0, 0, 0, 2, 0]),
+       "empty": ([5, 0, 9], [0, 0, 1])}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("heads", [(32, 8), (7, 1), (70, 70)], ids=str)
+@pytest.mark.parametrize("shape", sorted(FEW))
+def test_append_q8_of_few_tokens(gpu, dtype, head_dim, heads, shape):
+    hq, hkv = heads
+    lens, new = FEW[shape]
+    rot, _ = rotary_of(pa, head_dim, gpu, head_dim // 2, hq == 7, 0.9)
+    qs, tables, nb, codes, scales = q8_case(gpu, hkv, head_dim, 5 + hq, lens, new)
+    total = int(qs[-1])
+    assert total <= 2 * len(lens)
+    bt, cl, st = to_dev(gpu, tables, lens, qs)
+    pos = torch.from_numpy(places(lens, new)).to(gpu)
+    for size in (0.1, 1.0, 30.0):
+        q, k, v = projection(total + 2, hq, hkv, head_dim, dtype, 11, gpu, pad=8)
+        k *= size
+        v *= size
+        want = [t.clone() for t in (*codes, *scales)]
+        wide, _ = pa.rotary(k[:total].float(), None, pos, rot)
+        pa.kv_append_q8(wide, v[:total].float().contiguous(), *want, bt, cl, st)
+        qo = torch.full((total + 2, hq, head_dim), 7.0, dtype=q.dtype, device=gpu)
+        pa.rotary_kv_append_q8(q, k, v, None, rot, *codes, *scales, bt, cl, st, q_out=qo)
+        pa.check_status()
+        assert same_bits(qo[:total], pa.rotary(q[:total], None, pos, rot)[0]) and (qo[total:] == 7).all()
+        for a, b in zip((*codes, *scales), want):
+            assert same_bits(a, b)
+
+
+def test_append_q8_of_few_tokens_reports(gpu):
+    """A bad block, a sequence that runs backwards, one behind it among an
+    earlier one's rows, one longer than its table."""
+    rot, _ = rotary_of(pa, 64, gpu)
+    gen = np.random.default_rng(1)
+    lens = [20, 10, 18, 9, 200, 3, 3]
+    starts = np.array([0, 4, 1, 6, 7, 8, 8, 8], dtype=np.int32)
+    tables, nb = window_tables(np.minimum(lens, 32), np.minimum(lens, 32), 0, 0, gen)
+    _, _, codes, scales = cache8(nb, 2, 64, 3, gpu)
+    tables[3, 0] = 1 << 20
+    q, k, v = projection(8, 4, 2, 64, "bf16", 3, gpu)
+    pos = torch.from_numpy(gen.integers(0, 999, 8).astype(np.int32)).to(gpu)
+    bt, cl, st = to_dev(gpu, tables, lens, starts)
+    want = [t.clone() for t in (*codes, *scales)]
+    wide, _ = pa.rotary(k.float(), None, pos, rot)
+    pa.kv_append_q8(wide, v.float().contiguous(), *want, bt, cl, st)
+    qo = torch.full((8, 4, 64), 7.0, dtype=q.dtype, device=gpu)
+    with pytest.raises(pa.PagedAttnError):
+        pa.check_status()
+    pa.rotary_kv_append_q8(q, k, v, pos, rot, *codes, *scales, bt, cl, st, q_out=qo)
+    with pytest.raises(pa.PagedAttnError) as e:
+        pa.check_status()
+    assert e.value.status == 5
+    for a, b in zip((*codes, *scales), want):
+        assert same_bits(a, b)
+    right = pa.rotary(q, None, pos, rot)[0]
+    assert same_bits(qo[:7], right[:7]) and (qo[7:] == 7).all()
+
+
 def test_append_q8_keys_alone_and_prepared(gpu):
     rot, _ = rotary_of(pa, 128, gpu)
     qs, tables, nb, codes, scales = q8_case(gpu, 2, 128, 5)
