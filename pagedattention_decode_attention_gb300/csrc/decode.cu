@@ -62,6 +62,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -993,9 +994,14 @@ __device__ __noinline__ void store_rotated(const Params& p, int b, long long slo
 // ROT: the query rows and the new K rows are rotated (rotary.cuh) in the
 // warp's staging buffer, between their copy and the fragments.  Each lane
 // computes two cosines an item and holds the frequencies; the rotated query is
-// not rounded to T: what the rounding leaves over goes through a second
-// product (bf16 outputs 0.0022 from 64-bit arithmetic, 0.0031 without).
-template <typename T, int D, int W, int NT, bool ROT>
+// not rounded to T: what the rounding leaves over (its rest) enters the product
+// too (bf16 outputs 0.0022 from 64-bit arithmetic, 0.0031 without).  A product
+// has 8 query columns: with at most 4 heads in a group the rests take the other
+// 4 and are added by a shuffle (kRotFolded), else they take a second product
+// (kRotTwice; the 7B-shaped batch: 77.9 us so).
+constexpr int kRotFolded = 1, kRotTwice = 2;
+
+template <typename T, int D, int W, int NT, int ROT>
 __global__ void __launch_bounds__(W * 32)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const Params p) {
@@ -1008,10 +1014,11 @@ __global__ void __launch_bounds__(W * 32)
                 "a team warp's results fit the first two stages of its ring");
   constexpr int HALVES = D / 64;  // 128-byte TMA boxes per tile row
   constexpr int NJ = D / 16;      // 16-column items of a row's rotation
-  static_assert(!ROT || NT == 1, "rotation is built for one sequence's rows");
+  static_assert(ROT == 0 || NT == 1, "rotation is built for one sequence's rows");
   // f16 weights of the rotating kernel are 2^(x - max + 7): without the lift a
   // dominant token leaves the small ones under f16's precision
-  constexpr float kLift = ROT && std::is_same<T, __half>::value ? 7.f : 0.f;
+  constexpr bool fold = ROT == kRotFolded;
+  constexpr float kLift = ROT != 0 && std::is_same<T, __half>::value ? 7.f : 0.f;
   // The next item is claimed when this many blocks of the current one are
   // still to be issued: its claim takes one pipeline step per block (counter,
   // unit, table entries, query copy), so it is ready when the ring wants it.
@@ -1064,7 +1071,8 @@ __global__ void __launch_bounds__(W * 32)
   // The next kernel of the stream may start launching; it waits for this
   // one's completion before it touches memory.
   dev::grid_launch_dependents();
-  int64_t freqs[ROT ? D / 64 : 1];
+  int64_t freqs[ROT != 0 ? D / 64 : 1];
+  rot::WarpAngles<D> angles;  // of the item whose query rows were last requested
   // This warp's first item, dealt statically.  W consecutive items (the
   // heads of one unit, reading neighbouring tiles) per CTA measured best
   // when every warp gets one (MHA 7B decode 0.868 of the measured copy
@@ -1140,7 +1148,7 @@ __global__ void __launch_bounds__(W * 32)
     }
   }
   dev::grid_dependency_wait();  // the kernel before this one has completed
-  if constexpr (ROT) rot::WarpAngles<D>::load_freqs(p.rot, lane, freqs);
+  if constexpr (ROT != 0) rot::WarpAngles<D>::load_freqs(p.rot, lane, freqs);
   TIME_MARK(0, dev::global_timer_ns());
 
   const unsigned long long tmo = p.timeout_ns;
@@ -1195,7 +1203,7 @@ __global__ void __launch_bounds__(W * 32)
         for (int i = 0; i < Hq * D * 2 / 16; ++i) row[i] = make_uint4(0, 0, 0, 0);
         const long long slot = fused ? p.slot_mapping[b] : -1;
         if (slot >= num_slots) dev::flag_status(p.status, kStatusBounds);
-        if (ROT && slot >= 0 && slot < num_slots) {
+        if (ROT != 0 && slot >= 0 && slot < num_slots) {
           store_rotated<T, D>(p, b, slot);
         } else if (slot >= 0 && slot < num_slots) {
           for (int h = 0; h < Hkv; ++h) {
@@ -1299,7 +1307,7 @@ __global__ void __launch_bounds__(W * 32)
       }
       nxt.rows = nxt.m * G;
       nxt.nsplit = __ldg(&p.ws.nsplits[nxt.b]);
-      if constexpr (ROT) nxt.pos = p.positions ? __ldg(&p.positions[nxt.b]) : nxt.ctx - 1;
+      if constexpr (ROT != 0) nxt.pos = p.positions ? __ldg(&p.positions[nxt.b]) : nxt.ctx - 1;
       // only an item of one sequence carries its new token
       cslot = fused && (cu.z & 0xff00) == 0 ? __ldg(&p.slot_mapping[nxt.b]) : -1;
       nxt.phys = lane < nxt.nblk
@@ -1402,7 +1410,7 @@ __global__ void __launch_bounds__(W * 32)
       __syncwarp();
       // lane r copies query row r (member r / G, head r % G of the group)
       // into row r of the buffer
-      if constexpr (ROT) {
+      if constexpr (ROT != 0) {
         if (lane < G)
           dev::bulk_load(qbuf + lane * S::kQRow,
                          static_cast<const T*>(p.q) + nxt.b * p.q_stride + (nxt.g * G + lane) * D,
@@ -1428,6 +1436,8 @@ __global__ void __launch_bounds__(W * 32)
                          my_q);
         }
       }
+      // (the angles are computed while the rows are on their way)
+      if constexpr (ROT != 0) angles.set(freqs, nxt.pos, p.rot.magnitude);
       ++q_issued;
       cstage = 4;
     }
@@ -1506,7 +1516,7 @@ __global__ void __launch_bounds__(W * 32)
     // B fragments of Q^T (k = head_dim, n = query head of the group)
     bool arrived = mbar_wait_bounded(my_q, q_taken & 1, tmo, p.status);
     // (the rotation's shuffles need every lane: a warp that gives up does as one)
-    if constexpr (ROT) arrived = __all_sync(0xffffffffu, arrived);
+    if constexpr (ROT != 0) arrived = __all_sync(0xffffffffu, arrived);
     if (!arrived) {
       drain();
       return;
@@ -1525,20 +1535,20 @@ __global__ void __launch_bounds__(W * 32)
         const uint16_t* qrow = qbuf + hq * S::kQRow + n0;
 #pragma unroll
         for (int kk = 0; kk < KT; ++kk) {
-          f0[t][kk] = hq < rows ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk) : 0u;
-          f1[t][kk] = hq < rows ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 8) : 0u;
+          const bool held = hq < rows || (fold && hq >= 4 && hq - 4 < rows);
+          f0[t][kk] = held ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk) : 0u;
+          f1[t][kk] = held ? *reinterpret_cast<const uint32_t*>(qrow + 16 * kk + 8) : 0u;
         }
       }
     };
-    uint32_t ql0[ROT ? KT : 1], ql1[ROT ? KT : 1];  // what q's rounding leaves over
-    if constexpr (ROT) {
+    uint32_t ql0[ROT == kRotTwice ? KT : 1], ql1[ROT == kRotTwice ? KT : 1];  // not folded: the rests' fragments
+    if constexpr (ROT != 0) {
       // a lane rotates item lane % NJ of rows lane / NJ, + 32 / NJ, ..., and
       // the first lanes the new K row's; the rows are replaced by their
-      // rounded values, then, once those are fragments, by what is left over
+      // rounded values.  The rests go to rows 4 .. 7 (folded), or to the rows
+      // themselves once the rounded values are fragments
       constexpr int kRows = 32 / NJ, kTurns = (8 + kRows - 1) / kRows;
       const int j = lane % NJ;
-      rot::WarpAngles<D> angles;
-      angles.set(freqs, cur.pos, p.rot.magnitude);
       float c[8], sn[8];
       angles.gather(j, c, sn);
       const int2 at = rot::item_columns(p.rot, j);
@@ -1568,31 +1578,36 @@ __global__ void __launch_bounds__(W * 32)
           rest[1].from_float(y + 8);
         }
       };
+      auto put_rest = [&](int i, uint16_t* row) {
+        left[i][0].store(reinterpret_cast<T*>(row + at.x));
+        left[i][1].store(reinterpret_cast<T*>(row + at.y));
+      };
 #pragma unroll
       for (int i = 0; i < kTurns; ++i) {
+        if (i * kRows >= rows) break;
         left[i][0].v[0] = left[i][1].v[0] = make_uint4(0, 0, 0, 0);
         const int r = i * kRows + lane / NJ;
         if (r < rows && turns) turn_row(qbuf + r * S::kQRow, left[i]);
+        if (fold && r < rows) put_rest(i, qbuf + (r + 4) * S::kQRow);
       }
       if (cur.slot >= 0 && lane < NJ && turns) turn_row(qbuf + 8 * S::kQRow, nullptr);
       __syncwarp();
       fragments(qb0, qb1);
-      __syncwarp();
+      if constexpr (!fold) {
+        __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kTurns; ++i) {
-        const int r = i * kRows + lane / NJ;
-        if (r < rows) {
-          left[i][0].store(reinterpret_cast<T*>(qbuf + r * S::kQRow + at.x));
-          left[i][1].store(reinterpret_cast<T*>(qbuf + r * S::kQRow + at.y));
+        for (int i = 0; i < kTurns; ++i) {
+          const int r = i * kRows + lane / NJ;
+          if (r < rows) put_rest(i, qbuf + r * S::kQRow);
         }
-      }
-      __syncwarp();
-      uint32_t f0[NT][KT], f1[NT][KT];
-      fragments(f0, f1);
+        __syncwarp();
+        uint32_t f0[NT][KT], f1[NT][KT];
+        fragments(f0, f1);
 #pragma unroll
-      for (int kk = 0; kk < KT; ++kk) {
-        ql0[kk] = f0[0][kk];
-        ql1[kk] = f1[0][kk];
+        for (int kk = 0; kk < KT; ++kk) {
+          ql0[kk] = f0[0][kk];
+          ql1[kk] = f1[0][kk];
+        }
       }
     } else {
       fragments(qb0, qb1);
@@ -1637,7 +1652,8 @@ __global__ void __launch_bounds__(W * 32)
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) o[t][mt][0] = o[t][mt][1] = o[t][mt][2] = o[t][mt][3] = 0.f;
-      m0[t] = m1[t] = -INFINITY;
+      // (ROT: finite, so that scores of -inf have no weight from the start)
+      m0[t] = m1[t] = ROT != 0 ? -FLT_MAX : -INFINITY;
       l0[t] = l1[t] = 0.f;
     }
     const float sl2 = p.scale_log2;
@@ -1649,9 +1665,7 @@ __global__ void __launch_bounds__(W * 32)
       const int st = cst;
       if (NT == 1 && j == nblk - 1 && nsplit > 1 && lane == 0)
         seen = dev::ld_relaxed_gpu(&p.ws.arrivals[size_t(b) * Hkv + g]);
-      bool landed = mbar_wait_bounded(&my_full[st], cph, tmo, p.status);
-      if constexpr (ROT) landed = __all_sync(0xffffffffu, landed);
-      if (!landed) {
+      if (!mbar_wait_bounded(&my_full[st], cph, tmo, p.status)) {
         drain();
         return;
       }
@@ -1720,7 +1734,7 @@ __global__ void __launch_bounds__(W * 32)
             else
               M::run(sa[t], a0, a1, a2, a3, qb0[t][kk], qb1[t][kk]);
           }
-          if constexpr (ROT) {
+          if constexpr (ROT == kRotTwice) {
             if (kk & 1)
               M::run(sd, a0, a1, a2, a3, ql0[kk], ql1[kk]);
             else
@@ -1739,10 +1753,14 @@ __global__ void __launch_bounds__(W * 32)
           pb0[t] = pb1[t] = 0u;
           continue;
         }
-        if constexpr (ROT) {
+        if constexpr (ROT != 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)  // (an infinite score has no rest: 0 or a sign's opposite times infinity)
-            if (fabsf(sa[0][e] + sb[0][e]) < INFINITY) sb[0][e] += sc[e] + sd[e];
+          for (int e = 0; e < 4; ++e) {
+            // (an infinite score has no rest: 0 or a sign's opposite times infinity)
+            const float whole = sa[0][e] + sb[0][e];
+            const float rest = fold ? __shfl_xor_sync(0xffffffffu, whole, 2) : sc[e] + sd[e];
+            if (fabsf(whole) < INFINITY) sb[0][e] += rest;
+          }
         }
         // a member's own block counts for that member's rows only
         const bool c0 = bmem < 0 || mc0[t] == bmem, c1 = bmem < 0 || mc1[t] == bmem;
@@ -1757,12 +1775,10 @@ __global__ void __launch_bounds__(W * 32)
           bm1 = fmaxf(bm1, __shfl_xor_sync(0xffffffffu, bm1, o_));
         }
         const float mn0 = fmaxf(m0[t], bm0), mn1 = fmaxf(m1[t], bm1);
-        // (ROT: as long as every score was -inf, nothing has a weight)
-        const float rf0 = ROT && mn0 == -INFINITY ? 0.f : mn0, rf1 = ROT && mn1 == -INFINITY ? 0.f : mn1;
-        const float al0 = dev::fast_exp2(m0[t] - rf0), al1 = dev::fast_exp2(m1[t] - rf1);
+        const float al0 = dev::fast_exp2(m0[t] - mn0), al1 = dev::fast_exp2(m1[t] - mn1);
         m0[t] = mn0;
         m1[t] = mn1;
-        const float lf0 = rf0 - kLift, lf1 = rf1 - kLift;
+        const float lf0 = mn0 - kLift, lf1 = mn1 - kLift;
         const uint32_t p01 = M::pack(dev::fast_exp2(x0 - lf0), dev::fast_exp2(x1 - lf1));
         const uint32_t p23 = M::pack(dev::fast_exp2(x2 - lf0), dev::fast_exp2(x3 - lf1));
         {
@@ -2361,13 +2377,13 @@ struct DeviceState {
   int sms = 0;
   Tuning tuning;
   KernelConfig cfg[2][2];   // [bf16?][head_dim 128?]
-  KernelConfig cfg_rot[2][2];  // the same for the rotating decode (8 warps)
+  KernelConfig cfg_rot[2][2][2];  // [kRotFolded - 1 ..] the same for the rotating decode (8 warps)
   KernelConfig cfg2[2][2];  // the same for two query-row tiles (grouped decode, 8 warps)
 };
 DeviceState g_dev[kMaxDevices];
 
 
-template <typename T, int D, int W, int NT = 1, bool ROT = false>
+template <typename T, int D, int W, int NT = 1, int ROT = 0>
 cudaError_t configure_kernel(KernelConfig* cfg, const Tuning& t, size_t optin, size_t per_sm) {
   // shared memory per CTA when `ctas_per_sm` CTAs share an SM (1 KiB reserved each)
   size_t budget = per_sm / t.ctas_per_sm - 1024;
@@ -2392,14 +2408,16 @@ cudaError_t configure_all(DeviceState& st, size_t optin, size_t per_sm) {
   if (e == cudaSuccess) e = configure_kernel<__half, 128, W>(&st.cfg[0][1], st.tuning, optin, per_sm);
   if (e == cudaSuccess) e = configure_kernel<__half, 64, W>(&st.cfg[0][0], st.tuning, optin, per_sm);
   // the rotating decode and the grouped decode always run 8 math warps per CTA
-  if (e == cudaSuccess)
-    e = configure_kernel<__nv_bfloat16, 128, 8, 1, true>(&st.cfg_rot[1][1], st.tuning, optin, per_sm);
-  if (e == cudaSuccess)
-    e = configure_kernel<__nv_bfloat16, 64, 8, 1, true>(&st.cfg_rot[1][0], st.tuning, optin, per_sm);
-  if (e == cudaSuccess)
-    e = configure_kernel<__half, 128, 8, 1, true>(&st.cfg_rot[0][1], st.tuning, optin, per_sm);
-  if (e == cudaSuccess)
-    e = configure_kernel<__half, 64, 8, 1, true>(&st.cfg_rot[0][0], st.tuning, optin, per_sm);
+  auto rotating = [&](auto rot) {
+    constexpr int R = decltype(rot)::value;
+    KernelConfig(&c)[2][2] = st.cfg_rot[R - 1];
+    if (e == cudaSuccess) e = configure_kernel<__nv_bfloat16, 128, 8, 1, R>(&c[1][1], st.tuning, optin, per_sm);
+    if (e == cudaSuccess) e = configure_kernel<__nv_bfloat16, 64, 8, 1, R>(&c[1][0], st.tuning, optin, per_sm);
+    if (e == cudaSuccess) e = configure_kernel<__half, 128, 8, 1, R>(&c[0][1], st.tuning, optin, per_sm);
+    if (e == cudaSuccess) e = configure_kernel<__half, 64, 8, 1, R>(&c[0][0], st.tuning, optin, per_sm);
+  };
+  rotating(std::integral_constant<int, kRotFolded>());
+  rotating(std::integral_constant<int, kRotTwice>());
   if (e == cudaSuccess)
     e = configure_kernel<__nv_bfloat16, 128, 8, 2>(&st.cfg2[1][1], st.tuning, optin, per_sm);
   if (e == cudaSuccess)
@@ -2428,7 +2446,8 @@ int device_setup(int device) {
     for (int a = 0; a < 2 && st.error == PA_OK; ++a)
       for (int d = 0; d < 2; ++d)
         if (st.cfg[a][d].stages < 1 || st.cfg[a][d].ctas_per_sm < 1 ||
-            st.cfg_rot[a][d].stages < 1 || st.cfg_rot[a][d].ctas_per_sm < 1 ||
+            st.cfg_rot[0][a][d].stages < 1 || st.cfg_rot[0][a][d].ctas_per_sm < 1 ||
+            st.cfg_rot[1][a][d].stages < 1 || st.cfg_rot[1][a][d].ctas_per_sm < 1 ||
             st.cfg2[a][d].stages < 1 || st.cfg2[a][d].ctas_per_sm < 1)
           st.error = PA_ERR_UNSUPPORTED;
   });
@@ -2436,7 +2455,7 @@ int device_setup(int device) {
   return PA_OK;
 }
 
-template <typename T, int D, int W, int NT = 1, bool ROT = false>
+template <typename T, int D, int W, int NT = 1, int ROT = 0>
 int launch_tc(Params prm, const KernelConfig& kc, int sms, cudaStream_t stream) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   alignas(64) CUtensorMap mk, mv;
@@ -2689,12 +2708,17 @@ int run_impl(const void* q, const void* k_cache, const void* v_cache, const int3
   const DeviceState& st = g_dev[device];
   const KernelConfig& kc = st.cfg[dtype == PA_BF16][head_dim == 128];
   if (app.rot.freqs) {
-    const KernelConfig& kr = st.cfg_rot[dtype == PA_BF16][head_dim == 128];
-    if (dtype == PA_BF16)
-      return head_dim == 128 ? launch_tc<__nv_bfloat16, 128, 8, 1, true>(prm, kr, st.sms, stream)
-                             : launch_tc<__nv_bfloat16, 64, 8, 1, true>(prm, kr, st.sms, stream);
-    return head_dim == 128 ? launch_tc<__half, 128, 8, 1, true>(prm, kr, st.sms, stream)
-                           : launch_tc<__half, 64, 8, 1, true>(prm, kr, st.sms, stream);
+    auto go = [&](auto rot) {
+      constexpr int R = decltype(rot)::value;
+      const KernelConfig& kr = st.cfg_rot[R - 1][dtype == PA_BF16][head_dim == 128];
+      if (dtype == PA_BF16)
+        return head_dim == 128 ? launch_tc<__nv_bfloat16, 128, 8, 1, R>(prm, kr, st.sms, stream)
+                               : launch_tc<__nv_bfloat16, 64, 8, 1, R>(prm, kr, st.sms, stream);
+      return head_dim == 128 ? launch_tc<__half, 128, 8, 1, R>(prm, kr, st.sms, stream)
+                             : launch_tc<__half, 64, 8, 1, R>(prm, kr, st.sms, stream);
+    };
+    return prm.group <= 4 ? go(std::integral_constant<int, kRotFolded>())
+                          : go(std::integral_constant<int, kRotTwice>());
   }
   if (st.tuning.warps == 4) {
     if (dtype == PA_BF16)

@@ -704,7 +704,7 @@ __device__ __forceinline__ float append_row(const Params& p, uint8_t* tiles, siz
 // returned): a row of any size keeps every bit down to 2^-38 of its largest
 // element.  f16 queries: x is left with what the rounding left over.
 template <int NJ, bool REST>
-__device__ __forceinline__ int place_q(float (&x)[16], uint16_t* to, const int2 at) {
+__device__ __forceinline__ int place_q(float (&x)[16], uint16_t* to, const int2 at, bool live) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
@@ -726,8 +726,10 @@ __device__ __forceinline__ int place_q(float (&x)[16], uint16_t* to, const int2 
       x[2 * i + 1] = fabsf(f.y) < INFINITY ? x[2 * i + 1] - f.y : 0.f;
     }
   }
-  *reinterpret_cast<uint4*>(to + at.x) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(to + at.y) = make_uint4(w[4], w[5], w[6], w[7]);
+  if (live) {
+    *reinterpret_cast<uint4*>(to + at.x) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(to + at.y) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
   return e;
 }
 
@@ -767,9 +769,12 @@ __device__ __forceinline__ q8::Row8<float> rotate_row(const Params& p, const q8:
 // ROT (with APPEND): the query rows and the new K row are rotated on the way.  A
 // segment's rows are loaded as items (rotary.cuh), rotated in registers, and
 // turned into fragments through the warp's shared memory.  They are rounded to
-// f16, not to T; where T is f16, what that leaves over goes through a second
-// product (outputs 2.8e-4 from 64-bit arithmetic, 3.8e-4 without).
-template <typename T, bool Q8, int D, bool APPEND, bool ROT>
+// f16, not to T; where T is f16, what that leaves over (the rest) enters the
+// product too (outputs 2.8e-4 from 64-bit arithmetic, 3.8e-4 without): in the
+// product's free columns 4 .. 7 and added by a shuffle where a group has at most
+// 4 heads, else by a second product (64 sequences of 32/32 heads, f16: 70.5 us
+// with the second product).
+template <typename T, bool Q8, int D, bool APPEND, bool ROT, bool FOLD>
 __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const Params p) {
@@ -778,6 +783,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
   static_assert(!ROT || (Q8 && APPEND), "rotation is built for the 8-bit append");
   constexpr bool kRest = ROT && std::is_same<T, __half>::value;
   constexpr int NJ = D / 16;  // 16-column items of a row's rotation
+  constexpr bool fold = kRest && FOLD;
   constexpr int ST = S::kStages, kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr bool kTwoParts = S::kTwoParts;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -941,36 +947,46 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
       angles.gather(lane % NJ, c, sn);
       const int2 at = rot::item_columns(p.rot, lane % NJ);
       float x[D / 64][16];
-      int e[D / 64];
+      int e[D / 64] = {};
       __syncwarp();  // (the last segment's rows are read)
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
+        if (i * (32 / NJ) >= G) break;
         rot::Chunk<T> u, w;
         u.v[0] = raw[2 * i];
         w.v[0] = raw[2 * i + 1];
         u.to_float(x[i]);
         w.to_float(x[i] + 8);
         if (16 * (lane % NJ) < p.rot.dim) rot::turn_item(p.rot.interleaved, x[i], c, sn);
-        e[i] = place_q<NJ, kRest>(x[i], rows + (i * (32 / NJ) + lane / NJ) * S::kQRow, at);
+        const int r = i * (32 / NJ) + lane / NJ;
+        e[i] = place_q<NJ, kRest>(x[i], rows + r * S::kQRow, at, r < G);
+        if (fold && r < G) {
+          rot::Chunk<__half> a, z;
+          a.from_float(x[i]);
+          z.from_float(x[i] + 8);
+          a.store(reinterpret_cast<__half*>(rows + (r + 4) * S::kQRow + at.x));
+          z.store(reinterpret_cast<__half*>(rows + (r + 4) * S::kQRow + at.y));
+        }
       }
       __syncwarp();
-      // (rows past the group were loaded as zeros)
+      const int row = fold && g >= 4 ? g - 4 : g;  // the head of this lane's column
       auto fragments = [&](uint4 (&w)[D / 32]) {
-        load_q<__half, Q8, D>(reinterpret_cast<const __half*>(rows + g * S::kQRow), true, t, w);
+        load_q<__half, Q8, D>(reinterpret_cast<const __half*>(rows + g * S::kQRow), row < G, t, w);
       };
       fragments(raw);
       convert_q<__half, Q8, D>(raw, qf);
-      // row g's exponent: item 0 of the row has it
-      qexp = __shfl_sync(0xffffffffu, e[0], (g % (32 / NJ)) * NJ);
+      // its exponent: item 0 of the row has it
+      qexp = __shfl_sync(0xffffffffu, e[0], (row % (32 / NJ)) * NJ);
       if constexpr (D == 128) {
-        const int high = __shfl_sync(0xffffffffu, e[D / 64 - 1], (g % (32 / NJ)) * NJ);
-        if (g >= 32 / NJ) qexp = high;
+        const int high = __shfl_sync(0xffffffffu, e[D / 64 - 1], (row % (32 / NJ)) * NJ);
+        if (row >= 32 / NJ) qexp = high;
       }
-      if constexpr (kRest) {
-        // what the rounding left over, as fragments, each lane's together
+      if constexpr (kRest && !fold) {
+        // the rests as fragments, each lane's together
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
+          if (i * (32 / NJ) >= G) break;
           uint16_t* to = rows + (i * (32 / NJ) + lane / NJ) * S::kQRow;
           rot::Chunk<__half> u, w;
           u.from_float(x[i]);
@@ -1080,7 +1096,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
         for (int k = 0; k < S::kSteps; k += 2) {
           Mm::run(s[i], f[k][0], f[k][1], f[k][2], f[k][3], qf[k][0], qf[k][1]);
           Mm::run(s2[i], f[k + 1][0], f[k + 1][1], f[k + 1][2], f[k + 1][3], qf[k + 1][0], qf[k + 1][1]);
-          if constexpr (kRest) {
+          if constexpr (kRest && !fold) {
             // (convert_q's order: two steps to 16 bytes)
             const uint4 w = reinterpret_cast<const uint4*>(rows)[k / 2 * 32 + lane];
             Mm::run(s[i], f[k][0], f[k][1], f[k][2], f[k][3], w.x, w.y);
@@ -1093,6 +1109,13 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
       float top0 = -INFINITY, top1 = -INFINITY, high0 = -INFINITY, high1 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
+        if constexpr (fold) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[i][e] += s2[i][e];
+            s2[i][e] = __shfl_xor_sync(0xffffffffu, s[i][e], 2);
+          }
+        }
         const float c0 = Q8 ? f0 * bks[i] : f0, c1 = Q8 ? f1 * bks[i] : f1;
         x[i][0] = (s[i][0] + s2[i][0]) * c0;
         x[i][1] = (s[i][1] + s2[i][1]) * c1;
@@ -1491,15 +1514,18 @@ DeviceState g_dev[kMaxDevices];
 template <typename T, bool Q8, int D>
 cudaError_t configure() {
   const int bytes = int(Tiles<T, Q8, D>::kBytes);
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, false, false>,
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, false, false, false>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if constexpr (Q8) {
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                bytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               int(Tiles<T, Q8, D, true>::kBytes));
+      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true, true, false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(Tiles<T, Q8, D, true>::kBytes));
+    if (e == cudaSuccess && std::is_same<T, __half>::value)
+      e = cudaFuncSetAttribute(attend_kernel<T, Q8, D, true, true, std::is_same<T, __half>::value>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(Tiles<T, Q8, D, true>::kBytes));
   }
   return e;
 }
@@ -1590,11 +1616,14 @@ cudaError_t launch_attend(cudaLaunchConfig_t cfg, const CUtensorMap& mk, const C
   if constexpr (Q8) {
     if (p.rot.freqs) {
       cfg.dynamicSmemBytes = Tiles<T, Q8, D, true>::kBytes;
-      return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true, true>, mk, mv, p);
+      if (std::is_same<T, __half>::value && p.group <= 4)
+        return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true, true, std::is_same<T, __half>::value>, mk, mv,
+                                  p);
+      return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true, true, false>, mk, mv, p);
     }
-    if (p.new_rows[0]) return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true, false>, mk, mv, p);
+    if (p.new_rows[0]) return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, true, false, false>, mk, mv, p);
   }
-  return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, false, false>, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, attend_kernel<T, Q8, D, false, false, false>, mk, mv, p);
 }
 
 template <typename T, bool Q8>
