@@ -1571,9 +1571,13 @@ __global__ void __launch_bounds__(W * 32)
         if (rest) {
           u.to_float(y);
           w.to_float(y + 8);
-          // (nothing is left over of an infinity)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = fabsf(y[i]) < INFINITY ? x[i] - y[i] : 0.f;
+          for (int i = 0; i < 16; i += 2) {
+            const float2 z = rot::fma2(make_float2(y[i], y[i + 1]), make_float2(-1.f, -1.f),
+                                       make_float2(x[i], x[i + 1]));
+            y[i] = z.x;
+            y[i + 1] = z.y;
+          }
           rest[0].from_float(y);
           rest[1].from_float(y + 8);
         }

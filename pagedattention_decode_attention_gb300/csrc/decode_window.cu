@@ -424,7 +424,7 @@ struct Tiles {
   static constexpr size_t kFlags = kBars + size_t(kWarps) * kStages * 8;  // int[kWarps + 4]
   // rows 16 bytes apart, so that lanes reading one column of several do not meet in a bank
   static constexpr int kQRow = D + 8;
-  static constexpr int kQBytes = ROT ? kMaxGroup * kQRow * 2 : 0;
+  static constexpr int kQBytes = ROT ? kMaxGroup * kQRow * 2 + int(sizeof(rot::AngleTable<D>)) : 0;
   static constexpr size_t kRows = (kFlags + (kWarps + 4) * 4 + 15) & ~size_t(15);
   static constexpr size_t kBytes = ROT ? kRows + size_t(kWarps) * kQBytes : kFlags + (kWarps + 4) * 4;
   // merge of a sequence's pieces over CTAs, in the ring's place
@@ -705,25 +705,23 @@ __device__ __forceinline__ float append_row(const Params& p, uint8_t* tiles, siz
 // element.  f16 queries: x is left with what the rounding left over.
 template <int NJ, bool REST>
 __device__ __forceinline__ int place_q(float (&x)[16], uint16_t* to, const int2 at, bool live) {
-  uint32_t top = 0;
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
 #pragma unroll
-  for (int o = NJ / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const int e0 = int(top >> 23);  // biased exponent; 0: nothing, 255: not finite
+  for (int o = NJ / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int e0 = int(__float_as_uint(top) >> 23);  // biased exponent; 0: nothing, 255: not finite
   const int e = e0 == 0 || e0 == 255 ? 0 : max(e0 - 127 - 13, -120);
   const float down = __uint_as_float(uint32_t(127 - e) << 23);
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[2 * i] *= down;
-    x[2 * i + 1] *= down;
-    w[i] = dev::Mma<__half>::pack(x[2 * i], x[2 * i + 1]);
+    const float2 y = rot::mul2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(down, down));
+    w[i] = dev::Mma<__half>::pack(y.x, y.y);
     if constexpr (REST) {
-      // (of an infinity nothing is left over)
-      const float2 f = dev::Mma<__half>::unpack(w[i]);
-      x[2 * i] = fabsf(f.x) < INFINITY ? x[2 * i] - f.x : 0.f;
-      x[2 * i + 1] = fabsf(f.y) < INFINITY ? x[2 * i + 1] - f.y : 0.f;
+      const float2 z = rot::fma2(dev::Mma<__half>::unpack(w[i]), make_float2(-1.f, -1.f), y);
+      x[2 * i] = z.x;
+      x[2 * i + 1] = z.y;
     }
   }
   if (live) {
@@ -734,31 +732,41 @@ __device__ __forceinline__ int place_q(float (&x)[16], uint16_t* to, const int2 
 }
 
 // The new K row rotated, 8 columns a lane (lanes 0 - 15; the others hold V's and
-// keep it), in 32 bits.
+// keep it), in 32 bits: a column is y cos + other sin, `other` its pair's other
+// column, its sign turned in the pair's first.
 template <typename T, int D>
 __device__ __forceinline__ q8::Row8<float> rotate_row(const Params& p, const q8::Row8<T>& x,
-                                                      const rot::WarpAngles<D>& angles) {
+                                                      const rot::AngleTable<D>& table) {
   const int lane = threadIdx.x & 31, chunk = lane & 15, half = p.rot.dim / 16;
-  rot::Chunk<T> raw;
+  const bool inter = p.rot.interleaved, second = !inter && chunk >= half;
+  const int j = inter ? chunk / 2 : second ? chunk - half : chunk;
+  const int from = (lane + (chunk < half ? half : -half)) & 31;
+  const uint32_t sign = inter ? 0x00008000u : second ? 0u : 0x80008000u;
+  rot::Chunk<T> raw, other;
   raw.v[0] = x.v;
-  float y[8], c[8], s[8];
-  raw.to_float(y);
-  const bool second = !p.rot.interleaved && chunk >= half;
-  const int j = p.rot.interleaved ? chunk / 2 : second ? chunk - half : chunk;
-  angles.gather(j & (rot::WarpAngles<D>::NJ - 1), c, s);
-  const int from = lane + (chunk < half ? half : -half);
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&x.v);
+  uint32_t* o = reinterpret_cast<uint32_t*>(&other.v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float other = __shfl_sync(0xffffffffu, y[i], from & 31);
-    if (lane >= 16 || p.rot.interleaved || chunk >= 2 * half) continue;
-    float a = second ? other : y[i], b = second ? y[i] : other;
-    rot::turn_pair(a, b, c[i], s[i]);
-    y[i] = second ? b : a;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t far = __shfl_sync(0xffffffffu, w[i], from);
+    o[i] = (inter ? __byte_perm(w[i], 0, 0x1032) : far) ^ sign;
   }
-  if (lane < 16 && p.rot.interleaved && 8 * chunk < p.rot.dim) {
+  float y[8], z[8], c[8], s[8];
+  raw.to_float(y);
+  if (lane < 16 && chunk < 2 * half) {
+    other.to_float(z);
+    table.get(j, c, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      rot::turn_pair(y[2 * i], y[2 * i + 1], chunk & 1 ? c[4 + i] : c[i], chunk & 1 ? s[4 + i] : s[i]);
+    for (int i = 0; i < 4; ++i) {
+      // the angles of columns 2 i, 2 i + 1: their own pairs', or the one they are
+      const float2 far = chunk & 1 ? make_float2(c[4 + i], s[4 + i]) : make_float2(c[i], s[i]);
+      const float2 cc = inter ? make_float2(far.x, far.x) : make_float2(c[2 * i], c[2 * i + 1]);
+      const float2 ss = inter ? make_float2(far.y, far.y) : make_float2(s[2 * i], s[2 * i + 1]);
+      const float2 a = rot::fma2(make_float2(y[2 * i], y[2 * i + 1]), cc,
+                                 rot::mul2(make_float2(z[2 * i], z[2 * i + 1]), ss));
+      y[2 * i] = a.x;
+      y[2 * i + 1] = a.y;
+    }
   }
   q8::Row8<float> out;
   out.v[0] = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
@@ -899,6 +907,8 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
   int position = 0;           // of the segment's new token
   int64_t freqs[ROT ? D / 64 : 1];
   uint16_t* rows = reinterpret_cast<uint16_t*>(smem + S::kRows + size_t(warp) * S::kQBytes);
+  rot::AngleTable<D>* table = reinterpret_cast<rot::AngleTable<D>*>(rows + kMaxGroup * S::kQRow);
+  int turned = -1;            // the sequence whose angles the table holds
   auto fetch_q = [&](int qb, int qh, int length) {
     if constexpr (ROT) {
       const int2 at = rot::item_columns(p.rot, lane % NJ);
@@ -940,15 +950,20 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
     const bool starts = v == 0, ends = v + run == seq.y;
     uint32_t qf[S::kSteps][2];
     int qexp;
-    rot::WarpAngles<D> angles;
     if constexpr (ROT) {
-      angles.set(freqs, position, p.rot.magnitude);
+      __syncwarp();  // (the last segment's rows are read)
+      if (turned != b) {
+        rot::WarpAngles<D> angles;
+        angles.set(freqs, position, p.rot.magnitude);
+        table->put(angles, lane);
+        turned = b;
+        __syncwarp();
+      }
       float c[8], sn[8];
-      angles.gather(lane % NJ, c, sn);
+      table->get(lane % NJ, c, sn);
       const int2 at = rot::item_columns(p.rot, lane % NJ);
       float x[D / 64][16];
       int e[D / 64] = {};
-      __syncwarp();  // (the last segment's rows are read)
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         if (i * (32 / NJ) >= G) break;
@@ -1233,7 +1248,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
       float now;
       if constexpr (ROT)
         now = append_row<float, D>(p, ring + stage * S::kStage, size_t(own), (seq.x - 1) & 15, old,
-                                   rotate_row<T, D>(p, fresh, angles));
+                                   rotate_row<T, D>(p, fresh, *table));
       else
         now = append_row<T, D>(p, ring + stage * S::kStage, size_t(own), (seq.x - 1) & 15, old, fresh);
       const float now_k = __shfl_sync(0xffffffffu, now, 0), now_v = __shfl_sync(0xffffffffu, now, 16);

@@ -132,6 +132,34 @@ struct WarpAngles {
   }
 };
 
+// A warp's angles in shared memory, an item's 8 pairs as 4 pieces of 16 bytes
+// (two cosines, two sines), items side by side.
+template <int D>
+struct AngleTable {
+  float4 cs[4][D / 16];
+  // by all lanes of the warp that holds `a`
+  __device__ __forceinline__ void put(const WarpAngles<D>& a, int lane) {
+    const int j = lane % (D / 16), q = lane / (D / 16);
+    if constexpr (D == 128) {
+      cs[q][j] = make_float4(a.cs[0].x, a.cs[1].x, a.cs[0].y, a.cs[1].y);
+    } else {
+      float* to = reinterpret_cast<float*>(&cs[q >> 1][j]) + (q & 1);
+      to[0] = a.cs[0].x;
+      to[2] = a.cs[0].y;
+    }
+  }
+  __device__ __forceinline__ void get(int j, float (&c)[8], float (&s)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = cs[i][j];
+      c[2 * i] = x.x;
+      c[2 * i + 1] = x.y;
+      s[2 * i] = x.z;
+      s[2 * i + 1] = x.w;
+    }
+  }
+};
+
 // Where an item's two 8-column chunks begin (its first and second half).
 __device__ __forceinline__ int2 item_columns(const Args& r, int j) {
   if (!r.interleaved && 16 * j < r.dim) return make_int2(8 * j, 8 * j + r.dim / 2);
