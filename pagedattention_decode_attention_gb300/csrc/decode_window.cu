@@ -426,7 +426,8 @@ struct Tiles {
   static constexpr int kQRow = D + 8;
   static constexpr int kQBytes = ROT ? kMaxGroup * kQRow * 2 + int(sizeof(rot::AngleTable<D>)) : 0;
   static constexpr size_t kRows = (kFlags + (kWarps + 4) * 4 + 15) & ~size_t(15);
-  static constexpr size_t kBytes = ROT ? kRows + size_t(kWarps) * kQBytes : kFlags + (kWarps + 4) * 4;
+  static constexpr size_t kFreqs = kRows + size_t(kWarps) * kQBytes;  // int64[D / 2]
+  static constexpr size_t kBytes = ROT ? kFreqs + D / 2 * 8 : kFlags + (kWarps + 4) * 4;
   // merge of a sequence's pieces over CTAs, in the ring's place
   static_assert(kRing >= size_t(kMaxCtas) * kMaxGroup * 12, "merge weights");
   static_assert(size_t(kStages) * kStage >= sizeof(Piece<D>), "a warp's last piece");
@@ -673,8 +674,15 @@ __device__ __forceinline__ float append_row(const Params& p, uint8_t* tiles, siz
     return m;
   };
   uint32_t top = largest(false);
-  const uint32_t fine = largest(true);
-  if (top >= q8::Row8<T>::kInf) top = fine;
+  if constexpr (std::is_same<T, float>::value) {
+    if (__any_sync(0xffffffffu, top >= q8::Row8<T>::kInf)) {
+      const uint32_t fine = largest(true);
+      if (top >= q8::Row8<T>::kInf) top = fine;
+    }
+  } else {
+    const uint32_t fine = largest(true);
+    if (top >= q8::Row8<T>::kInf) top = fine;
+  }
   const float want = __uint_as_float(q8::pow2_bits(q8::scale_exponent(q8::Row8<T>::float_bits(top))));
   const float scale = off > 0 ? fmaxf(old, want) : want;
   const bool grows = off > 0 && scale > old;
@@ -904,12 +912,11 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
   // a segment's query rows are loaded a segment ahead; the first one's before
   // the table entries that the copies wait for
   uint4 raw[D / 32];
-  int position = 0;           // of the segment's new token
-  int64_t freqs[ROT ? D / 64 : 1];
   uint16_t* rows = reinterpret_cast<uint16_t*>(smem + S::kRows + size_t(warp) * S::kQBytes);
   rot::AngleTable<D>* table = reinterpret_cast<rot::AngleTable<D>*>(rows + kMaxGroup * S::kQRow);
+  int64_t* freqs = reinterpret_cast<int64_t*>(smem + S::kFreqs);
   int turned = -1;            // the sequence whose angles the table holds
-  auto fetch_q = [&](int qb, int qh, int length) {
+  auto fetch_q = [&](int qb, int qh) {
     if constexpr (ROT) {
       const int2 at = rot::item_columns(p.rot, lane % NJ);
 #pragma unroll
@@ -922,17 +929,25 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
           raw[2 * i + 1] = *reinterpret_cast<const uint4*>(row + at.y);
         }
       }
-      position = p.positions ? p.positions[qb] : length - 1;
     } else {
       load_q<T, Q8, D>(static_cast<const T*>(p.q) + (size_t(qb) * p.num_q_heads + qh * G + g) * D, g < G, t, raw);
     }
   };
+  int64_t first_freqs[ROT ? D / 64 : 1];
   if (count > 0) {
-    fetch_q(start.x, start.y, start_seq.x);
-    if constexpr (ROT) rot::WarpAngles<D>::load_freqs(p.rot, lane, freqs);
+    fetch_q(start.x, start.y);
+    if constexpr (ROT) rot::WarpAngles<D>::load_freqs(p.rot, lane, first_freqs);
     fill();
   }
   for (int i = 0; i < ST && issued < count; ++i) issue();
+  if constexpr (ROT) {
+    // (every warp of the CTA writes the same, and a lane reads what it wrote:
+    // the loop has no registers to spare for them)
+    if (count > 0) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) freqs[rot::WarpAngles<D>::pair_of(lane, i)] = first_freqs[i];
+    }
+  }
 
   // ---- the warp's segments: runs of blocks of one (sequence, KV head)
   int b = start.x, h = start.y, v = start.z;
@@ -954,7 +969,10 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
       __syncwarp();  // (the last segment's rows are read)
       if (turned != b) {
         rot::WarpAngles<D> angles;
-        angles.set(freqs, position, p.rot.magnitude);
+        int64_t f[D / 64];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) f[i] = freqs[rot::WarpAngles<D>::pair_of(lane, i)];
+        angles.set(f, p.positions ? p.positions[b] : seq.x - 1, p.rot.magnitude);
         table->put(angles, lane);
         turned = b;
         __syncwarp();
@@ -1028,7 +1046,7 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
         do nseq = p.seqs[++nb];
         while (nseq.y == 0);
       }
-      fetch_q(nb, nh, nseq.x);
+      fetch_q(nb, nh);
     }
     float f0 = p.scale_log2, f1 = p.scale_log2;
     if constexpr (Q8) {
