@@ -741,8 +741,8 @@ PA_API int pa_rotary(const void* q, const void* k, const int32_t* positions, con
 
 /* ------------------------------------------------------------------------
  * pa_rotary_kv_append -- pa_rotary of q and k, the rotated keys going to their
- * slots of a paged cache with v beside them, in one launch: the codes of
- * pa_rotary followed by pa_kv_append, bit for bit.
+ * slots of a paged cache with v beside them, in one launch: bit for bit
+ * pa_rotary followed by pa_kv_append.
  *
  * A token with a negative slot has its query rotated and stores nothing; a
  * slot >= num_blocks * 16 stores nothing and sets PA_ERR_DEVICE_BOUNDS.  q_out
@@ -785,10 +785,10 @@ PA_API int pa_rotary_kv_append_q8(const void* q, const void* k, const void* v,
  *
  * positions may be NULL: context_lens[b] - 1.  The caches end up as
  * pa_rotary_kv_append leaves them, bit for bit.  The rotated query is not
- * rounded to q's type before its product (f16 and bf16: its first 16 and 22
- * bits are used), so the output is nearer to exact arithmetic than that call
+ * rounded to q's type before its product (its first 22 bits are used for f16,
+ * 16 for bf16), so the output is nearer to exact arithmetic than that call
  * followed by pa_paged_attention_decode_run; a query whose rotated values pass
- * its type's range gives infinities.  PA_F32 runs as two launches, which keep
+ * its type's range gives infinite scores.  PA_F32 runs as two launches, which keep
  * the rotated queries in out.  out overlaps no input.  Everything else as for
  * pa_paged_attention_decode_append_run.
  * ---------------------------------------------------------------------- */

@@ -788,8 +788,12 @@ __device__ __forceinline__ q8::Row8<float> rotate_row(const Params& p, const q8:
 // f16, not to T; where T is f16, what that leaves over (the rest) enters the
 // product too (outputs 2.8e-4 from 64-bit arithmetic, 3.8e-4 without): in the
 // product's free columns 4 .. 7 and added by a shuffle where a group has at most
-// 4 heads, else by a second product (64 sequences of 32/32 heads, f16: 70.5 us
-// with the second product).
+// 4 heads (FOLD), else by a second product (64 sequences of 32/32 heads, f16,
+// so: 60.9 us folded, 70.5 with the second product).
+//
+// What it costs (one launch of many): the first batch above 87.1 us, 84.5 with
+// its rows rotated already; the third 54.0 and 41.8, 2048 segments and as many
+// new tokens, each some 400 instructions more that a warp goes through alone.
 template <typename T, bool Q8, int D, bool APPEND, bool ROT, bool FOLD>
 __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -1284,16 +1288,21 @@ __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
       __syncwarp();
     };
     int left = run;
-    for (; left >= 2 && ok; left -= 2) {
-      if constexpr (APPEND) {
-        if (left == 2 && own >= 0) join(2);
-        if (!ok) break;
+    // (with a second product one block at a time: two leave too few registers,
+    // 8 heads per KV head in f16 58.4 us and 61.3)
+    constexpr bool kPairs = !(kRest && !fold);
+    if constexpr (kPairs) {
+      for (; left >= 2 && ok; left -= 2) {
+        if constexpr (APPEND) {
+          if (left == 2 && own >= 0) join(2);
+          if (!ok) break;
+        }
+        take(std::integral_constant<int, 2>());
       }
-      take(std::integral_constant<int, 2>());
     }
-    if (left && ok) {
+    for (; left && ok; --left) {
       if constexpr (APPEND) {
-        if (own >= 0) join(1);
+        if (left == 1 && own >= 0) join(1);
       }
       if (ok) take(std::integral_constant<int, 1>());
     }

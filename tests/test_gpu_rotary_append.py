@@ -132,7 +132,7 @@ def test_append_q8_is_rotary_then_append(gpu, dtype, head_dim, heads, given):
 
 
 # a decode step; a chunk or two among sequences that have nothing new
-FEW = {"step": ([1, 16, 17, 100, 33, 5000, 48, 31, 2, 15], [1] * 10),
+FEW = {"step": ([1, 16, 17, 100, 33, 700, 48, 31, 2, 15], [1] * 10),
        "chunks": ([40, 16, 17, 7, 33, 18, 48, 31, 2, 15, 12, 11, 99, 20, 10], [24, 0, 0, 1, 0, 2, 0, 0, 0, 0, 0, 0, 0, 2, 0]),
        "empty": ([5, 0, 9], [0, 0, 1])}
 

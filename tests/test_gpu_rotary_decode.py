@@ -208,6 +208,18 @@ def test_scores_of_minus_infinity(gpu):
     assert_within(out, ref, limit(ref, spread, size, 90, "bf16", "bf16", 0.0, where, w, QUERY["bf16"]))
 
 
+@pytest.mark.parametrize("heads", [(1, 1), (7, 1), (8, 2)], ids=str)
+def test_rows_that_repeat(gpu, heads):
+    """A stride of zero: every sequence with the same query, key and value."""
+    lens, tables, kc, vc, q, k, v, slots, rot, w = case16(gpu, [40, 1, 300, 17], *heads, 128, "bf16", 13)
+    one = [t[:1].expand(4, -1, -1) for t in (q, k, v)]
+    kw, vw = kc.clone(), vc.clone()
+    want, _ = step16(gpu, lens, tables, kw, vw, *(t.contiguous() for t in one), slots, rot)
+    got, where = step16(gpu, lens, tables, kc, vc, *one, slots, rot)
+    assert same_bits(got, want) and same_bits(kc, kw)
+    check16(got, where, w, rot, lens, tables, kc, vc, one[0], "bf16")
+
+
 def test_unwritten_slots_may_hold_anything(gpu):
     """NaN and infinities behind the last token, and in the new token's slot
     before it is written."""
