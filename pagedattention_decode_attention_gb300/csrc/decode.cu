@@ -988,6 +988,8 @@ __device__ __noinline__ void store_rotated(const Params& p, int b, long long slo
   }
 }
 
+constexpr int kRotFolded = 1, kRotTwice = 2;
+
 // NT: query-row tiles of 8 per item (1: up to 8 rows, one sequence's query
 // group; 2: up to 16, the rows of the members of a group sharing the item's
 // blocks).
@@ -995,12 +997,11 @@ __device__ __noinline__ void store_rotated(const Params& p, int b, long long slo
 // warp's staging buffer, between their copy and the fragments.  Each lane
 // computes two cosines an item and holds the frequencies; the rotated query is
 // not rounded to T: what the rounding leaves over (its rest) enters the product
-// too (bf16 outputs 0.0022 from 64-bit arithmetic, 0.0031 without).  A product
+// too (24 sequences, bf16: 0.0019 from 64-bit arithmetic, 0.0031 without, one
+// rounding of the exact output 0.0017).  A product
 // has 8 query columns: with at most 4 heads in a group the rests take the other
 // 4 and are added by a shuffle (kRotFolded), else they take a second product
 // (kRotTwice; the 7B-shaped batch: 77.9 us so).
-constexpr int kRotFolded = 1, kRotTwice = 2;
-
 template <typename T, int D, int W, int NT, int ROT>
 __global__ void __launch_bounds__(W * 32)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
@@ -1015,9 +1016,9 @@ __global__ void __launch_bounds__(W * 32)
   constexpr int HALVES = D / 64;  // 128-byte TMA boxes per tile row
   constexpr int NJ = D / 16;      // 16-column items of a row's rotation
   static_assert(ROT == 0 || NT == 1, "rotation is built for one sequence's rows");
+  constexpr bool fold = ROT == kRotFolded;
   // f16 weights of the rotating kernel are 2^(x - max + 7): without the lift a
   // dominant token leaves the small ones under f16's precision
-  constexpr bool fold = ROT == kRotFolded;
   constexpr float kLift = ROT != 0 && std::is_same<T, __half>::value ? 7.f : 0.f;
   // The next item is claimed when this many blocks of the current one are
   // still to be issued: its claim takes one pipeline step per block (counter,

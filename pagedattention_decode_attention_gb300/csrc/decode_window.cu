@@ -786,7 +786,7 @@ __device__ __forceinline__ q8::Row8<float> rotate_row(const Params& p, const q8:
 // segment's rows are loaded as items (rotary.cuh), rotated in registers, and
 // turned into fragments through the warp's shared memory.  They are rounded to
 // f16, not to T; where T is f16, what that leaves over (the rest) enters the
-// product too (outputs 2.8e-4 from 64-bit arithmetic, 3.8e-4 without): in the
+// product too (outputs 2.8e-4 from 64-bit arithmetic, 4.1e-4 without): in the
 // product's free columns 4 .. 7 and added by a shuffle where a group has at most
 // 4 heads (FOLD), else by a second product (64 sequences of 32/32 heads, f16,
 // so: 60.9 us folded, 70.5 with the second product).
