@@ -422,7 +422,7 @@ struct Tiles {
   static constexpr size_t kPieces = kRing;                  // Piece[kWarps]
   static constexpr size_t kBars = kPieces + kWarps * sizeof(Piece<D>);
   static constexpr size_t kFlags = kBars + size_t(kWarps) * kStages * 8;  // int[kWarps + 4]
-  // rows 16 bytes apart, so that lanes reading one column of several do not meet in a bank
+  // rows padded by 16 bytes, so that lanes reading one column of several do not meet in a bank
   static constexpr int kQRow = D + 8;
   static constexpr int kQBytes = ROT ? kMaxGroup * kQRow * 2 + int(sizeof(rot::AngleTable<D>)) : 0;
   static constexpr size_t kRows = (kFlags + (kWarps + 4) * 4 + 15) & ~size_t(15);
