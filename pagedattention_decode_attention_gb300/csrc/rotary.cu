@@ -74,7 +74,12 @@ __device__ __forceinline__ void store_item(T* row, int2 at, bool wide, bool join
 }
 
 // A group is 32 / NJ heads of one of a token's q, k and v, one item a lane; a warp
-// takes N groups of one token, all its loads before anything else.
+// takes N groups of one token, all its loads before anything else; its angles,
+// one or two pairs a lane, are computed while they are on their way.  Bound by
+// bytes: 13.2 K tokens rotated (271 MB) 41.3 us, 0.97 of the copy rate; 6.4 K
+// appended (157 MB) 24.7 us, 0.94; 3.3 K of 32 bits (107 MB) 16.9 us, 0.94 (19.6
+// in 16-byte accesses: half of every 32-byte sector at a time).  128 tokens 2.3
+// us: launch and latency.
 template <typename T, int D, bool APPEND, int N>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const Params p) {
   constexpr int NJ = D / 16, kHeads = 32 / NJ;
@@ -180,11 +185,11 @@ cudaError_t launch_rows(Params p, int groups, cudaStream_t stream) {
   };
   // A warp's angles cost as much as two groups' rotation, and what a warp has
   // in flight hides its latency: the more groups it takes the better, as long
-  // as the warps fill the GPU.  (16-bit rows, one group, three, four: 2.4, 2.6,
-  // 2.8 us for 128 tokens of 12 groups; 5.8, 4.1, 4.5 for 1024; 31.2, 25.2,
-  // 25.6 for 6401; 48.1, 38.0, 36.0 for 7200 of 16.)  A group of 32-bit rows is
-  // twice the bytes, and one a warp is enough (17.0 us for 3268 tokens of 8
-  // groups, 17.0 with three, 17.1 with four).
+  // as the warps fill the GPU.  (16-bit rows, one group, three, four: 2.4, 2.5,
+  // 2.8 us for 128 tokens of 12 groups; 5.1, 3.9, 5.6 for 1024; 27.5, 23.2, 25.7
+  // for 6000; 41.7, 36.6, 35.8 for 7200 of 16.)  A group of 32-bit rows is twice
+  // the bytes, and one a warp is enough (17.0 us for 3268 tokens of 8 groups,
+  // 17.0 with three, 17.1 with four).
   const int64_t units = int64_t(p.num_tokens) * groups;
   if constexpr (sizeof(T) == 2) {
     if (units > 100000 && (groups + 3) / 4 < (groups + 2) / 3) return go(std::integral_constant<int, 4>());
