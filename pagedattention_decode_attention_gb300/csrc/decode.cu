@@ -1670,7 +1670,14 @@ __global__ void __launch_bounds__(W * 32)
       const int st = cst;
       if (NT == 1 && j == nblk - 1 && nsplit > 1 && lane == 0)
         seen = dev::ld_relaxed_gpu(&p.ws.arrivals[size_t(b) * Hkv + g]);
-      if (!mbar_wait_bounded(&my_full[st], cph, tmo, p.status)) {
+      if constexpr (ROT != 0) {
+        // (a warp that gives up does as one)
+        if (!__all_sync(0xffffffffu, dev::mbar_try_wait(&my_full[st], cph)) &&
+            !__all_sync(0xffffffffu, mbar_wait_bounded(&my_full[st], cph, tmo, p.status))) {
+          drain();
+          return;
+        }
+      } else if (!mbar_wait_bounded(&my_full[st], cph, tmo, p.status)) {
         drain();
         return;
       }

@@ -132,3 +132,17 @@ def test_python_binding_refuses():
                                                                 0, 0, 0.1, None, q)):
         with pytest.raises(ValueError, match="workspace"):
             call()
+
+
+def test_the_rotating_decode_gives_up_by_whole_warps():
+    """Its lanes hand query columns to one another for every block, so a wait
+    that runs out is voted on (read in the source: the path cannot be staged)."""
+    import os
+    import re
+    with open(os.path.join(build.PKG, "csrc", "decode.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    kernel = text[text.index("decode_kernel(const __grid_constant__"):text.index("decode_f32_kernel")]
+    rows = r"arrived = mbar_wait_bounded\(my_q,[^;]*;\s*if constexpr \(ROT != 0\) arrived = __all_sync\(0xffffffffu, arrived\);"
+    blocks = r"if constexpr \(ROT != 0\) \{\s*if \(!__all_sync\(0xffffffffu, dev::mbar_try_wait\([^;]*&&\s*" \
+             r"!__all_sync\(0xffffffffu, mbar_wait_bounded\("
+    assert len(re.findall(rows, kernel)) == 1 and len(re.findall(blocks, kernel)) == 1
