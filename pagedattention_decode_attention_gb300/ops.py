@@ -1067,20 +1067,20 @@ class Rotary:
         turns = rotary_turns(frequencies)
         _require(turns.numel() == self.rotary_dim // 2, "frequencies must be rotary_dim / 2 numbers")
         self.interleaved, self.magnitude = bool(interleaved), float(magnitude)
-        self._keep(turns, device)
-
-    def _keep(self, turns, device):
         # (a blocking copy: any stream may read it from here on)
-        self._host, self.turns = turns, turns.to(device)
-        self.device = self.turns.device
+        both = torch.stack([turns, -turns]).to(device)
+        self.device = both.device
+        other = object.__new__(Rotary)
+        other.__dict__.update(self.__dict__)
+        self.turns, other.turns = both[0], both[1]
+        self._transposed, other._transposed = other, self
 
     def transposed(self) -> "Rotary":
         """The transposed rotation: what takes the gradients of rotated rows to
-        those of the rows (and undoes a rotation of magnitude 1)."""
-        other = object.__new__(Rotary)
-        other.__dict__.update(self.__dict__)
-        other._keep(-self._host, self.device)
-        return other
+        those of the rows (and undoes a rotation of magnitude 1).  Made with
+        this one, and alive as long as it is: no work, so a call on any stream
+        or under capture may ask for it on the way."""
+        return self._transposed
 
     def _args(self, dev, head_dim):
         """The C arguments, checked against the tensors they are used with."""
