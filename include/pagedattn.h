@@ -701,9 +701,11 @@ PA_API int pa_paged_attention_decode_noalloc(const void* q, const void* k_cache,
  *                     magnitude of 0.1 ln(factor) + 1)
  * pa_rotary_turns (host) turns any frequencies, in radians per position, into
  * what the device calls take: w / 2 pi, less whole turns, times 2^64, as a
- * 64-bit integer.  Its product with a position wraps at a whole turn by
- * itself, so angles are exact to 2^-33 of a turn at any 32-bit position.  The
- * caller copies them to the device once (`turns`, 8-byte aligned).
+ * 64-bit integer, the quotient rounded once.  Its product with a position wraps
+ * at a whole turn by itself, so the angles of a frequency as given are exact to
+ * 2^-33 of a turn at any 32-bit position (a kernel then takes what is left of the
+ * nearest quarter turn in 32 bits).  The caller copies them to the device once
+ * (`turns`, 8-byte aligned).
  *
  * Positions are any int32, negative ones too.  The transposed rotation, which
  * takes the gradients of rotated rows to those of the rows, is the same call
