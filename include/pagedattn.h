@@ -788,11 +788,11 @@ PA_API int pa_rotary_kv_append_q8(const void* q, const void* k, const void* v,
  * positions may be NULL: context_lens[b] - 1.  The caches end up as
  * pa_rotary_kv_append leaves them, bit for bit.  The rotated query is not
  * rounded to q's type before its product (its first 22 bits are used for f16,
- * 16 for bf16), so the output is nearer to exact arithmetic than that call
- * followed by pa_paged_attention_decode_run; a query whose rotated values pass
- * its type's range gives infinite scores.  PA_F32 runs as two launches, which keep
- * the rotated queries in out.  out overlaps no input.  Everything else as for
- * pa_paged_attention_decode_append_run.
+ * down to 2^-36; 16 for bf16), so the output is nearer to exact arithmetic than
+ * that call followed by pa_paged_attention_decode_run; a query whose rotated
+ * values pass its type's range gives infinite scores.  PA_F32 runs as two
+ * launches, which keep the rotated queries in out.  out overlaps no input.
+ * Everything else as for pa_paged_attention_decode_append_run.
  * ---------------------------------------------------------------------- */
 PA_API int pa_paged_attention_decode_rotary_append_run(
     const void* q, const void* k_new, const void* v_new, const int32_t* positions,

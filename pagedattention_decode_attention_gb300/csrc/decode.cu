@@ -1020,6 +1020,10 @@ __global__ void __launch_bounds__(W * 32)
   // f16 weights of the rotating kernel are 2^(x - max + 7): without the lift a
   // dominant token leaves the small ones under f16's precision
   constexpr float kLift = ROT != 0 && std::is_same<T, __half>::value ? 7.f : 0.f;
+  // f16 rests are held times 2^11 (the largest, 16, stays within f16): as they
+  // are, they would end at f16's smallest step, 2^-24, and a value under 2^-3
+  // would lose what they are for
+  constexpr float kRestUp = std::is_same<T, __half>::value ? 2048.f : 1.f;
   // The next item is claimed when this many blocks of the current one are
   // still to be issued: its claim takes one pipeline step per block (counter,
   // unit, table entries, query copy), so it is ready when the ring wants it.
@@ -1574,8 +1578,9 @@ __global__ void __launch_bounds__(W * 32)
           w.to_float(y + 8);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float2 z = rot::fma2(make_float2(y[i], y[i + 1]), make_float2(-1.f, -1.f),
-                                       make_float2(x[i], x[i + 1]));
+            float2 z = rot::fma2(make_float2(y[i], y[i + 1]), make_float2(-1.f, -1.f),
+                                 make_float2(x[i], x[i + 1]));
+            if constexpr (kRestUp != 1.f) z = rot::mul2(z, make_float2(kRestUp, kRestUp));
             y[i] = z.x;
             y[i + 1] = z.y;
           }
@@ -1771,7 +1776,7 @@ __global__ void __launch_bounds__(W * 32)
             // (an infinite score has no rest: 0 or a sign's opposite times infinity)
             const float whole = sa[0][e] + sb[0][e];
             const float rest = fold ? __shfl_xor_sync(0xffffffffu, whole, 2) : sc[e] + sd[e];
-            if (fabsf(whole) < INFINITY) sb[0][e] += rest;
+            if (fabsf(whole) < INFINITY) sb[0][e] = fmaf(rest, 1.f / kRestUp, sb[0][e]);
           }
         }
         // a member's own block counts for that member's rows only
