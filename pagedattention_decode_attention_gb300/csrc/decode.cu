@@ -2180,7 +2180,8 @@ __global__ void __launch_bounds__(128) decode_f32_kernel(const Params p) {
     qr[e] = qv[e];
     acc[e] = 0.f;
   }
-  float m = -INFINITY, l = 0.f;
+  // (finite, so that scores of -inf have no weight from the start)
+  float m = -FLT_MAX, l = 0.f;
   for (int t = 0; t < ctx; ++t) {
     int phys = table[t / kBlockSize];
     if (phys < 0 || phys >= p.num_blocks) {
