@@ -1118,6 +1118,11 @@ def _ptr(t):
     return C.c_void_p(None if t is None else t.data_ptr())
 
 
+def _given(name: str, out, source=True) -> None:
+    """A prepared call's output: one made here would be out of the caller's reach."""
+    _require(out is not None or source is None, f"{name} must be given to a prepared call")
+
+
 def _rotary_args(q, k, positions, rot, q_out, k_out, stream):
     _require(q is not None or k is not None, "need q or k")
     ref = q if q is not None else k
@@ -1173,6 +1178,8 @@ def rotary(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tens
 
 
 def prepare_rotary(q, k, positions, rot: Rotary, q_out, k_out, stream=None) -> Prepared:
+    _given("q_out", q_out, q)
+    _given("k_out", k_out, k)
     dev, args, _, keep = _rotary_args(q, k, positions, rot, q_out, k_out, stream)
     return Prepared(capi.lib().pa_rotary, args, keep, dev)
 
@@ -1238,6 +1245,7 @@ def rotary_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
 
 def prepare_rotary_kv_append(q, k, v, positions, rot: Rotary, k_cache, v_cache, slot_mapping,
                              q_out, stream=None) -> Prepared:
+    _given("q_out", q_out, q)
     dev, args, _, keep = _rotary_append_args(q, k, v, positions, rot, k_cache, v_cache,
                                              slot_mapping, q_out, stream)
     return Prepared(capi.lib().pa_rotary_kv_append, args, keep, dev)
@@ -1291,6 +1299,7 @@ def rotary_kv_append_q8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor
 def prepare_rotary_kv_append_q8(q, k, v, positions, rot: Rotary, k_cache, v_cache, k_scale,
                                 v_scale, block_tables, context_lens, query_start, q_out,
                                 stream=None) -> Prepared:
+    _given("q_out", q_out, q)
     dev, args, _, keep = _rotary_append_q8_args(q, k, v, positions, rot, k_cache, v_cache, k_scale,
                                                 v_scale, block_tables, context_lens, query_start,
                                                 q_out, stream)
@@ -1364,6 +1373,7 @@ def paged_attention_decode_rotary_append_run(q, k_new, v_new, positions, rot: Ro
 def prepare_decode_rotary_append_run(q, k_new, v_new, positions, rot: Rotary, slot_mapping,
                                      k_cache, v_cache, block_tables, context_lens, scale,
                                      workspace, out, stream=None) -> Prepared:
+    _given("out", out)
     dev, args, _, keep = _decode_rotary_args(q, k_new, v_new, positions, rot, slot_mapping, None,
                                              k_cache, v_cache, block_tables, context_lens, 0, 0,
                                              scale, workspace, out, stream)
@@ -1391,6 +1401,7 @@ def prepare_decode_q8_rotary_append_run(q, k_new, v_new, positions, rot: Rotary,
                                         k_scale, v_scale, block_tables, context_lens, window: int,
                                         num_sinks: int, scale: float, workspace, out,
                                         stream=None) -> Prepared:
+    _given("out", out)
     dev, args, _, keep = _decode_rotary_args(q, k_new, v_new, positions, rot, None,
                                              (k_scale, v_scale), k_cache, v_cache, block_tables,
                                              context_lens, window, num_sinks, scale, workspace,
