@@ -402,11 +402,12 @@ __device__ __forceinline__ void store_unit(const RotaryAppendParams& p, const Un
 }
 
 // Units as append_kernel's; a warp takes every (8 gridDim.y)-th head of Q, K and V
-// of its unit.  Bound by bytes and, nearly, by instructions (2.2 a cycle and SM;
+// of its unit.  Bound by bytes and, nearly, by instructions (1.8 a cycle and SM;
 // the angles are shared by a CTA, products go two to an instruction): 10.6 K
-// tokens of 32/8 heads, 238 MB, 38.8 us, 0.91 of the copy rate; 9.9 K of 32/32
-// heads of 64, 203 MB, 41.2 us, 0.73 (half of its rows are quantised).  Three
-// CTAs an SM: two 48.5 us, four 53.6 (they spill).
+// tokens of 32/8 heads, 238 MB, 38.8 us, 0.91 of the copy rate; 10.6 K of 32/32
+// heads of 64, 217 MB, 42.8 us, 0.75 (two thirds of its rows are quantised); 6 K
+// fp32 rows of 32/8 heads, 259 MB, 42.7 us, 0.90.  Three CTAs an SM (head_dim 128;
+// they spill 20 bytes a thread): two 48.5 us, four 53.6 (212 - 264 bytes).
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : D == 64 ? 4 : 3)
     rotary_append_kernel(const RotaryAppendParams p) {
@@ -472,13 +473,14 @@ __global__ void __launch_bounds__(kAppendWarps * 32, sizeof(T) == 4 ? 2 : D == 6
   }
 }
 
-// The same where sequences have a token or two (a decode step): a unit is (token,
-// block the call writes to), unit query_start[b] + i the i-th block of sequence
-// b; a CTA takes a unit, a warp 32 / NJ heads of Q, K or V and its rows in turn,
-// an item a lane.  A chain of latencies: the sequence, its row, table entry and
-// position, the block's scale.  128 tokens of 48 heads: 2.6 us, 4.7 by blocks of
-// 16 rows.  (With the registers of two CTAs an SM 3.3, though 512 tokens then
-// take 6.6 and not 8.8.)
+// The same where sequences have a token or two on average (a decode step): a unit
+// is (token, block the call writes to), unit query_start[b] + i the i-th block of
+// sequence b; a CTA takes a unit, a warp 32 / NJ heads of Q, K or V and its rows in
+// turn, an item a lane.  A chunk among single tokens pays for those turns: 255
+// tokens and a chunk of 256 17.5 us in one call, 9.5 us in two.  A chain of
+// latencies: the sequence, its row, table entry and position, the block's scale.
+// 128 tokens of 48 heads: 2.6 us, 4.7 by blocks of 16 rows.  (With the registers of
+// two CTAs an SM 3.3, though 512 tokens then take 6.6 and not 8.8.)
 constexpr int kFewWarps = 16;
 
 template <typename T, int D>

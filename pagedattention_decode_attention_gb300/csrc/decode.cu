@@ -998,10 +998,11 @@ constexpr int kRotFolded = 1, kRotTwice = 2;
 // computes two cosines an item and holds the frequencies; the rotated query is
 // not rounded to T: what the rounding leaves over (its rest) enters the product
 // too (24 sequences, bf16: 0.0019 from 64-bit arithmetic, 0.0031 without, one
-// rounding of the exact output 0.0017).  A product
-// has 8 query columns: with at most 4 heads in a group the rests take the other
-// 4 and are added by a shuffle (kRotFolded), else they take a second product
-// (kRotTwice; the 7B-shaped batch: 77.9 us so).
+// rounding of the exact output 0.0017).  The weights' rounding to T has no
+// second part here: with the query's rest in, it is all that 0.0019 has over
+// 0.0017.  A product has 8 query columns: with at most 4 heads in a group the
+// rests take the other 4 and are added by a shuffle (kRotFolded), else they take a
+// second product (kRotTwice; the 7B-shaped batch: 77.9 us so, 76.8 folded).
 template <typename T, int D, int W, int NT, int ROT>
 __global__ void __launch_bounds__(W * 32)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k,

@@ -125,7 +125,7 @@ struct Params {
   const void* k_new;
   const void* v_new;
   const int64_t* slot_mapping;
-  // Rotation (decode_kernel<..., true>): q's rows and k_new's are rotated for
+  // Rotation (decode_kernel's ROT not 0): q's rows and k_new's are rotated for
   // positions[b] (null: context_lens[b] - 1), and rows of q, k_new and v_new
   // are these many elements apart.
   rot::Args rot;

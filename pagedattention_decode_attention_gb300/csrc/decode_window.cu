@@ -793,7 +793,8 @@ __device__ __forceinline__ q8::Row8<float> rotate_row(const Params& p, const q8:
 //
 // What it costs (one launch of many): the first batch above 87.1 us, 84.5 with
 // its rows rotated already; the third 54.0 and 41.8, 2048 segments and as many
-// new tokens, each some 400 instructions more that a warp goes through alone.
+// new tokens, each some 400 instructions more that a warp goes through alone: that
+// batch is faster as two launches, rotary first (45.2; bf16 52.1 and 49.2).
 template <typename T, bool Q8, int D, bool APPEND, bool ROT, bool FOLD>
 __global__ void __launch_bounds__(Tiles<T, Q8, D, ROT>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmap_k,

@@ -35,9 +35,9 @@ struct Args {
 // Cosine and sine of the angle position * freq, times m.
 //
 // The nearest quarter turn comes off in integers; what is left, at most an
-// eighth of a turn, is rounded once to 32 bits, and the Taylor series of both
-// end below half a step there: a^11 / 11! and a^12 / 12! for a <= pi / 4 are 2e-9
-// a and 2e-10.
+// eighth of a turn, goes to 32 bits in three roundings (the integer, 2 pi's
+// constant, their product), and the Taylor series of both end below half a step
+// there: a^11 / 11! and a^12 / 12! for a <= pi / 4 are 2e-9 a and 2e-10.
 __device__ __forceinline__ float2 cos_sin(int position, int64_t freq, float m) {
   const uint64_t turn = uint64_t(int64_t(position)) * uint64_t(freq);
   const uint32_t quarter = uint32_t((turn + (uint64_t(1) << 61)) >> 62);  // 0 .. 3

@@ -1019,7 +1019,10 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
     """Angles per position (radians, float64 ``[rotary_dim / 2]`` on the host) of
     rotary positions: ``base ** (-2 i / rotary_dim)``, scaled for long contexts
     by ``"linear"``, ``"base"`` or ``"bands"`` (``low`` and ``high`` count a
-    pair's turns over ``original_context`` tokens; see ``pagedattn.h``)."""
+    pair's turns over ``original_context`` tokens; see ``pagedattn.h``).  A model
+    whose bands were blended over the pairs' numbers, as some YaRN programs do,
+    was trained with other frequencies: pass those to :class:`Rotary`'s
+    ``frequencies``."""
     _require(scaling in _SCALINGS, "scaling must be None, 'linear', 'base' or 'bands'")
     out = torch.empty(max(int(rotary_dim) // 2, 0), dtype=torch.float64)
     capi.check(capi.lib().pa_rotary_frequencies(
